@@ -1,0 +1,441 @@
+"""Binding of the operators around the 4-bit GEMMs (include/ufp4_block.h): RMS
+norm with the residual's addition and an optional E4M3 output, the MoE router
+with its balance loss, dispatch to and combination from expert order, and the
+global gradient norm with clipping.
+
+As in ufp4.py: torch provides device memory (outputs are allocated here unless
+given) and the current stream, every step runs in libufp4's HIP kernels, and
+there is no fallback.  Tensors of a wrong type raise TypeError, of a wrong
+shape, stride or device ValueError; what the library itself refuses raises
+UFP4Error.  Nothing here waits for the GPU or copies to the host.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Sequence, Tuple
+
+import torch
+
+from . import ufp4 as U
+
+# Every symbol include/ufp4_block.h declares.
+EXPORTS = ("ufp4_rmsnorm", "ufp4_rmsnorm_bwd", "ufp4_rmsnorm_bwd_workspace_size",
+           "ufp4_moe_route", "ufp4_moe_route_bwd", "ufp4_moe_route_workspace_size",
+           "ufp4_moe_dispatch", "ufp4_moe_dispatch_bwd", "ufp4_moe_combine",
+           "ufp4_moe_combine_bwd", "ufp4_grad_norm", "ufp4_grad_clip",
+           "ufp4_grad_norm_workspace_size")
+MAX_EXPERTS, MAX_CHOICES = 1024, 16
+E4M3 = torch.float8_e4m3fn
+_CODE = U._OUT_CODE                               # element types: float32, bfloat16
+
+
+class RoutingDesc(ctypes.Structure):
+    """Mirror of ufp4_routing."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("experts", "gates", "slots", "lse", "counts",
+                                               "offsets", "n_tokens", "losses")]
+
+
+class GradDesc(ctypes.Structure):
+    """Mirror of ufp4_grad."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+_lib = None
+
+
+def lib() -> ctypes.CDLL:
+    """libufp4.so with the block operators' C signatures declared."""
+    global _lib
+    if _lib is not None and _lib is U._lib:
+        return _lib
+    L = U.lib()
+    P, I64, I32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    R, G = ctypes.POINTER(RoutingDesc), ctypes.c_void_p
+    L.ufp4_rmsnorm.argtypes = [P, I64, P, I64, P, I32, I32, I64, I64, ctypes.c_float, P, P, P, P,
+                               P, P]
+    L.ufp4_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, P, I64, I32, I32, I64, I64, P, P, P, S, P]
+    L.ufp4_rmsnorm_bwd_workspace_size.argtypes = [I64, I64]
+    L.ufp4_moe_route.argtypes = [P, I64, I32, P, I64, I32, I32, I32, R, P, S, P]
+    L.ufp4_moe_route_bwd.argtypes = [P, I64, I32, I64, I32, I32, I32, R, P, P, P, P]
+    L.ufp4_moe_route_workspace_size.argtypes = [I64, I32]
+    L.ufp4_moe_dispatch.argtypes = [P, I64, P, I32, I64, I32, I64, P, P]
+    L.ufp4_moe_dispatch_bwd.argtypes = [P, P, I32, I64, I32, I64, P, P]
+    L.ufp4_moe_combine.argtypes = [P, P, P, P, I64, I32, I64, I32, I64, P, P]
+    L.ufp4_moe_combine_bwd.argtypes = [P, I64, P, P, P, I32, I64, I32, I64, P, P, P]
+    L.ufp4_grad_norm.argtypes = [G, I64, P, S, P, P]
+    L.ufp4_grad_clip.argtypes = [G, I64, P, ctypes.c_double, ctypes.c_double, P]
+    L.ufp4_grad_norm_workspace_size.argtypes = []
+    for f in EXPORTS:
+        getattr(L, f).restype = S if f.endswith("_size") else I32
+    _lib = L
+    return L
+
+
+# ---------------------------------------------------------------------------
+# Checks
+# ---------------------------------------------------------------------------
+def _rows2d(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
+    """The row stride of a 2-D tensor with unit column stride, of `like`'s
+    shape, type and device when given."""
+    if t.dtype not in _CODE:
+        raise TypeError(f"{name} is float32 or bfloat16, got {t.dtype}")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} has type {t.dtype}, expected {like.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    elif not t.is_cuda:
+        raise ValueError(f"{name} is not on a GPU")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} is 2-D with at least one column, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} needs unit column stride, got strides {t.stride()}")
+    # a single row's stride is not used (and may be anything)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _exact(t: torch.Tensor, name: str, dtype, shape, device) -> torch.Tensor:
+    """t, contiguous and of that type, shape and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t
+
+
+def _weight(w: torch.Tensor, x: torch.Tensor) -> int:
+    if w.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"weight is {x.dtype} or float32, got {w.dtype}")
+    _exact(w, "weight", w.dtype, (x.shape[1],), x.device)
+    return _CODE[w.dtype]
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+# ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+class NormOut(NamedTuple):
+    """y (None unless asked for), h = x + residual (x itself without one), rstd
+    FP32 [rows], and with q8 the E4M3 rows q and their FP32 scales
+    (y ~ q * scale[:, None]), else None."""
+    y: Optional[torch.Tensor]
+    h: torch.Tensor
+    rstd: torch.Tensor
+    q: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+
+
+def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, y: bool = True, q8: bool = False,
+                 out_h: Optional[torch.Tensor] = None) -> NormOut:
+    """RMS norm of x (+ residual), 2-D bf16 or float32 with any row stride; the
+    weight is of x's type or float32.  `y` and `q8` choose the outputs: the
+    input's type, and E4M3 with one scale per row (max |y| / 448).  `out_h`
+    receives the sum and may be x or residual itself (in place)."""
+    ld = _rows2d(x, "x")
+    wd = _weight(weight, x)
+    rows, cols = x.shape
+    dev = x.device
+    ldr, h = 0, x
+    if residual is not None:
+        ldr = _rows2d(residual, "residual", x)
+        h = torch.empty((rows, cols), dtype=x.dtype, device=dev) if out_h is None else \
+            _exact(out_h, "out_h", x.dtype, (rows, cols), dev)
+    elif out_h is not None:
+        raise ValueError("out_h is given without a residual")
+    out = torch.empty((rows, cols), dtype=x.dtype, device=dev) if y else None
+    rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    q = scale = None
+    if q8:
+        q = torch.empty((rows, cols), dtype=E4M3, device=dev)
+        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    st = lib().ufp4_rmsnorm(_p(x), ld, _p(residual), ldr, _p(weight), _CODE[x.dtype], wd, rows,
+                            cols, eps, _p(h) if residual is not None else None, _p(out), _p(q),
+                            _p(scale), _p(rstd), U._stream(dev))
+    U._check(st, "ufp4_rmsnorm")
+    return NormOut(out, h, rstd, q, scale)
+
+
+def ufp4_rmsnorm_bwd_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols))
+
+
+def ufp4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dh: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dw) of ufp4_rmsnorm from dy, the gradient of y, and dh, what
+    reaches h from elsewhere (None: nothing).  dx is the gradient of x and of
+    the residual; dw has the weight's type."""
+    ldh = _rows2d(h, "h")
+    ldy = _rows2d(dy, "dy", h)
+    ldd = _rows2d(dh, "dh", h) if dh is not None else 0
+    wd = _weight(weight, h)
+    rows, cols = h.shape
+    dev = h.device
+    _exact(rstd, "rstd", torch.float32, (rows,), dev)
+    dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+    dw = torch.empty((cols,), dtype=weight.dtype, device=dev)
+    ws, nbytes = _workspace(workspace, lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols), dev)
+    st = lib().ufp4_rmsnorm_bwd(_p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
+                                _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes,
+                                U._stream(dev))
+    U._check(st, "ufp4_rmsnorm_bwd")
+    return dx, dw
+
+
+def _workspace(given: Optional[torch.Tensor], nbytes: int, device):
+    if given is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device), nbytes
+    if given.device != device or not given.is_contiguous():
+        raise ValueError(f"the workspace is contiguous and on {device}")
+    return given, given.numel() * given.element_size()
+
+
+# ---------------------------------------------------------------------------
+# Router
+# ---------------------------------------------------------------------------
+class Routing(NamedTuple):
+    """What the router decides (see ufp4_routing in include/ufp4_block.h).
+    `offsets` is what UFP4ExpertLinear and the grouped GEMMs take over
+    tokens * k rows, `slots` what dispatch and combine take."""
+    experts: torch.Tensor      # int32 [tokens, k], -1 where there is no choice
+    gates: torch.Tensor        # float32 [tokens, k]
+    slots: torch.Tensor        # int32 [tokens, k], ~row where there is no choice
+    lse: torch.Tensor          # float32 [tokens]
+    counts: torch.Tensor       # int64 [experts]
+    offsets: torch.Tensor      # int64 [experts + 1]
+    n_tokens: torch.Tensor     # int64 [1]
+    losses: torch.Tensor       # float32 [2]: balance, z
+    renorm: bool
+
+    def desc(self) -> RoutingDesc:
+        return RoutingDesc(*(t.data_ptr() for t in self[:8]))
+
+
+def ufp4_moe_route_workspace_size(tokens: int, n_experts: int) -> int:
+    return int(lib().ufp4_moe_route_workspace_size(tokens, n_experts))
+
+
+def ufp4_moe_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None,
+                   renorm: bool = True, workspace: Optional[torch.Tensor] = None) -> Routing:
+    """Route each token to the k experts of its largest logits (2-D, float32 or
+    bf16).  `valid` (bool [tokens]) leaves padding tokens out; `renorm` makes a
+    token's gates sum to one, else they are the softmax probabilities."""
+    ld = _rows2d(logits, "logits")
+    t, e = logits.shape
+    dev = logits.device
+    if valid is not None:
+        _exact(valid, "valid", torch.bool, (t,), dev)
+    if not 1 <= k <= min(e, MAX_CHOICES):
+        raise ValueError(f"k = {k}: 1 to {MAX_CHOICES} choices of at most {e} experts")
+    i32, f32, i64 = torch.int32, torch.float32, torch.int64
+    r = Routing(torch.empty((t, k), dtype=i32, device=dev),
+                torch.empty((t, k), dtype=f32, device=dev),
+                torch.empty((t, k), dtype=i32, device=dev),
+                torch.empty((t,), dtype=f32, device=dev),
+                torch.empty((e,), dtype=i64, device=dev),
+                torch.empty((e + 1,), dtype=i64, device=dev),
+                torch.empty((1,), dtype=i64, device=dev),
+                torch.empty((2,), dtype=f32, device=dev), bool(renorm))
+    ws, nbytes = _workspace(workspace, lib().ufp4_moe_route_workspace_size(t, e), dev)
+    d = r.desc()
+    st = lib().ufp4_moe_route(_p(logits), ld, _CODE[logits.dtype], _p(valid), t, e, k, int(renorm),
+                              ctypes.byref(d), _p(ws), nbytes, U._stream(dev))
+    U._check(st, "ufp4_moe_route")
+    return r
+
+
+def ufp4_moe_route_bwd(logits: torch.Tensor, r: Routing, d_gates: Optional[torch.Tensor] = None,
+                       d_losses: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of the logits given to ufp4_moe_route, from that of the
+    gates (float32 [tokens, k]) and of the losses (float32 [2], on the GPU)."""
+    ld = _rows2d(logits, "logits")
+    t, e = logits.shape
+    dev = logits.device
+    k = r.experts.shape[1]
+    _exact(r.experts, "experts", torch.int32, (t, k), dev)
+    _exact(r.gates, "gates", torch.float32, (t, k), dev)
+    _exact(r.lse, "lse", torch.float32, (t,), dev)
+    _exact(r.counts, "counts", torch.int64, (e,), dev)
+    _exact(r.n_tokens, "n_tokens", torch.int64, (1,), dev)
+    if d_gates is not None:
+        _exact(d_gates, "d_gates", torch.float32, (t, k), dev)
+    if d_losses is not None:
+        _exact(d_losses, "d_losses", torch.float32, (2,), dev)
+    out = torch.empty((t, e), dtype=logits.dtype, device=dev)
+    d = r.desc()
+    st = lib().ufp4_moe_route_bwd(_p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
+                                  ctypes.byref(d), _p(d_gates), _p(d_losses), _p(out),
+                                  U._stream(dev))
+    U._check(st, "ufp4_moe_route_bwd")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Dispatch and combine
+# ---------------------------------------------------------------------------
+def _slots(slots: torch.Tensor, tokens: Optional[int], device) -> Tuple[int, int]:
+    if slots.dim() != 2:
+        raise ValueError(f"slots is [tokens, k], got {tuple(slots.shape)}")
+    t, k = slots.shape
+    _exact(slots, "slots", torch.int32, (t if tokens is None else tokens, k), device)
+    if not 1 <= k <= MAX_CHOICES:
+        raise ValueError(f"k = {k}: 1 to {MAX_CHOICES} choices")
+    return t, k
+
+
+def _expert_rows(xs: torch.Tensor, name: str, slots: torch.Tensor) -> Tuple[int, int, int]:
+    """(tokens, k, columns) of a dense [tokens * k, columns] tensor."""
+    _rows2d(xs, name)
+    t, k = _slots(slots, None, xs.device)
+    _exact(xs, name, xs.dtype, (t * k, xs.shape[1]), xs.device)
+    return t, k, xs.shape[1]
+
+
+def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
+    """x [tokens, cols] to expert order, [tokens * k, cols]; rows without a
+    choice are zero."""
+    ld = _rows2d(x, "x")
+    t, k = _slots(slots, x.shape[0], x.device)
+    cols = x.shape[1]
+    xs = torch.empty((t * k, cols), dtype=x.dtype, device=x.device)
+    st = lib().ufp4_moe_dispatch(_p(x), ld, _p(slots), _CODE[x.dtype], t, k, cols, _p(xs),
+                                 U._stream(x.device))
+    U._check(st, "ufp4_moe_dispatch")
+    return xs
+
+
+def ufp4_moe_dispatch_bwd(dxs: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
+    """The gradient of dispatch's input: each token's sum over its choices."""
+    t, k, cols = _expert_rows(dxs, "dxs", slots)
+    dx = torch.empty((t, cols), dtype=dxs.dtype, device=dxs.device)
+    st = lib().ufp4_moe_dispatch_bwd(_p(dxs), _p(slots), _CODE[dxs.dtype], t, k, cols, _p(dx),
+                                     U._stream(dxs.device))
+    U._check(st, "ufp4_moe_dispatch_bwd")
+    return dx
+
+
+def ufp4_moe_combine(ys: torch.Tensor, slots: torch.Tensor, gates: torch.Tensor,
+                     residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + the gate-weighted sum of each token's rows of ys."""
+    t, k, cols = _expert_rows(ys, "ys", slots)
+    _exact(gates, "gates", torch.float32, (t, k), ys.device)
+    ldr = 0
+    if residual is not None:
+        ldr = _rows2d(residual, "residual")
+        if residual.shape != (t, cols) or residual.device != ys.device:
+            raise ValueError(f"residual is [{t}, {cols}] on {ys.device}, got "
+                             f"{tuple(residual.shape)} on {residual.device}")
+        if residual.dtype != ys.dtype:
+            raise TypeError(f"residual has type {residual.dtype}, expected {ys.dtype}")
+    y = torch.empty((t, cols), dtype=ys.dtype, device=ys.device)
+    st = lib().ufp4_moe_combine(_p(ys), _p(slots), _p(gates), _p(residual), ldr, _CODE[ys.dtype],
+                                t, k, cols, _p(y), U._stream(ys.device))
+    U._check(st, "ufp4_moe_combine")
+    return y
+
+
+def ufp4_moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor,
+                         gates: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dys, d_gates) of ufp4_moe_combine; dy itself is the residual's
+    gradient."""
+    t, k, cols = _expert_rows(ys, "ys", slots)
+    ldy = _rows2d(dy, "dy")
+    if dy.shape != (t, cols) or dy.device != ys.device:
+        raise ValueError(f"dy is [{t}, {cols}] on {ys.device}, got {tuple(dy.shape)} on "
+                         f"{dy.device}")
+    if dy.dtype != ys.dtype:
+        raise TypeError(f"dy has type {dy.dtype}, expected {ys.dtype}")
+    _exact(gates, "gates", torch.float32, (t, k), ys.device)
+    dys = torch.empty_like(ys)
+    dg = torch.empty((t, k), dtype=torch.float32, device=ys.device)
+    st = lib().ufp4_moe_combine_bwd(_p(dy), ldy, _p(ys), _p(slots), _p(gates), _CODE[ys.dtype], t,
+                                    k, cols, _p(dys), _p(dg), U._stream(ys.device))
+    U._check(st, "ufp4_moe_combine_bwd")
+    return dys, dg
+
+
+# ---------------------------------------------------------------------------
+# Gradient norm and clipping
+# ---------------------------------------------------------------------------
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one stretch of memory, in any order."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _grad_list(tensors, out):
+    """(descriptors, count, device) of a list of dense tensors."""
+    n = len(tensors)
+    if out is not None and len(out) != n:
+        raise ValueError(f"{len(out)} outputs for {n} tensors")
+    d = (GradDesc * max(1, n))()
+    dev = None
+    for i, t in enumerate(tensors):
+        code = _CODE.get(t.dtype)
+        if code is None:
+            raise TypeError(f"tensor {i} is float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            raise ValueError(f"tensor {i} is on {t.device}: all are on one GPU")
+        dev = t.device
+        if not _dense(t):
+            raise ValueError(f"tensor {i} is not dense: strides {t.stride()} of {tuple(t.shape)}")
+        o, ocode = t, code
+        if out is not None:
+            o = out[i]
+            ocode = _CODE.get(o.dtype)
+            if ocode is None:
+                raise TypeError(f"output {i} is float32 or bfloat16, got {o.dtype}")
+            if o.shape != t.shape or o.device != dev or \
+                    (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous())):
+                raise ValueError(f"output {i} differs from its tensor in shape, strides or device")
+        d[i] = GradDesc(t.data_ptr(), o.data_ptr(), t.numel(), code, ocode)
+    return d, n, dev
+
+
+def _norm_of(d, n, dev, workspace):
+    if dev is None:
+        raise ValueError("no tensors")
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(workspace, lib().ufp4_grad_norm_workspace_size(), dev)
+    st = lib().ufp4_grad_norm(ctypes.addressof(d), n, _p(ws), nbytes, _p(norm), U._stream(dev))
+    U._check(st, "ufp4_grad_norm")
+    return norm
+
+
+def ufp4_grad_norm(tensors: Sequence[torch.Tensor],
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The 2-norm over all elements of all tensors (bf16 or float32, dense), a
+    float32 scalar on the GPU."""
+    d, n, dev = _grad_list(tensors, None)
+    return _norm_of(d, n, dev, workspace)
+
+
+def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
+                    out: Optional[Sequence[torch.Tensor]] = None, eps: float = 1e-6,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scale all tensors by min(1, max_norm / (norm + eps)), in place or into
+    `out` (same shapes; bf16 or float32), and return the norm before it.  The
+    coefficient stays on the GPU: nothing waits."""
+    d, n, dev = _grad_list(tensors, out)
+    norm = _norm_of(d, n, dev, workspace)
+    st = lib().ufp4_grad_clip(ctypes.addressof(d), n, _p(norm), max_norm, eps, U._stream(dev))
+    U._check(st, "ufp4_grad_clip")
+    return norm

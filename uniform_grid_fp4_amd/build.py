@@ -8,12 +8,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libufp4.so")
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "stats.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "stats.hip",
+           "block_api.hip", "rmsnorm.hip", "route.hip", "exchange.hip", "gradnorm.hip"]
 # The bench's MFMA issue-rate probe: a separate library, not part of the ABI.
 PROBE_LIB = os.path.join(HERE, "libufp4_probe.so")
 PROBE_SOURCES = ["probe.hip"]
@@ -24,7 +27,7 @@ PROBE_SOURCES = ["probe.hip"]
 #   butterfly outputs can be subnormal).
 # -packed-fp32-ops disabled: no v_pk_* FP32 instructions are generated.
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -38,10 +41,7 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP toolchain is required to build libufp4.so")
 
 
-def _compile(sources, out, verbose):
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, *srcs, "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -51,7 +51,19 @@ def _compile(sources, out, verbose):
              if "packed-fp32-ops" not in ln and ln.strip()]
     if noise and verbose:
         print("\n".join(noise), file=sys.stderr)
-    os.replace(tmp, out)
+
+
+def _compile(sources, out, verbose):
+    """Each source to an object (a few at a time), then one shared library."""
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, s + ".o") for s in sources]
+        base = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+        with ThreadPoolExecutor(max_workers=min(4, len(sources))) as pool:
+            list(pool.map(lambda so: _run([*base, "-c", os.path.join(CSRC, so[0]), "-o", so[1]],
+                                          verbose), zip(sources, objs)))
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", out + ".tmp"],
+             verbose)
+    os.replace(out + ".tmp", out)
 
 
 def build(verbose: bool = False) -> str:

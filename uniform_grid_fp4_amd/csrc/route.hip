@@ -1,0 +1,552 @@
+// MoE router (gfx950): softmax, top-k choices, gates, counts, group offsets,
+// each choice's row in expert order, the balance and z losses, and the
+// backward pass.
+//   lse = log sum exp(l),  p = exp(l - lse)
+//   balance = E sum_e (counts_e / (k N)) (sum_t p_te / N),  z = sum lse^2 / N
+//
+// Sixteen lanes (one DPP row) hold one token's logits, so that the row
+// reductions are four DPP steps and a wave works on four tokens at once.  A
+// workgroup takes kRouteTokens = 64 tokens: the choices of an expert are then
+// one 64-bit mask in LDS, its count a population count, and a choice's place
+// among the workgroup's tokens the population count below its token's bit, all
+// independent of the order in which the lanes ran.  A second kernel scans the
+// counts over the workgroups and sums their probabilities, a third turns
+// places into rows.  Few tokens (one workgroup) take a single launch.
+#include "block_device.h"
+#include "block_kernels.h"
+
+namespace ufp4 {
+
+constexpr int kGroups = 16;                      // tokens in flight per workgroup
+constexpr int kPer = kRouteTokens / kGroups;     // tokens per group of 16 lanes
+
+// Workspace of a call with nblk workgroups, E experts:
+//   uint32 base [nblk][E + 1]  choices per workgroup and expert (last: choices
+//                              that do not exist), then their exclusive sums
+//   float  psum [nblk][E]      sums of p
+//   double z    [nblk], uint32 live [nblk]
+//   uint32 total[E + 2]        choices per expert, missing choices, tokens
+//   double ptotal[E + 1]       sums of p, and of lse^2
+struct RouteWs {
+  uint32_t *base;
+  float *psum;
+  double *z;
+  uint32_t *live;
+  uint32_t *total;
+  double *ptotal;
+};
+__host__ __device__ inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+__host__ __device__ inline size_t route_layout(int64_t nblk, int e, void *p, RouteWs *w) {
+  char *at = static_cast<char *>(p);
+  size_t used = 0;
+  const size_t sizes[6] = {4u * (size_t)nblk * (e + 1), 4u * (size_t)nblk * e, 8u * (size_t)nblk,
+                           4u * (size_t)nblk, 4u * (size_t)(e + 2), 8u * (size_t)(e + 1)};
+  void *parts[6];
+  for (int i = 0; i < 6; ++i) {
+    parts[i] = at + used;
+    used += up16(sizes[i]);
+  }
+  if (w != nullptr) {
+    w->base = static_cast<uint32_t *>(parts[0]);
+    w->psum = static_cast<float *>(parts[1]);
+    w->z = static_cast<double *>(parts[2]);
+    w->live = static_cast<uint32_t *>(parts[3]);
+    w->total = static_cast<uint32_t *>(parts[4]);
+    w->ptotal = static_cast<double *>(parts[5]);
+  }
+  return used;
+}
+static int64_t route_blocks(int64_t tokens) {
+  const int64_t n = (tokens + kRouteTokens - 1) / kRouteTokens;
+  return n < 1 ? 1 : n;
+}
+size_t route_workspace_bytes(int64_t tokens, int n_experts) {
+  return route_layout(route_blocks(tokens), n_experts, nullptr, nullptr);
+}
+
+// A logit as an unsigned number of the same order, equal for -0 and +0; 0 for
+// -inf and NaN, which are never chosen.
+__device__ __forceinline__ uint32_t order_key(float l) {
+  const uint32_t b = __float_as_uint(l + 0.0f);
+  const bool never = !(l > -INFINITY);
+  return never ? 0u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
+}
+
+template <int ROT>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROT, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, row_rotate<8>(v));
+  v = max(v, row_rotate<4>(v));
+  v = max(v, row_rotate<2>(v));
+  return max(v, row_rotate<1>(v));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  v = min(v, row_rotate<8>(v));
+  v = min(v, row_rotate<4>(v));
+  v = min(v, row_rotate<2>(v));
+  return min(v, row_rotate<1>(v));
+}
+
+// Expert held by lane l in register i: sixteen lanes take runs of W
+// consecutive experts (one 16-byte load where the runs are that long).
+template <typename T, int R>
+struct Hold {
+  static constexpr int W = R < Elem<T>::V ? R : Elem<T>::V;
+  __device__ static __forceinline__ int expert(int lane, int i) {
+    return (i / W) * (16 * W) + lane * W + i % W;
+  }
+  // The token's logits; -inf past the last expert.
+  __device__ static __forceinline__ void load(const T *p, int e, int lane, float (&f)[R]) {
+#pragma unroll
+    for (int i = 0; i < R; i += W) {
+      const int at = expert(lane, i);
+      if (W == Elem<T>::V && at + W <= e) {
+        float v[Elem<T>::V];
+        Elem<T>::unpack(*reinterpret_cast<const u32x4_any *>(p + at), v);
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[i + j] = v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[i + j] = at + j < e ? Elem<T>::get(p[at + j]) : -INFINITY;
+      }
+    }
+  }
+};
+
+// Exclusive sums of v over 1024 or fewer entries in LDS by one workgroup of
+// 256 threads; returns the total.  s_tmp: 256 words.
+__device__ uint32_t scan_shared(uint32_t *v, int n, uint32_t *s_tmp) {
+  const int per = (n + 255) / 256, at = threadIdx.x * per;
+  uint32_t mine = 0;
+  for (int i = 0; i < per; ++i) mine += at + i < n ? v[at + i] : 0u;
+  s_tmp[threadIdx.x] = mine;
+  __syncthreads();
+  for (int o = 1; o < 256; o <<= 1) {
+    const uint32_t below = (int)threadIdx.x >= o ? s_tmp[threadIdx.x - o] : 0u;
+    __syncthreads();
+    s_tmp[threadIdx.x] += below;
+    __syncthreads();
+  }
+  uint32_t run = s_tmp[threadIdx.x] - mine;
+  for (int i = 0; i < per; ++i) {
+    if (at + i >= n) break;
+    const uint32_t x = v[at + i];
+    v[at + i] = run;
+    run += x;
+  }
+  const uint32_t total = s_tmp[255];
+  __syncthreads();
+  return total;
+}
+
+__device__ __forceinline__ void write_totals(const RouteArgs &a, double balance, double z,
+                                             uint32_t tokens) {
+  const double n = (double)tokens;
+  *a.n_tokens = (int64_t)tokens;
+  a.offsets[a.n_experts] = a.tokens * a.k;
+  a.losses[0] = tokens ? (float)((double)a.n_experts * balance / ((double)a.k * n * n)) : 0.0f;
+  a.losses[1] = tokens ? (float)(z / n) : 0.0f;
+}
+
+// Choices, gates and, for the workgroup's 64 tokens, places and counts; with
+// ALONE (one workgroup) everything else too.  Dynamic LDS: 28 bytes per expert.
+template <typename T, int R, bool ALONE>
+__global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const RouteWs ws) {
+  extern __shared__ __align__(16) char s_dyn[];
+  __shared__ uint32_t s_scan[256];
+  __shared__ uint32_t s_lost[kRouteTokens], s_live[kRouteTokens];
+  __shared__ float s_lse[kRouteTokens];
+  __shared__ double s_part[4];
+  const int E = a.n_experts, k = a.k;
+  unsigned long long *s_mask = reinterpret_cast<unsigned long long *>(s_dyn);
+  float *s_p = reinterpret_cast<float *>(s_dyn + 8 * E);
+  uint32_t *s_off = reinterpret_cast<uint32_t *>(s_dyn + 24 * E);
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < E; e += 256) s_mask[e] = 0;
+  float psum[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) psum[i] = 0.0f;
+  __syncthreads();
+  int32_t choice[kPer], found[kPer];             // lane j: the token's j-th choice
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int local = n * kGroups + group;
+    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + local;
+    const bool here = t < a.tokens;
+    bool live = here && (a.valid == nullptr || a.valid[t] != 0);
+    float f[R];
+    if (live) {
+      Hold<T, R>::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) f[i] = -INFINITY;
+    }
+    float top = -INFINITY, nan = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      top = fmaxf(top, f[i]);
+      nan = f[i] != f[i] ? f[i] : nan;
+    }
+    top = row_max(top);
+    nan = row_sum(nan);
+    live = live && (top > -INFINITY || nan != nan);
+    // the choices: k rounds of the largest key left, the lowest expert among
+    // equals; lane j keeps round j's
+    uint32_t key[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) key[i] = order_key(f[i]);
+    int32_t mine = -1, count = 0;
+    float picked = -INFINITY;
+    for (int j = 0; j < k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) best = max(best, key[i]);
+      best = row_max(best);
+      uint32_t who = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (key[i] == best) who = min(who, (uint32_t)Hold<T, R>::expert(lane, i));
+      who = row_min(who);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if ((uint32_t)Hold<T, R>::expert(lane, i) == who) key[i] = 0u;
+      if (best != 0u) ++count;
+      if (lane == j && best != 0u) {
+        mine = (int32_t)who;
+        picked = __uint_as_float((best & 0x80000000u) ? best ^ 0x80000000u : ~best);
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      f[i] = live && Hold<T, R>::expert(lane, i) < E ? expf(f[i] - top) : 0.0f;
+      sum += f[i];
+    }
+    sum = row_sum(sum);
+    const float lse = live ? top + logf(sum) : -INFINITY;
+    const float inv = live ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) psum[i] = __builtin_fmaf(f[i], inv, psum[i]);
+    float gate = mine >= 0 ? expf(picked - top) : 0.0f;
+    const float total = row_sum(gate);
+    gate = mine < 0 ? 0.0f : (a.renorm ? gate / total + nan : gate * inv);
+    choice[n] = mine;
+    found[n] = count;
+    if (here && lane < k) {
+      a.experts[t * k + lane] = mine;
+      a.gates[t * k + lane] = gate;
+    }
+    if (mine >= 0) atomicOr(&s_mask[mine], 1ull << local);
+    if (lane == 0) {
+      if (here) a.lse[t] = lse;
+      s_lost[local] = here ? (uint32_t)(k - count) : 0u;
+      s_live[local] = live ? 1u : 0u;
+      s_lse[local] = live ? lse : 0.0f;
+    }
+  }
+  // p sums: the wave's four groups, then the waves through LDS
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    psum[i] += __shfl_xor(psum[i], 16, 64);
+    psum[i] += __shfl_xor(psum[i], 32, 64);
+    const int e = Hold<T, R>::expert(lane, i);
+    if ((threadIdx.x & 48) == 0 && e < E) s_p[wave * E + e] = psum[i];
+  }
+  __syncthreads();
+  // wave 0, lane = token: missing choices before each token, tokens, z
+  uint32_t lost_all = 0, tokens = 0;
+  double z = 0.0;
+  if (threadIdx.x < kRouteTokens) {
+    const uint32_t own = s_lost[threadIdx.x];
+    uint32_t run = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t below = __shfl_up(run, o, 64);
+      if ((int)threadIdx.x >= o) run += below;
+    }
+    lost_all = __shfl(run, 63, 64);
+    s_lost[threadIdx.x] = run - own;
+    tokens = (uint32_t)__popcll(__ballot(s_live[threadIdx.x] != 0));
+    z = lanes_sum((double)s_lse[threadIdx.x] * (double)s_lse[threadIdx.x]);
+  }
+  double balance = 0.0;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    const uint32_t c = (uint32_t)__popcll(s_mask[e]);
+    const float p = ((s_p[e] + s_p[E + e]) + s_p[2 * E + e]) + s_p[3 * E + e];
+    if (ALONE) {
+      s_off[e] = c;
+      a.counts[e] = (int64_t)c;
+      balance += (double)c * (double)p;
+    } else {
+      ws.base[(int64_t)blockIdx.x * (E + 1) + e] = c;
+      ws.psum[(int64_t)blockIdx.x * E + e] = p;
+    }
+  }
+  uint32_t routed = 0;
+  if (ALONE) {
+    balance = lanes_sum(balance);
+    if ((threadIdx.x & 63) == 0) s_part[wave] = balance;
+    __syncthreads();
+    routed = scan_shared(s_off, E, s_scan);
+    for (int e = threadIdx.x; e < E; e += 256) a.offsets[e] = (int64_t)s_off[e];
+    if (threadIdx.x == 0)
+      write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], z, tokens);
+  } else {
+    if (threadIdx.x == 0) {
+      ws.base[(int64_t)blockIdx.x * (E + 1) + E] = lost_all;
+      ws.z[blockIdx.x] = z;
+      ws.live[blockIdx.x] = tokens;
+    }
+    __syncthreads();                             // s_lost
+  }
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int local = n * kGroups + group;
+    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + local;
+    if (t >= a.tokens || lane >= k) continue;
+    const int e = choice[n];
+    uint32_t place;
+    if (e >= 0) {
+      place = (uint32_t)__popcll(s_mask[e] & ((1ull << local) - 1ull));
+      if (ALONE) place += s_off[e];
+    } else {
+      // a token's choices that exist come first
+      place = s_lost[local] + (uint32_t)(lane - found[n]);
+      place = ~(ALONE ? place + routed : place);
+    }
+    a.slots[t * k + lane] = (int32_t)place;
+  }
+}
+
+// Column c of base over the workgroups: exclusive sums in place and the total;
+// psum's columns summed in FP64.  64 runs of workgroups per column, 16 columns
+// per workgroup of 1024 threads; the last workgroup sums z and the tokens.
+__global__ __launch_bounds__(1024) void route_scan_kernel(const RouteArgs a, const RouteWs ws,
+                                                          int nblk) {
+  __shared__ uint32_t s_n[64][16];
+  __shared__ double s_d[64][16];
+  const int E = a.n_experts;
+  const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int per = (nblk + 63) / 64, b0 = min(run * per, nblk), b1 = min(b0 + per, nblk);
+  const bool tail = blockIdx.x == gridDim.x - 1;
+  const int c = blockIdx.x * 16 + col;
+  uint32_t n = 0;
+  double d = 0.0;
+  if (tail) {
+    if (col == 0)
+      for (int b = b0; b < b1; ++b) {
+        n += ws.live[b];
+        d += ws.z[b];
+      }
+  } else if (c <= E) {
+    for (int b = b0; b < b1; ++b) {
+      n += ws.base[(int64_t)b * (E + 1) + c];
+      if (c < E) d += (double)ws.psum[(int64_t)b * E + c];
+    }
+  }
+  s_n[run][col] = n;
+  s_d[run][col] = d;
+  __syncthreads();
+  if (run == 0) {
+    uint32_t total = 0;
+    double sum = 0.0;
+    for (int i = 0; i < 64; ++i) {
+      const uint32_t v = s_n[i][col];
+      s_n[i][col] = total;
+      total += v;
+      sum += s_d[i][col];
+    }
+    if (tail) {
+      if (col == 0) {
+        ws.total[E + 1] = total;
+        ws.ptotal[E] = sum;
+      }
+    } else if (c <= E) {
+      ws.total[c] = total;
+      if (c < E) ws.ptotal[c] = sum;
+    }
+  }
+  __syncthreads();
+  if (tail || c > E) return;
+  uint32_t at = s_n[run][col];
+  for (int b = b0; b < b1; ++b) {
+    uint32_t *p = ws.base + (int64_t)b * (E + 1) + c;
+    const uint32_t v = *p;
+    *p = at;
+    at += v;
+  }
+}
+
+// Places to rows, for the 64 tokens of a workgroup; workgroup 0 writes the
+// counts, offsets and losses.
+__global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, const RouteWs ws) {
+  __shared__ uint32_t s_off[kRouteMaxExperts];
+  __shared__ uint32_t s_scan[256];
+  __shared__ double s_part[4];
+  const int E = a.n_experts, k = a.k;
+  const bool first = blockIdx.x == 0;
+  double balance = 0.0;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    const uint32_t c = ws.total[e];
+    s_off[e] = c;
+    if (first) {
+      a.counts[e] = (int64_t)c;
+      balance += (double)c * ws.ptotal[e];
+    }
+  }
+  __syncthreads();
+  const uint32_t routed = scan_shared(s_off, E, s_scan);
+  if (first) {
+    balance = lanes_sum(balance);
+    if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = balance;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 256) a.offsets[e] = (int64_t)s_off[e];
+    if (threadIdx.x == 0)
+      write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], ws.ptotal[E],
+                   ws.total[E + 1]);
+  }
+  const uint32_t *base = ws.base + (int64_t)blockIdx.x * (E + 1);
+  const int64_t i0 = (int64_t)blockIdx.x * kRouteTokens * k;
+  const int64_t i1 = min(i0 + (int64_t)kRouteTokens * k, a.tokens * k);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
+    const int32_t e = a.experts[i], place = a.slots[i];
+    a.slots[i] = e >= 0 ? (int32_t)(s_off[e] + base[e] + (uint32_t)place)
+                        : (int32_t)~(routed + base[E] + (uint32_t)~place);
+  }
+}
+
+// d l_e = p_e (c_e - sum p c - s) + 2 dz lse p_e / N, plus g_j (dg_j - s') at
+// the chosen, where c_e = dbal E counts_e / (k N^2); with renorm s = 0 and
+// s' = sum g dg, without s = sum g dg and s' = 0.  Dynamic LDS: per group a
+// row of E floats that takes the chosen experts' terms to the lanes that hold
+// them, zero in between.
+template <typename T, int R>
+__global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64_t nblk) {
+  extern __shared__ __align__(16) char s_dyn[];
+  const int E = a.n_experts, k = a.k;
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+  float *s_add = reinterpret_cast<float *>(s_dyn) + group * E;
+  for (int e = lane; e < E; e += 16) s_add[e] = 0.0f;
+  const double n = (double)*a.n_tokens;
+  const double dbal = a.d_losses != nullptr ? (double)a.d_losses[0] : 0.0;
+  const double dz = a.d_losses != nullptr ? (double)a.d_losses[1] : 0.0;
+  const float z_of = n > 0.0 ? (float)(2.0 * dz / n) : 0.0f;
+  const float c_of = n > 0.0 ? (float)(dbal * E / ((double)k * n * n)) : 0.0f;
+  float c[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = Hold<T, R>::expert(lane, i);
+    c[i] = e < E ? c_of * (float)a.counts[e] : 0.0f;
+  }
+  __syncthreads();
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < nblk * kGroups;
+       t += (int64_t)gridDim.x * kGroups) {
+    const bool here = t < a.tokens;
+    const float lse = here ? a.lse[t] : -INFINITY;
+    const bool live = lse != -INFINITY;
+    float f[R];
+    if (live) {
+      Hold<T, R>::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) f[i] = -INFINITY;
+    }
+    int32_t mine = -1;
+    float g = 0.0f, dg = 0.0f;
+    if (live && lane < k) {
+      mine = a.experts[t * k + lane];
+      if (mine >= E) mine = -1;
+      g = a.gates[t * k + lane];
+      dg = mine >= 0 && a.d_gates != nullptr ? a.d_gates[t * k + lane] : 0.0f;
+    }
+    const float s = row_sum(g * dg);
+    if (mine >= 0) s_add[mine] = a.renorm ? g * (dg - s) : g * dg;
+    // p from the row's own maximum and sum: exp(l - lse) would carry lse's
+    // rounding, which for large logits is larger than the logits' distances
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < R; ++i) top = fmaxf(top, f[i]);
+    top = row_max(top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      f[i] = live && Hold<T, R>::expert(lane, i) < E ? expf(f[i] - top) : 0.0f;
+      sum += f[i];
+    }
+    const float inv = live ? 1.0f / row_sum(sum) : 0.0f;
+    float pc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      f[i] *= inv;
+      pc = __builtin_fmaf(f[i], c[i], pc);
+    }
+    pc = row_sum(pc);
+    const float shift = (live ? z_of * lse : 0.0f) - pc - (a.renorm ? 0.0f : s);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int e = Hold<T, R>::expert(lane, i);
+      if (here && e < E)
+        static_cast<T *>(a.d_logits)[t * E + e] =
+            Elem<T>::put(__builtin_fmaf(f[i], c[i] + shift, s_add[e]));
+    }
+    __syncthreads();
+    if (mine >= 0) s_add[mine] = 0.0f;
+    __syncthreads();
+  }
+}
+
+template <typename T, int R>
+static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
+  const int64_t nblk = route_blocks(a.tokens);
+  RouteWs ws;
+  route_layout(nblk, a.n_experts, a.workspace, &ws);
+  const size_t lds = 28u * (size_t)a.n_experts;
+  if (nblk == 1) {
+    hipLaunchKernelGGL((route_kernel<T, R, true>), dim3(1), dim3(256), lds, st, a, ws);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((route_kernel<T, R, false>), dim3((unsigned)nblk), dim3(256), lds, st, a,
+                     ws);
+  hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((a.n_experts + 1 + 15) / 16 + 1)),
+                     dim3(1024), 0, st, a, ws, (int)nblk);
+  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)nblk), dim3(256), 0, st, a, ws);
+  return hipGetLastError();
+}
+
+template <typename T, int R>
+static hipError_t route_back(const RouteArgs &a, hipStream_t st) {
+  if (a.tokens == 0) return hipSuccess;
+  const int64_t nblk = (a.tokens + kGroups - 1) / kGroups;
+  const unsigned grid = (unsigned)(nblk < 4096 ? nblk : 4096);
+  hipLaunchKernelGGL((route_bwd_kernel<T, R>), dim3(grid), dim3(256),
+                     (size_t)kGroups * 4u * (size_t)a.n_experts, st, a, nblk);
+  return hipGetLastError();
+}
+
+// Logits per lane: the smallest power of two that holds the experts.
+template <typename T>
+static hipError_t route_any(const RouteArgs &a, bool back, hipStream_t st) {
+#define UFP4_ROUTE(R) \
+  if (a.n_experts <= 16 * R) return back ? route_back<T, R>(a, st) : route_fwd<T, R>(a, st)
+  UFP4_ROUTE(1);
+  UFP4_ROUTE(2);
+  UFP4_ROUTE(4);
+  UFP4_ROUTE(8);
+  UFP4_ROUTE(16);
+  UFP4_ROUTE(32);
+  UFP4_ROUTE(64);
+#undef UFP4_ROUTE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t st) {
+  return a.bf16 ? route_any<uint16_t>(a, false, st) : route_any<float>(a, false, st);
+}
+hipError_t launch_route_bwd(const RouteArgs &a, hipStream_t st) {
+  return a.bf16 ? route_any<uint16_t>(a, true, st) : route_any<float>(a, true, st);
+}
+
+}  // namespace ufp4
