@@ -97,6 +97,10 @@ __device__ __forceinline__ float row_sum(float v) {
   v += row_rotate<1>(v);
   return v;
 }
+template <int ROT>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROT, 0xF, 0xF, false);
+}
 // fmaxf drops a NaN operand; callers that must keep NaN test for it apart.
 __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, row_rotate<8>(v));
@@ -105,17 +109,22 @@ __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, row_rotate<1>(v));
   return v;
 }
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, row_rotate<8>(v));
+  v = max(v, row_rotate<4>(v));
+  v = max(v, row_rotate<2>(v));
+  return max(v, row_rotate<1>(v));
+}
 __device__ __forceinline__ float lanes_sum(float v) {
   v = row_sum(v);
   v += __shfl_xor(v, 16, 64);
   v += __shfl_xor(v, 32, 64);
   return v;
 }
-__device__ __forceinline__ float lanes_max(float v) {
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   v = row_max(v);
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  v = fmaxf(v, __shfl_xor(v, 32, 64));
-  return v;
+  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  return max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
 }
 __device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
@@ -138,14 +147,14 @@ __device__ __forceinline__ float group_sum(float v, float *s) {
   return t;
 }
 template <int WAVES>
-__device__ __forceinline__ float group_max(float v, float *s) {
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t *s) {
   v = lanes_max(v);
   if (WAVES == 1) return v;
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = s[0];
+  uint32_t t = s[0];
 #pragma unroll
-  for (int i = 1; i < WAVES; ++i) t = fmaxf(t, s[i]);
+  for (int i = 1; i < WAVES; ++i) t = max(t, s[i]);
   return t;
 }
 

@@ -12,11 +12,15 @@ constexpr float kE4M3Max = 448.0f;
 
 // What the row's largest |y| gives: the stored scale and the factors that
 // take y to q.  1 / scale overflows FP32 below 448 / 2^128, so rows below
-// 2^-64 are lifted by 2^64 first (exact).
+// 2^-64 are lifted by 2^64 first (exact).  The maximum is taken over the bits
+// of |y| as unsigned numbers, where infinities and NaN are the largest: either
+// makes the whole row NaN.
 struct RowScale {
   float scale, lift, inv;
 };
-__device__ __forceinline__ RowScale row_scale(float top) {
+__device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
+  const float top = top_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                            : __uint_as_float(top_bits);
   RowScale s;
   s.scale = top / kE4M3Max;
   s.lift = top < 0x1p-64f ? 0x1p64f : 1.0f;
@@ -31,12 +35,169 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
                                                    true);
 }
 
+// Rows held in registers: TPR threads (one wave or a workgroup of four) hold a
+// row as NV vectors each, so x and the residual are read once and everything
+// else happens in registers.  A workgroup walks over rows with the weight kept
+// in registers and the next row's loads in flight.  TAIL: the row length is
+// not a multiple of the vector.
+template <int NV, typename T, bool TAIL>
+struct RowVecs {
+  static constexpr int V = Elem<T>::V;
+  u32x4 v[NV];
+  __device__ __forceinline__ void load(const T *p, int first, int step, int cols) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * step;
+      if (TAIL) {
+        v[i] = c < cols ? load_vec(p + c, cols - c) : u32x4(0);
+      } else {
+        v[i] = c < cols ? *reinterpret_cast<const u32x4_any *>(p + c) : u32x4(0);
+      }
+    }
+  }
+};
+template <typename T, bool TAIL>
+__device__ __forceinline__ void row_store(T *p, int c, int cols, u32x4 v) {
+  if (c >= cols) return;
+  if (TAIL)
+    store_vec(p + c, cols - c, v);
+  else
+    *reinterpret_cast<u32x4_any *>(p + c) = v;
+}
+
+// The weights of one vector's columns: packed as the rows are when the types
+// agree, FP32 otherwise.
+template <typename T, typename W, bool TAIL>
+struct WeightVec {
+  static constexpr int V = Elem<T>::V;
+  float f[V];
+  __device__ __forceinline__ void load(const W *w, int c, int cols) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 0.0f;
+    if (c >= cols) return;
+    constexpr int VW = Elem<W>::V;
+#pragma unroll
+    for (int i = 0; i < V; i += VW) {
+      float g[VW];
+      Elem<W>::unpack(TAIL ? load_vec(w + c + i, cols - c - i)
+                           : (u32x4)*reinterpret_cast<const u32x4_any *>(w + c + i), g);
+#pragma unroll
+      for (int j = 0; j < VW; ++j) f[i + j] = g[j];
+    }
+  }
+  __device__ __forceinline__ void get(float (&g)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = f[i];
+  }
+};
+template <bool TAIL>
+struct WeightVec<uint16_t, uint16_t, TAIL> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint16_t *w, int c, int cols) {
+    if (TAIL)
+      v = c < cols ? load_vec(w + c, cols - c) : u32x4(0);
+    else
+      v = c < cols ? *reinterpret_cast<const u32x4_any *>(w + c) : u32x4(0);
+  }
+  __device__ __forceinline__ void get(float (&g)[8]) const { Elem<uint16_t>::unpack(v, g); }
+};
+
+template <typename T, typename W, int TPR, int NV, bool TAIL>
+__global__ __launch_bounds__(256) void rmsnorm_kernel(const NormArgs a) {
+  constexpr int V = Elem<T>::V, ROWS = 256 / TPR, WAVES = TPR / 64, STEP = TPR * V;
+  __shared__ float s_sum[2][4];
+  __shared__ uint32_t s_max[2][4];
+  const int cols = (int)a.cols;
+  const int first = (threadIdx.x % TPR) * V;
+  WeightVec<T, W, TAIL> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i].load(static_cast<const W *>(a.w), first + i * STEP, cols);
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
+  RowVecs<NV, T, TAIL> nx, nr;
+  if (row < a.rows) {
+    nx.load(x + row * a.ld_x, first, STEP, cols);
+    if (res != nullptr) nr.load(res + row * a.ld_res, first, STEP, cols);
+  }
+  // with one wave per row the waves leave the loop on their own; with four,
+  // all four have the same row
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    RowVecs<NV, T, TAIL> h = nx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V];
+      Elem<T>::unpack(h.v[i], f);
+      if (res != nullptr) {
+        float r[V];
+        Elem<T>::unpack(nr.v[i], r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] += r[j];
+        h.v[i] = Elem<T>::pack(f);
+        Elem<T>::unpack(h.v[i], f);
+        row_store<T, TAIL>(static_cast<T *>(a.h) + row * a.cols, first + i * STEP, cols, h.v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
+    }
+    const int64_t next = row + step;
+    if (next < a.rows) {
+      nx.load(x + next * a.ld_x, first, STEP, cols);
+      if (res != nullptr) nr.load(res + next * a.ld_res, first, STEP, cols);
+    }
+    sum = group_sum<WAVES>(sum, s_sum[turn]);
+    const float rstd = 1.0f / sqrtf(sum / (float)cols + a.eps);
+    if (first == 0) a.rstd[row] = rstd;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V], g[V];
+      Elem<T>::unpack(h.v[i], f);
+      w[i].get(g);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[j] = f[j] * rstd * g[j];
+        top = max(top, __float_as_uint(fabsf(f[j])));
+      }
+      if (a.y != nullptr)
+        row_store<T, TAIL>(static_cast<T *>(a.y) + row * a.cols, first + i * STEP, cols,
+                           Elem<T>::pack(f));
+    }
+    if (a.q == nullptr) continue;
+    top = group_max<WAVES>(top, s_max[turn]);
+    const RowScale s = row_scale(top);
+    if (first == 0) a.scale[row] = s.scale;
+    uint8_t *q = a.q + row * a.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V], g[V];
+      Elem<T>::unpack(h.v[i], f);
+      w[i].get(g);
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * g[j];
+      const int c = first + i * STEP;
+      uint32_t b[V / 4];
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) b[j] = e4m3x4(f + 4 * j, s);
+      if (!TAIL || c + V <= cols) {
+        if (c < cols) __builtin_memcpy(q + c, b, V);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (c + j < cols) q[c + j] = (uint8_t)(b[j / 4] >> (8 * (j % 4)));
+      }
+    }
+  }
+}
+
 // One workgroup per row at a time, three passes over it; a thread reads back
 // only what it wrote itself.
 template <typename T, typename W>
 __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
   constexpr int V = Elem<T>::V;
-  __shared__ float s_sum[4], s_max[4], s_bad[4];
+  __shared__ float s_sum[4];
+  __shared__ uint32_t s_max[4];
   const W *w = static_cast<const W *>(a.w);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
@@ -62,22 +223,20 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
     const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
     if (threadIdx.x == 0) a.rstd[row] = rstd;
     const T *src = res != nullptr ? h : x;
-    float top = 0.0f, bad = 0.0f;
+    uint32_t top = 0;
     for (int64_t c = threadIdx.x * V; c < a.cols; c += 256 * V) {
       float f[V];
       Elem<T>::unpack(load_vec(src + c, a.cols - c), f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         f[i] = f[i] * rstd * (c + i < a.cols ? Elem<W>::get(w[c + i]) : 0.0f);
-        top = fmaxf(top, fabsf(f[i]));
-        bad += f[i] * 0.0f;                      // NaN once any y is not finite
+        top = max(top, __float_as_uint(fabsf(f[i])));
       }
       if (a.y != nullptr)
         store_vec(static_cast<T *>(a.y) + row * a.cols + c, a.cols - c, Elem<T>::pack(f));
     }
     if (a.q != nullptr) {
       top = group_max<4>(top, s_max);
-      top += group_sum<4>(bad, s_bad);
       const RowScale s = row_scale(top);
       if (threadIdx.x == 0) a.scale[row] = s.scale;
       uint8_t *q = a.q + row * a.cols;
@@ -97,6 +256,105 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
       }
     }
     __syncthreads();                             // the next row reuses the LDS words
+  }
+}
+
+// Backward with rows held in registers as above: dx, and the workgroup's share
+// of dw, which stays in registers over all its rows (in the order of the
+// rows) and goes to partial[workgroup][cols] at the end, the four waves of a
+// wave-per-row workgroup added in wave order.
+template <typename T, typename W, int TPR, int NV, bool TAIL>
+__global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int V = Elem<T>::V, ROWS = 256 / TPR, WAVES = TPR / 64, STEP = TPR * V;
+  __shared__ float s_sum[2][4];
+  const int cols = (int)a.cols;
+  const int first = (threadIdx.x % TPR) * V;
+  WeightVec<T, W, TAIL> w[NV];
+  float acc[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    w[i].load(static_cast<const W *>(a.w), first + i * STEP, cols);
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const T *dy = static_cast<const T *>(a.dy), *h = static_cast<const T *>(a.h);
+  const T *dh = static_cast<const T *>(a.dh);
+  RowVecs<NV, T, TAIL> ny, nh;
+  float nrstd = 0.0f;
+  if (row < a.rows) {
+    ny.load(dy + row * a.ld_dy, first, STEP, cols);
+    nh.load(h + row * a.ld_h, first, STEP, cols);
+    nrstd = a.rstd[row];
+  }
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    const RowVecs<NV, T, TAIL> vy = ny, vh = nh;
+    const float rstd = nrstd;
+    RowVecs<NV, T, TAIL> vd;
+    if (dh != nullptr) vd.load(dh + row * a.ld_dh, first, STEP, cols);
+    const int64_t next = row + step;
+    if (next < a.rows) {
+      ny.load(dy + next * a.ld_dy, first, STEP, cols);
+      nh.load(h + next * a.ld_h, first, STEP, cols);
+      nrstd = a.rstd[next];
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V], g[V], wf[V];
+      Elem<T>::unpack(vh.v[i], f);
+      Elem<T>::unpack(vy.v[i], g);
+      w[i].get(wf);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[j] *= rstd;
+        acc[i][j] = __builtin_fmaf(g[j], f[j], acc[i][j]);
+        sum = __builtin_fmaf(g[j] * wf[j], f[j], sum);
+      }
+    }
+    const float mean = group_sum<WAVES>(sum, s_sum[turn]) / (float)cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V], g[V], wf[V];
+      Elem<T>::unpack(vh.v[i], f);
+      Elem<T>::unpack(vy.v[i], g);
+      w[i].get(wf);
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = rstd * __builtin_fmaf(-f[j] * rstd, mean, g[j] * wf[j]);
+      if (dh != nullptr) {
+        Elem<T>::unpack(vd.v[i], g);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] += g[j];
+      }
+      row_store<T, TAIL>(static_cast<T *>(a.dx) + row * a.cols, first + i * STEP, cols,
+                         Elem<T>::pack(f));
+    }
+  }
+  float *partial = a.partial + (int64_t)blockIdx.x * a.cols;
+  if (ROWS == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = first + i * STEP + j;
+        if (c < cols) partial[c] = acc[i][j];
+      }
+    return;
+  }
+  __shared__ float s_acc[ROWS == 1 ? 1 : ROWS][64 * V + 1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_acc[threadIdx.x / TPR][first + j] = acc[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < STEP && i * STEP + c < cols; c += 256) {
+      float t = s_acc[0][c];
+#pragma unroll
+      for (int r = 1; r < ROWS; ++r) t += s_acc[r][c];
+      partial[i * STEP + c] = t;
+    }
   }
 }
 
@@ -157,22 +415,76 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const NormBwdArgs a, in
   a.partial[(int64_t)blockIdx.y * a.cols + c] = sum;
 }
 
-// dw, second half: the slices' sums in slice order.
+// dw, second half: the slices' sums in a fixed order, 64 runs of slices side
+// by side for 16 columns per workgroup.
 template <typename W>
-__global__ __launch_bounds__(256) void rmsnorm_dw_final_kernel(const NormBwdArgs a, int slices) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= a.cols) return;
+__global__ __launch_bounds__(1024) void rmsnorm_dw_final_kernel(const NormBwdArgs a, int slices) {
+  __shared__ float s_sum[64][17];
+  const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + col;
   float sum = 0.0f;
-  for (int s = 0; s < slices; ++s) sum += a.partial[(int64_t)s * a.cols + c];
-  static_cast<W *>(a.dw)[c] = Elem<W>::put(sum);
+  if (c < a.cols) {
+#pragma unroll 4
+    for (int s = run; s < slices; s += 64) sum += a.partial[(int64_t)s * a.cols + c];
+  }
+  s_sum[run][col] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    if (run < o) s_sum[run][col] += s_sum[run + o][col];
+    __syncthreads();
+  }
+  if (run == 0 && c < a.cols) static_cast<W *>(a.dw)[c] = Elem<W>::put(s_sum[0][col]);
 }
 
 // A launch holds fewer than 2^32 threads; rows beyond the grid are looped over.
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
 
+// Threads per row and vectors per thread for a row of so many vectors: a wave
+// takes up to 4 vectors per lane, longer rows a workgroup, up to 8 vectors per
+// thread; (0, 0) beyond (the looping kernels).
+struct RowShape {
+  int tpr, nv;
+};
+static RowShape row_shape(int64_t cols, int v) {
+  const int64_t n = (cols + v - 1) / v;
+  if (n <= 64) return {64, 1};
+  if (n <= 128) return {64, 2};
+  if (n <= 256) return {64, 4};
+  if (n <= 512) return {256, 2};
+  if (n <= 768) return {256, 3};
+  if (n <= 1024) return {256, 4};
+  if (n <= 1536) return {256, 6};
+  if (n <= 2048) return {256, 8};
+  return {0, 0};
+}
+constexpr int kNormGrid = 2048;      // 8 workgroups of 4 waves per CU
+constexpr int kNormBwdGrid = 1024;
+static int64_t row_groups(int64_t rows, int tpr) { return (rows * tpr + 255) / 256; }
+
+#define UFP4_ROW_SHAPES(F) F(64, 1) F(64, 2) F(64, 4) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
+
+template <typename T, typename W, bool TAIL>
+static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
+  const int64_t groups = row_groups(a.rows, s.tpr);
+  const dim3 grid((unsigned)(groups < kNormGrid ? groups : kNormGrid));
+#define UFP4_NORM(TPR, NV)                                                                   \
+  if (s.tpr == TPR && s.nv == NV) {                                                          \
+    hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, NV, TAIL>), grid, dim3(256), 0, st, a);    \
+    return hipGetLastError();                                                                \
+  }
+  UFP4_ROW_SHAPES(UFP4_NORM)
+#undef UFP4_NORM
+  return hipErrorInvalidValue;
+}
+
 template <typename T, typename W>
 static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
+  const RowShape s = row_shape(a.cols, Elem<T>::V);
+  if (s.tpr != 0)
+    return a.cols % Elem<T>::V ? norm_fwd_rows<T, W, true>(a, s, st)
+                               : norm_fwd_rows<T, W, false>(a, s, st);
   hipLaunchKernelGGL((rmsnorm_row_kernel<T, W>), dim3(row_grid(a.rows)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
@@ -182,22 +494,52 @@ hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t st) {
   return a.w_bf16 ? norm_fwd<uint16_t, uint16_t>(a, st) : norm_fwd<uint16_t, float>(a, st);
 }
 
+// Rows of partial sums that dw goes through: the workgroups of the register
+// kernel, or the looping kernel's slices of rows.  The element type is not
+// known here, so this is the larger of the two types' needs.
+static int bwd_slices(int64_t rows, int64_t cols, int v) {
+  const RowShape s = row_shape(cols, v);
+  int64_t n = s.tpr != 0 ? row_groups(rows, s.tpr) : (rows + 63) / 64;
+  const int64_t most = s.tpr != 0 ? kNormBwdGrid : 256;
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)n;
+}
 int norm_bwd_slices(int64_t rows, int64_t cols) {
-  (void)cols;
-  const int64_t s = (rows + 63) / 64;
-  return s < 1 ? 1 : (s > 256 ? 256 : (int)s);
+  const int a = bwd_slices(rows, cols, Elem<uint16_t>::V), b = bwd_slices(rows, cols, Elem<float>::V);
+  return a > b ? a : b;
+}
+
+template <typename T, typename W, bool TAIL>
+static hipError_t norm_bwd_rows(const NormBwdArgs &a, RowShape s, int slices, hipStream_t st) {
+#define UFP4_NORM(TPR, NV)                                                                   \
+  if (s.tpr == TPR && s.nv == NV) {                                                          \
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, W, TPR, NV, TAIL>), dim3(slices), dim3(256), 0, \
+                       st, a);                                                               \
+    return hipGetLastError();                                                                \
+  }
+  UFP4_ROW_SHAPES(UFP4_NORM)
+#undef UFP4_NORM
+  return hipErrorInvalidValue;
 }
 
 template <typename T, typename W>
 static hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t st) {
-  const int slices = norm_bwd_slices(a.rows, a.cols);
-  const int64_t per = (a.rows + slices - 1) / slices;
-  const unsigned chunks = (unsigned)((a.cols + 255) / 256);
-  hipLaunchKernelGGL((rmsnorm_dw_kernel<T>), dim3(chunks, slices), dim3(256), 0, st, a, per);
-  hipLaunchKernelGGL((rmsnorm_dw_final_kernel<W>), dim3(chunks), dim3(256), 0, st, a, slices);
-  if (a.rows > 0)
-    hipLaunchKernelGGL((rmsnorm_bwd_row_kernel<T, W>), dim3(row_grid(a.rows)), dim3(256), 0,
-                       st, a);
+  const int slices = bwd_slices(a.rows, a.cols, Elem<T>::V);
+  const RowShape s = row_shape(a.cols, Elem<T>::V);
+  if (s.tpr != 0) {
+    const hipError_t e = a.cols % Elem<T>::V ? norm_bwd_rows<T, W, true>(a, s, slices, st)
+                                             : norm_bwd_rows<T, W, false>(a, s, slices, st);
+    if (e != hipSuccess) return e;
+  } else {
+    const int64_t per = (a.rows + slices - 1) / slices;
+    const unsigned chunks = (unsigned)((a.cols + 255) / 256);
+    hipLaunchKernelGGL((rmsnorm_dw_kernel<T>), dim3(chunks, slices), dim3(256), 0, st, a, per);
+    if (a.rows > 0)
+      hipLaunchKernelGGL((rmsnorm_bwd_row_kernel<T, W>), dim3(row_grid(a.rows)), dim3(256), 0,
+                         st, a);
+  }
+  hipLaunchKernelGGL((rmsnorm_dw_final_kernel<W>), dim3((unsigned)((a.cols + 15) / 16)),
+                     dim3(1024), 0, st, a, slices);
   return hipGetLastError();
 }
 

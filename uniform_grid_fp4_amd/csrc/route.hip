@@ -72,16 +72,6 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   return never ? 0u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
 }
 
-template <int ROT>
-__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROT, 0xF, 0xF, false);
-}
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, row_rotate<8>(v));
-  v = max(v, row_rotate<4>(v));
-  v = max(v, row_rotate<2>(v));
-  return max(v, row_rotate<1>(v));
-}
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
   v = min(v, row_rotate<8>(v));
   v = min(v, row_rotate<4>(v));
