@@ -103,7 +103,8 @@ ufp4_status ufp4_rmsnorm_bwd(const void *dy, int64_t ld_dy, const void *h, int64
  *              n_experts * sum_e (counts_e / (k N)) (sum_t p_te / N)
  *            and the z loss  sum_t lse_t^2 / N;  both 0 when N is 0.
  * workspace: device, 16-byte aligned, at least
- * ufp4_moe_route_workspace_size(tokens, n_experts) bytes, overwritten.
+ * ufp4_moe_route_workspace_size(tokens, n_experts) bytes, overwritten (0 for
+ * up to 64 tokens: then it may be NULL).
  * 1 <= k <= 16, k <= n_experts <= 1024, tokens * k < 2^31.
  *
  * ufp4_moe_route_bwd: d_logits (dense, type dtype) from d_gates FP32

@@ -105,7 +105,8 @@ def test_route_rejects(bwd, kw, expect):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(r=routing(slots=0)), -1), (dict(r=routing(offsets=A + 4)), -1),
-    (dict(r=routing(losses=0)), -1), (dict(ws=None), -1), (dict(ws=A + 8), -1), (dict(n=16), -1),
+    (dict(r=routing(losses=0)), -1), (dict(t=65, ws=None), -1), (dict(t=65, ws=A + 8), -1),
+    (dict(t=65, n=16), -1),
 ])
 def test_route_forward_only_rejects(kw, expect):
     assert route(False, **kw) == expect
@@ -118,8 +119,8 @@ def test_route_bwd_only_rejects(kw):
 
 def test_route_workspace_size():
     size = B.ufp4_moe_route_workspace_size
-    assert size(0, 8) == size(64, 8) > 0            # one workgroup's records at least
-    assert size(65, 8) > size(64, 8)
+    assert size(0, 8) == size(64, 8) == 0           # one workgroup keeps everything in LDS
+    assert size(129, 8) > size(65, 8) > 0
     assert size(-1, 8) == 0 and size(8, 0) == 0 and size(8, 1025) == 0
 
 

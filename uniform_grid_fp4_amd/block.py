@@ -12,6 +12,9 @@ UFP4Error.  Nothing here waits for the GPU or copies to the host.
 from __future__ import annotations
 
 import ctypes
+import operator
+from array import array
+from itertools import chain
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -78,33 +81,36 @@ def lib() -> ctypes.CDLL:
 def _rows2d(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
     """The row stride of a 2-D tensor with unit column stride, of `like`'s
     shape, type and device when given."""
-    if t.dtype not in _CODE:
-        raise TypeError(f"{name} is float32 or bfloat16, got {t.dtype}")
     if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} has type {t.dtype}, expected {like.dtype}")
-        if t.shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    elif not t.is_cuda:
-        raise ValueError(f"{name} is not on a GPU")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} is 2-D with at least one column, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+        _like(t, name, like.dtype, like.shape, like.device)
+    else:
+        if t.dtype not in _CODE:
+            raise TypeError(f"{name} is float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} is not on a GPU")
+        if t.dim() != 2 or t.shape[1] < 1:
+            raise ValueError(f"{name} is 2-D with at least one column, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.shape[1]
+    ld, unit = t.stride()
+    if unit != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} needs unit column stride, got strides {t.stride()}")
     # a single row's stride is not used (and may be anything)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if t.shape[0] > 1 else t.shape[1]
+
+
+def _like(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _exact(t: torch.Tensor, name: str, dtype, shape, device) -> torch.Tensor:
     """t, contiguous and of that type, shape and device."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    _like(t, name, dtype, shape, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
     return t
@@ -119,6 +125,17 @@ def _weight(w: torch.Tensor, x: torch.Tensor) -> int:
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+# torch.cuda.current_stream(device).cuda_stream without the Stream object (2 us
+# a call, a tenth of a single-token norm's time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device: torch.device):
+    if _raw_stream is None or device.index is None:
+        return U._stream(device)
+    return _raw_stream(device.index)
 
 
 # ---------------------------------------------------------------------------
@@ -161,7 +178,7 @@ def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         scale = torch.empty((rows,), dtype=torch.float32, device=dev)
     st = lib().ufp4_rmsnorm(_p(x), ld, _p(residual), ldr, _p(weight), _CODE[x.dtype], wd, rows,
                             cols, eps, _p(h) if residual is not None else None, _p(out), _p(q),
-                            _p(scale), _p(rstd), U._stream(dev))
+                            _p(scale), _p(rstd), _stream(dev))
     U._check(st, "ufp4_rmsnorm")
     return NormOut(out, h, rstd, q, scale)
 
@@ -189,7 +206,7 @@ def ufp4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     ws, nbytes = _workspace(workspace, lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols), dev)
     st = lib().ufp4_rmsnorm_bwd(_p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
                                 _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes,
-                                U._stream(dev))
+                                _stream(dev))
     U._check(st, "ufp4_rmsnorm_bwd")
     return dx, dw
 
@@ -240,18 +257,19 @@ def ufp4_moe_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] =
     if not 1 <= k <= min(e, MAX_CHOICES):
         raise ValueError(f"k = {k}: 1 to {MAX_CHOICES} choices of at most {e} experts")
     i32, f32, i64 = torch.int32, torch.float32, torch.int64
-    r = Routing(torch.empty((t, k), dtype=i32, device=dev),
-                torch.empty((t, k), dtype=f32, device=dev),
-                torch.empty((t, k), dtype=i32, device=dev),
-                torch.empty((t,), dtype=f32, device=dev),
-                torch.empty((e,), dtype=i64, device=dev),
-                torch.empty((e + 1,), dtype=i64, device=dev),
-                torch.empty((1,), dtype=i64, device=dev),
+    # the whole-number outputs of a type share one allocation (a view costs a
+    # third of one)
+    experts, slots = torch.empty((2, t, k), dtype=i32, device=dev).unbind(0)
+    counts, offsets, n_tokens = torch.empty((2 * e + 2,), dtype=i64,
+                                            device=dev).split((e, e + 1, 1))
+    r = Routing(experts, torch.empty((t, k), dtype=f32, device=dev), slots,
+                torch.empty((t,), dtype=f32, device=dev), counts, offsets, n_tokens,
                 torch.empty((2,), dtype=f32, device=dev), bool(renorm))
-    ws, nbytes = _workspace(workspace, lib().ufp4_moe_route_workspace_size(t, e), dev)
+    need = lib().ufp4_moe_route_workspace_size(t, e)
+    ws, nbytes = (None, 0) if need == 0 else _workspace(workspace, need, dev)
     d = r.desc()
     st = lib().ufp4_moe_route(_p(logits), ld, _CODE[logits.dtype], _p(valid), t, e, k, int(renorm),
-                              ctypes.byref(d), _p(ws), nbytes, U._stream(dev))
+                              ctypes.byref(d), _p(ws), nbytes, _stream(dev))
     U._check(st, "ufp4_moe_route")
     return r
 
@@ -277,7 +295,7 @@ def ufp4_moe_route_bwd(logits: torch.Tensor, r: Routing, d_gates: Optional[torch
     d = r.desc()
     st = lib().ufp4_moe_route_bwd(_p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
                                   ctypes.byref(d), _p(d_gates), _p(d_losses), _p(out),
-                                  U._stream(dev))
+                                  _stream(dev))
     U._check(st, "ufp4_moe_route_bwd")
     return out
 
@@ -311,7 +329,7 @@ def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     cols = x.shape[1]
     xs = torch.empty((t * k, cols), dtype=x.dtype, device=x.device)
     st = lib().ufp4_moe_dispatch(_p(x), ld, _p(slots), _CODE[x.dtype], t, k, cols, _p(xs),
-                                 U._stream(x.device))
+                                 _stream(x.device))
     U._check(st, "ufp4_moe_dispatch")
     return xs
 
@@ -321,7 +339,7 @@ def ufp4_moe_dispatch_bwd(dxs: torch.Tensor, slots: torch.Tensor) -> torch.Tenso
     t, k, cols = _expert_rows(dxs, "dxs", slots)
     dx = torch.empty((t, cols), dtype=dxs.dtype, device=dxs.device)
     st = lib().ufp4_moe_dispatch_bwd(_p(dxs), _p(slots), _CODE[dxs.dtype], t, k, cols, _p(dx),
-                                     U._stream(dxs.device))
+                                     _stream(dxs.device))
     U._check(st, "ufp4_moe_dispatch_bwd")
     return dx
 
@@ -341,7 +359,7 @@ def ufp4_moe_combine(ys: torch.Tensor, slots: torch.Tensor, gates: torch.Tensor,
             raise TypeError(f"residual has type {residual.dtype}, expected {ys.dtype}")
     y = torch.empty((t, cols), dtype=ys.dtype, device=ys.device)
     st = lib().ufp4_moe_combine(_p(ys), _p(slots), _p(gates), _p(residual), ldr, _CODE[ys.dtype],
-                                t, k, cols, _p(y), U._stream(ys.device))
+                                t, k, cols, _p(y), _stream(ys.device))
     U._check(st, "ufp4_moe_combine")
     return y
 
@@ -361,7 +379,7 @@ def ufp4_moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
     dys = torch.empty_like(ys)
     dg = torch.empty((t, k), dtype=torch.float32, device=ys.device)
     st = lib().ufp4_moe_combine_bwd(_p(dy), ldy, _p(ys), _p(slots), _p(gates), _CODE[ys.dtype], t,
-                                    k, cols, _p(dys), _p(dg), U._stream(ys.device))
+                                    k, cols, _p(dys), _p(dg), _stream(ys.device))
     U._check(st, "ufp4_moe_combine_bwd")
     return dys, dg
 
@@ -381,41 +399,56 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+_T = torch.Tensor
+_dtype_of, _shape_of, _device_of = (operator.attrgetter(a) for a in ("dtype", "shape", "device"))
+
+
+def _codes(tensors, name):
+    try:
+        return [_CODE[d] for d in map(_dtype_of, tensors)]
+    except KeyError as e:
+        raise TypeError(f"{name} are float32 or bfloat16, got {e.args[0]}") from None
+
+
 def _grad_list(tensors, out):
-    """(descriptors, count, device) of a list of dense tensors."""
+    """(descriptors, count, device) of a list of dense tensors.  Lists hold
+    hundreds of small tensors and this is most of their call's time, so every
+    check runs over the whole list at once."""
     n = len(tensors)
-    if out is not None and len(out) != n:
-        raise ValueError(f"{len(out)} outputs for {n} tensors")
-    d = (GradDesc * max(1, n))()
-    dev = None
-    for i, t in enumerate(tensors):
-        code = _CODE.get(t.dtype)
-        if code is None:
-            raise TypeError(f"tensor {i} is float32 or bfloat16, got {t.dtype}")
-        if not t.is_cuda or (dev is not None and t.device != dev):
-            raise ValueError(f"tensor {i} is on {t.device}: all are on one GPU")
-        dev = t.device
-        if not _dense(t):
-            raise ValueError(f"tensor {i} is not dense: strides {t.stride()} of {tuple(t.shape)}")
-        o, ocode = t, code
-        if out is not None:
-            o = out[i]
-            ocode = _CODE.get(o.dtype)
-            if ocode is None:
-                raise TypeError(f"output {i} is float32 or bfloat16, got {o.dtype}")
-            if o.shape != t.shape or o.device != dev or \
-                    (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous())):
-                raise ValueError(f"output {i} differs from its tensor in shape, strides or device")
-        d[i] = GradDesc(t.data_ptr(), o.data_ptr(), t.numel(), code, ocode)
-    return d, n, dev
+    if n == 0:
+        raise ValueError("no tensors")
+    codes = _codes(tensors, "tensors")
+    devices = set(map(_device_of, tensors))
+    dev = devices.pop()
+    if devices or dev.type != "cuda":
+        raise ValueError("the tensors are on one GPU")
+    plain = all(map(_T.is_contiguous, tensors))
+    if not plain and not all(map(_dense, tensors)):
+        raise ValueError("a tensor is not dense in memory")
+    data = list(map(_T.data_ptr, tensors))
+    ends, ocodes = data, codes
+    if out is not None:
+        if len(out) != n:
+            raise ValueError(f"{len(out)} outputs for {n} tensors")
+        ocodes = _codes(out, "outputs")
+        if list(map(_shape_of, out)) != list(map(_shape_of, tensors)):
+            raise ValueError("an output has another shape than its tensor")
+        if set(map(_device_of, out)) != {dev}:
+            raise ValueError(f"the outputs are on {dev}")
+        if not (plain and all(map(_T.is_contiguous, out))) and \
+                any(o.stride() != t.stride() for o, t in zip(out, tensors)):
+            raise ValueError("an output has other strides than its tensor")
+        ends = list(map(_T.data_ptr, out))
+    # ufp4_grad is four 64-bit words, the two types in the last
+    words = array("Q", chain.from_iterable(zip(
+        data, ends, map(_T.numel, tensors), [c | o << 32 for c, o in zip(codes, ocodes)])))
+    return words, n, dev
 
 
 def _norm_of(d, n, dev, workspace):
-    if dev is None:
-        raise ValueError("no tensors")
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, lib().ufp4_grad_norm_workspace_size(), dev)
-    st = lib().ufp4_grad_norm(ctypes.addressof(d), n, _p(ws), nbytes, _p(norm), U._stream(dev))
+    st = lib().ufp4_grad_norm(d.buffer_info()[0], n, _p(ws), nbytes, _p(norm), _stream(dev))
     U._check(st, "ufp4_grad_norm")
     return norm
 
@@ -436,6 +469,6 @@ def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
     coefficient stays on the GPU: nothing waits."""
     d, n, dev = _grad_list(tensors, out)
     norm = _norm_of(d, n, dev, workspace)
-    st = lib().ufp4_grad_clip(ctypes.addressof(d), n, _p(norm), max_norm, eps, U._stream(dev))
+    st = lib().ufp4_grad_clip(d.buffer_info()[0], n, _p(norm), max_norm, eps, _stream(dev))
     U._check(st, "ufp4_grad_clip")
     return norm

@@ -188,9 +188,8 @@ ufp4_status ufp4_moe_route(const void *logits, int64_t ld, int32_t dtype, const 
   if (s != UFP4_OK) return s;
   if ((tokens > 0 && !good(r->slots, 4)) || !good(r->offsets, 8) || !good(r->losses, 4))
     return UFP4_ERR_INVALID_ARG;
-  if (!good(workspace, 16) ||
-      workspace_bytes < ufp4_moe_route_workspace_size(tokens, n_experts))
-    return UFP4_ERR_INVALID_ARG;
+  const size_t need = ufp4_moe_route_workspace_size(tokens, n_experts);
+  if (need > 0 && (!good(workspace, 16) || workspace_bytes < need)) return UFP4_ERR_INVALID_ARG;
   RouteArgs a = route_args(logits, ld, dtype, tokens, n_experts, k, renorm, r);
   a.valid = valid;
   a.workspace = workspace;

@@ -61,7 +61,8 @@ static int64_t route_blocks(int64_t tokens) {
   return n < 1 ? 1 : n;
 }
 size_t route_workspace_bytes(int64_t tokens, int n_experts) {
-  return route_layout(route_blocks(tokens), n_experts, nullptr, nullptr);
+  const int64_t nblk = route_blocks(tokens);
+  return nblk == 1 ? 0 : route_layout(nblk, n_experts, nullptr, nullptr);
 }
 
 // A logit as an unsigned number of the same order, equal for -0 and +0; 0 for
@@ -491,8 +492,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
 template <typename T, int R>
 static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   const int64_t nblk = route_blocks(a.tokens);
-  RouteWs ws;
-  route_layout(nblk, a.n_experts, a.workspace, &ws);
+  RouteWs ws{};
+  if (nblk > 1) route_layout(nblk, a.n_experts, a.workspace, &ws);
   const size_t lds = 28u * (size_t)a.n_experts;
   if (nblk == 1) {
     hipLaunchKernelGGL((route_kernel<T, R, true>), dim3(1), dim3(256), lds, st, a, ws);
