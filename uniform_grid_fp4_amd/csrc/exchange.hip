@@ -7,14 +7,24 @@
 
 namespace ufp4 {
 
-// The row of a slot, or -1 for one outside the array.
+// The row of a slot, or -1 for one outside the array (INT32_MIN always is).
 __device__ __forceinline__ int64_t slot_row(int32_t slot, int64_t rows) {
   const int32_t r = slot < 0 ? ~slot : slot;
   return r < rows ? r : -1;
 }
 
+// The slots of up to KB choices from the j-th on; those past k are "no row".
+template <int KB>
+struct Choices {
+  int32_t slot[KB];
+  __device__ __forceinline__ Choices(const ExchangeArgs &a, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < KB; ++j) slot[j] = j0 + j < a.k ? a.slots[t * a.k + j0 + j] : INT32_MIN;
+  }
+};
+
 // Thread = one vector of one token's row, written to its k rows.
-template <typename T>
+template <typename T, int KB>
 __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int64_t chunks) {
   constexpr int V = Elem<T>::V;
   const int64_t rows = a.tokens * a.k;
@@ -23,17 +33,22 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int
     const int64_t c = ((b - t * chunks) * 256 + threadIdx.x) * V;
     if (c >= a.cols) continue;
     const u32x4 v = load_vec(static_cast<const T *>(a.in) + t * a.ld_in + c, a.cols - c);
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t slot = a.slots[t * a.k + j];
-      const int64_t r = slot_row(slot, rows);
-      if (r >= 0)
-        store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, slot < 0 ? u32x4(0) : v);
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      const Choices<KB> ch(a, t, j0);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int64_t r = slot_row(ch.slot[j], rows);
+        if (r >= 0)
+          store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c,
+                    ch.slot[j] < 0 ? u32x4(0) : v);
+      }
     }
   }
 }
 
-// Thread = one vector of one token's row: the (weighted) sum of its k rows.
-template <typename T, bool GATED>
+// Thread = one vector of one token's row: the (weighted) sum of its k rows,
+// KB of them in flight at once.
+template <typename T, bool GATED, int KB>
 __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int64_t chunks) {
   constexpr int V = Elem<T>::V;
   const int64_t rows = a.tokens * a.k;
@@ -41,22 +56,36 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
     const int64_t t = b / chunks;
     const int64_t c = ((b - t * chunks) * 256 + threadIdx.x) * V;
     if (c >= a.cols) continue;
+    const T *in = static_cast<const T *>(a.in) + c;
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t slot = a.slots[t * a.k + j];
-      if (slot < 0 || slot >= rows) continue;
-      const float g = GATED ? a.gates[t * a.k + j] : 1.0f;
-      float f[V];
-      Elem<T>::unpack(load_vec(static_cast<const T *>(a.in) + (int64_t)slot * a.cols + c,
-                               a.cols - c), f);
+    u32x4 res = u32x4(0);
+    if (GATED && a.res != nullptr)
+      res = load_vec(static_cast<const T *>(a.res) + t * a.ld_res + c, a.cols - c);
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      const Choices<KB> ch(a, t, j0);
+      u32x4 v[KB];
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] = GATED ? __builtin_fmaf(g, f[i], sum[i]) : sum[i] + f[i];
+      for (int j = 0; j < KB; ++j) {
+        v[j] = u32x4(0);
+        if (ch.slot[j] >= 0 && ch.slot[j] < rows)
+          v[j] = load_vec(in + (int64_t)ch.slot[j] * a.cols, a.cols - c);
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        if (ch.slot[j] < 0 || ch.slot[j] >= rows) continue;
+        const float g = GATED ? a.gates[t * a.k + j0 + j] : 1.0f;
+        float f[V];
+        Elem<T>::unpack(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          sum[i] = GATED ? __builtin_fmaf(g, f[i], sum[i]) : sum[i] + f[i];
+      }
     }
     if (GATED && a.res != nullptr) {
       float f[V];
-      Elem<T>::unpack(load_vec(static_cast<const T *>(a.res) + t * a.ld_res + c, a.cols - c), f);
+      Elem<T>::unpack(res, f);
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += f[i];
     }
@@ -64,37 +93,65 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
   }
 }
 
-// One workgroup per token at a time: for each choice, dys = g dy and the dot
-// product of ys and dy.
-template <typename T>
+// One workgroup per token at a time: dys = g dy in each choice's row, and the
+// dot products of its row of ys with dy, which is read once per KB choices.
+template <typename T, int KB>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) {
   constexpr int V = Elem<T>::V;
-  __shared__ float s_dot[4];
+  __shared__ float s_dot[2][KB][4];
   const int64_t rows = a.tokens * a.k;
+  int turn = 0;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const T *dy = static_cast<const T *>(a.dy) + t * a.ld_dy;
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t slot = a.slots[t * a.k + j];
-      const int64_t r = slot_row(slot, rows);
-      const bool chosen = slot >= 0 && r >= 0;
-      const float g = chosen ? a.gates[t * a.k + j] : 0.0f;
-      float dot = 0.0f;
-      for (int64_t c = threadIdx.x * V; c < a.cols; c += 256 * V) {
-        float f[V], d[V];
-        Elem<T>::unpack(load_vec(dy + c, a.cols - c), d);
-        if (chosen) {
-          Elem<T>::unpack(load_vec(static_cast<const T *>(a.in) + r * a.cols + c, a.cols - c), f);
+    for (int j0 = 0; j0 < a.k; j0 += KB, turn ^= 1) {
+      const Choices<KB> ch(a, t, j0);
+      float g[KB], dot[KB];
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot = __builtin_fmaf(f[i], d[i], dot);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = chosen ? d[i] * g : 0.0f;
-        if (r >= 0)
-          store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(d));
+      for (int j = 0; j < KB; ++j) {
+        dot[j] = 0.0f;
+        g[j] = ch.slot[j] >= 0 ? a.gates[t * a.k + j0 + j] : 0.0f;
       }
-      dot = group_sum<4>(dot, s_dot);
-      if (threadIdx.x == 0) a.d_gates[t * a.k + j] = dot;
+      for (int64_t c = threadIdx.x * V; c < a.cols; c += 256 * V) {
+        float d[V];
+        u32x4 v[KB];
+        const u32x4 vd = load_vec(dy + c, a.cols - c);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          v[j] = u32x4(0);
+          if (ch.slot[j] >= 0 && ch.slot[j] < rows)
+            v[j] = load_vec(static_cast<const T *>(a.in) + (int64_t)ch.slot[j] * a.cols + c,
+                            a.cols - c);
+        }
+        Elem<T>::unpack(vd, d);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const int64_t r = slot_row(ch.slot[j], rows);
+          if (r < 0) continue;
+          float f[V];
+          if (ch.slot[j] >= 0) {
+            Elem<T>::unpack(v[j], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              dot[j] = __builtin_fmaf(f[i], d[i], dot[j]);
+              f[i] = d[i] * g[j];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = 0.0f;
+          }
+          store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(f));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        dot[j] = lanes_sum(dot[j]);
+        if ((threadIdx.x & 63) == 0) s_dot[turn][j][threadIdx.x >> 6] = dot[j];
+      }
       __syncthreads();
+      if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < a.k) {
+        const float *s = s_dot[turn][threadIdx.x];
+        a.d_gates[t * a.k + j0 + threadIdx.x] = ((s[0] + s[1]) + s[2]) + s[3];
+      }
     }
   }
 }
@@ -104,20 +161,29 @@ static unsigned grid_of(int64_t blocks) {
   return (unsigned)(blocks < (1 << 23) ? blocks : (1 << 23));
 }
 
-template <typename T>
-static hipError_t exchange(const ExchangeArgs &a, int what, hipStream_t st) {
-  if (a.tokens == 0) return hipSuccess;
+template <typename T, int KB>
+static hipError_t exchange_of(const ExchangeArgs &a, int what, hipStream_t st) {
   const int64_t per = 256 * Elem<T>::V, chunks = (a.cols + per - 1) / per;
   const dim3 grid(grid_of(a.tokens * chunks)), block(256);
   if (what == 0)
-    hipLaunchKernelGGL((dispatch_kernel<T>), grid, block, 0, st, a, chunks);
+    hipLaunchKernelGGL((dispatch_kernel<T, KB>), grid, block, 0, st, a, chunks);
   else if (what == 1)
-    hipLaunchKernelGGL((combine_kernel<T, false>), grid, block, 0, st, a, chunks);
+    hipLaunchKernelGGL((combine_kernel<T, false, KB>), grid, block, 0, st, a, chunks);
   else if (what == 2)
-    hipLaunchKernelGGL((combine_kernel<T, true>), grid, block, 0, st, a, chunks);
+    hipLaunchKernelGGL((combine_kernel<T, true, KB>), grid, block, 0, st, a, chunks);
   else
-    hipLaunchKernelGGL((combine_bwd_kernel<T>), dim3(grid_of(a.tokens)), block, 0, st, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<T, KB>), dim3(grid_of(a.tokens)), block, 0, st, a);
   return hipGetLastError();
+}
+
+// Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds k.
+template <typename T>
+static hipError_t exchange(const ExchangeArgs &a, int what, hipStream_t st) {
+  if (a.tokens == 0) return hipSuccess;
+  if (a.k <= 1) return exchange_of<T, 1>(a, what, st);
+  if (a.k <= 2) return exchange_of<T, 2>(a, what, st);
+  if (a.k <= 4) return exchange_of<T, 4>(a, what, st);
+  return exchange_of<T, 8>(a, what, st);
 }
 
 hipError_t launch_dispatch(const ExchangeArgs &a, hipStream_t st) {

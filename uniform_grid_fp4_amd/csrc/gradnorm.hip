@@ -33,15 +33,56 @@ __device__ __forceinline__ int item_of(const GradTable &g, int32_t p) {
   return lo;
 }
 
+// Eight elements of a tensor as FP32.
 template <typename T>
-__device__ __forceinline__ double piece_squares(const T *p, int64_t n) {
-  constexpr int V = Elem<T>::V;
-  double sum = 0.0;
-  for (int64_t c = threadIdx.x * V; c < n; c += 256 * V) {
-    float f[V];
-    Elem<T>::unpack(load_vec(p + c, n - c), f);
+__device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum = __builtin_fma((double)f[i], (double)f[i], sum);
+  for (int i = 0; i < 8; i += Elem<T>::V) {
+    float v[Elem<T>::V];
+    Elem<T>::unpack(*reinterpret_cast<const u32x4_any *>(p + i), v);
+#pragma unroll
+    for (int j = 0; j < Elem<T>::V; ++j) f[i + j] = v[j];
+  }
+}
+template <typename O>
+__device__ __forceinline__ void store8(O *p, const float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += Elem<O>::V) {
+    float v[Elem<O>::V];
+#pragma unroll
+    for (int j = 0; j < Elem<O>::V; ++j) v[j] = f[i + j];
+    *reinterpret_cast<u32x4_any *>(p + i) = Elem<O>::pack(v);
+  }
+}
+
+// A piece: runs of 8 elements per thread, kRuns of them in flight, then what
+// is left by single elements.
+constexpr int kRuns = 4;
+template <typename T>
+__device__ __forceinline__ double piece_squares(const T *p, int n) {
+  double sum = 0.0;
+  int c = threadIdx.x * 8;
+  for (; c + (kRuns - 1) * 2048 + 8 <= n; c += kRuns * 2048) {
+    float f[kRuns][8];
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) load8(p + c + r * 2048, f[r]);
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)f[r][i], (double)f[r][i], sum);
+  }
+  for (; c < n; c += 2048) {
+    if (c + 8 <= n) {
+      float f[8];
+      load8(p + c, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)f[i], (double)f[i], sum);
+    } else {
+      for (int i = c; i < n; ++i) {
+        const double f = (double)Elem<T>::get(p[i]);
+        sum = __builtin_fma(f, f, sum);
+      }
+    }
   }
   return sum;
 }
@@ -53,7 +94,7 @@ __global__ __launch_bounds__(256) void grad_squares_kernel(const GradTable g, do
   for (int32_t p = blockIdx.x; p < pieces; p += gridDim.x) {
     const int i = item_of(g, p);
     const int64_t at = (int64_t)(p - g.first[i]) * kPiece;
-    const int64_t n = min(g.n[i] - at, (int64_t)kPiece);
+    const int n = (int)min(g.n[i] - at, (int64_t)kPiece);
     sum += (g.bf16[i] & 1) ? piece_squares(static_cast<const uint16_t *>(g.data[i]) + at, n)
                            : piece_squares(static_cast<const float *>(g.data[i]) + at, n);
   }
@@ -79,8 +120,30 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(double *partials, int n,
 }
 
 template <typename T, typename O>
-__device__ __forceinline__ void piece_scale(const T *p, O *out, int64_t n, float coef) {
-  for (int64_t c = threadIdx.x; c < n; c += 256) out[c] = Elem<O>::put(Elem<T>::get(p[c]) * coef);
+__device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coef) {
+  int c = threadIdx.x * 8;
+  for (; c + (kRuns - 1) * 2048 + 8 <= n; c += kRuns * 2048) {
+    float f[kRuns][8];
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) load8(p + c + r * 2048, f[r]);
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[r][i] *= coef;
+      store8(out + c + r * 2048, f[r]);
+    }
+  }
+  for (; c < n; c += 2048) {
+    if (c + 8 <= n) {
+      float f[8];
+      load8(p + c, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= coef;
+      store8(out + c, f);
+    } else {
+      for (int i = c; i < n; ++i) out[i] = Elem<O>::put(Elem<T>::get(p[i]) * coef);
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, const float *norm,
@@ -89,11 +152,12 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, cons
   c = c >= 1.0 ? 1.0 : c;                        // a NaN stays
   const float coef = (float)c;
   const int32_t pieces = g.first[g.items];
-  for (int32_t p = blockIdx.x; p < pieces; p += gridDim.x) {
+  // from the last piece to the first: what the norm read last is still cached
+  for (int32_t p = pieces - 1 - (int32_t)blockIdx.x; p >= 0; p -= gridDim.x) {
     const int i = item_of(g, p);
     if (coef == 1.0f && g.data[i] == g.out[i]) continue;
     const int64_t at = (int64_t)(p - g.first[i]) * kPiece;
-    const int64_t n = min(g.n[i] - at, (int64_t)kPiece);
+    const int n = (int)min(g.n[i] - at, (int64_t)kPiece);
     const uint16_t *hs = static_cast<const uint16_t *>(g.data[i]) + at;
     const float *fs = static_cast<const float *>(g.data[i]) + at;
     uint16_t *hd = static_cast<uint16_t *>(g.out[i]) + at;
