@@ -82,6 +82,22 @@ __device__ __forceinline__ void store_vec(T *p, int64_t n, u32x4 w) {
     if (i < n) p[i] = Elem<T>::put(f[i]);
 }
 
+// The same for tensors that pass through once: streaming accesses leave the
+// caches to what is used again.
+template <typename T>
+__device__ __forceinline__ u32x4 load_once(const T *p, int64_t n) {
+  if (n >= Elem<T>::V)
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+  return load_vec(p, n);
+}
+template <typename T>
+__device__ __forceinline__ void store_once(T *p, int64_t n, u32x4 w) {
+  if (n >= Elem<T>::V)
+    __builtin_nontemporal_store((u32x4_any)w, reinterpret_cast<u32x4_any *>(p));
+  else
+    store_vec(p, n, w);
+}
+
 // Sum / maximum over the 16 lanes of a DPP row, in every lane, by rotations of
 // 8, 4, 2 and 1: each step adds two values that both lanes of a pair hold, so
 // all lanes get the same bits.

@@ -39,8 +39,8 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int
       for (int j = 0; j < KB; ++j) {
         const int64_t r = slot_row(ch.slot[j], rows);
         if (r >= 0)
-          store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c,
-                    ch.slot[j] < 0 ? u32x4(0) : v);
+          store_once(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c,
+                     ch.slot[j] < 0 ? u32x4(0) : v);
       }
     }
   }
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
       for (int j = 0; j < KB; ++j) {
         v[j] = u32x4(0);
         if (ch.slot[j] >= 0 && ch.slot[j] < rows)
-          v[j] = load_vec(in + (int64_t)ch.slot[j] * a.cols, a.cols - c);
+          v[j] = load_once(in + (int64_t)ch.slot[j] * a.cols, a.cols - c);
       }
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
         for (int j = 0; j < KB; ++j) {
           v[j] = u32x4(0);
           if (ch.slot[j] >= 0 && ch.slot[j] < rows)
-            v[j] = load_vec(static_cast<const T *>(a.in) + (int64_t)ch.slot[j] * a.cols + c,
+            v[j] = load_once(static_cast<const T *>(a.in) + (int64_t)ch.slot[j] * a.cols + c,
                             a.cols - c);
         }
         Elem<T>::unpack(vd, d);
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
 #pragma unroll
             for (int i = 0; i < V; ++i) f[i] = 0.0f;
           }
-          store_vec(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(f));
+          store_once(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(f));
         }
       }
 #pragma unroll
