@@ -82,20 +82,33 @@ __device__ __forceinline__ void store_vec(T *p, int64_t n, u32x4 w) {
     if (i < n) p[i] = Elem<T>::put(f[i]);
 }
 
-// The same for tensors that pass through once: streaming accesses leave the
-// caches to what is used again.
+// Streaming accesses, for tensors that the 256 MB memory-side cache cannot
+// hold until their next reader anyway: the caches stay with what is used again
+// (6144 columns, 16384 x 8 rows: dispatch 354 -> 309 us).  A smaller output is
+// left to the caches for that reader (a norm of 32768 x 2048 and a reader of
+// its output: 143 us, with streaming stores 147 us).
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
 template <typename T>
-__device__ __forceinline__ u32x4 load_once(const T *p, int64_t n) {
-  if (n >= Elem<T>::V)
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+__device__ __forceinline__ u32x4 load_as(const T *p, int64_t n, bool stream) {
+  if (stream && n >= Elem<T>::V) {
+    // The empty statements keep the compiler from making one access, without
+    // the hint, of the two branches' (here and below).
+    asm volatile("");
+    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+    asm volatile("");
+    return w;
+  }
   return load_vec(p, n);
 }
 template <typename T>
-__device__ __forceinline__ void store_once(T *p, int64_t n, u32x4 w) {
-  if (n >= Elem<T>::V)
+__device__ __forceinline__ void store_as(T *p, int64_t n, u32x4 w, bool stream) {
+  if (stream && n >= Elem<T>::V) {
+    asm volatile("");
     __builtin_nontemporal_store((u32x4_any)w, reinterpret_cast<u32x4_any *>(p));
-  else
+    asm volatile("");
+  } else {
     store_vec(p, n, w);
+  }
 }
 
 // Sum / maximum over the 16 lanes of a DPP row, in every lane, by rotations of

@@ -23,6 +23,7 @@ struct NormArgs {
   uint8_t *q;               // nullptr: not wanted
   float *scale;
   float *rstd;
+  bool stream;              // h and y by streaming stores
 };
 hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t st);
 
@@ -38,6 +39,7 @@ struct NormBwdArgs {
   int bf16, w_bf16;
   int64_t rows, cols;
   void *dx;
+  bool stream;              // dx by streaming stores
   void *dw;
   float *partial;           // [norm_bwd_slices(rows, cols), cols]
 };
@@ -83,6 +85,8 @@ struct ExchangeArgs {
   int k;
   void *out;                // xs, dx, y, dys
   float *d_gates;
+  bool stream;              // the rows in expert order by streaming accesses
+  bool stream_out;          // and the output in token order
 };
 hipError_t launch_dispatch(const ExchangeArgs &a, hipStream_t st);
 // The gate-weighted sum with a residual; gates nullptr: plain sum (dispatch's

@@ -39,8 +39,8 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int
       for (int j = 0; j < KB; ++j) {
         const int64_t r = slot_row(ch.slot[j], rows);
         if (r >= 0)
-          store_once(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c,
-                     ch.slot[j] < 0 ? u32x4(0) : v);
+          store_as(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c,
+                   ch.slot[j] < 0 ? u32x4(0) : v, a.stream);
       }
     }
   }
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
       for (int j = 0; j < KB; ++j) {
         v[j] = u32x4(0);
         if (ch.slot[j] >= 0 && ch.slot[j] < rows)
-          v[j] = load_once(in + (int64_t)ch.slot[j] * a.cols, a.cols - c);
+          v[j] = load_as(in + (int64_t)ch.slot[j] * a.cols, a.cols - c, a.stream);
       }
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
@@ -89,7 +89,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += f[i];
     }
-    store_vec(static_cast<T *>(a.out) + t * a.cols + c, a.cols - c, Elem<T>::pack(sum));
+    store_as(static_cast<T *>(a.out) + t * a.cols + c, a.cols - c, Elem<T>::pack(sum),
+             a.stream_out);
   }
 }
 
@@ -119,8 +120,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
         for (int j = 0; j < KB; ++j) {
           v[j] = u32x4(0);
           if (ch.slot[j] >= 0 && ch.slot[j] < rows)
-            v[j] = load_once(static_cast<const T *>(a.in) + (int64_t)ch.slot[j] * a.cols + c,
-                            a.cols - c);
+            v[j] = load_as(static_cast<const T *>(a.in) + (int64_t)ch.slot[j] * a.cols + c,
+                           a.cols - c, a.stream);
         }
         Elem<T>::unpack(vd, d);
 #pragma unroll
@@ -139,7 +140,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
 #pragma unroll
             for (int i = 0; i < V; ++i) f[i] = 0.0f;
           }
-          store_once(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(f));
+          store_as(static_cast<T *>(a.out) + r * a.cols + c, a.cols - c, Elem<T>::pack(f),
+                   a.stream);
         }
       }
 #pragma unroll
@@ -178,8 +180,11 @@ static hipError_t exchange_of(const ExchangeArgs &a, int what, hipStream_t st) {
 
 // Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds k.
 template <typename T>
-static hipError_t exchange(const ExchangeArgs &a, int what, hipStream_t st) {
+static hipError_t exchange(ExchangeArgs a, int what, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
+  const int64_t bytes = a.tokens * a.cols * (int64_t)sizeof(T);
+  a.stream = bytes * a.k >= kStreamBytes;
+  a.stream_out = bytes >= kStreamBytes;
   if (a.k <= 1) return exchange_of<T, 1>(a, what, st);
   if (a.k <= 2) return exchange_of<T, 2>(a, what, st);
   if (a.k <= 4) return exchange_of<T, 4>(a, what, st);

@@ -45,13 +45,13 @@ __device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
   }
 }
 template <typename O>
-__device__ __forceinline__ void store8(O *p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(O *p, const float (&f)[8], bool stream) {
 #pragma unroll
   for (int i = 0; i < 8; i += Elem<O>::V) {
     float v[Elem<O>::V];
 #pragma unroll
     for (int j = 0; j < Elem<O>::V; ++j) v[j] = f[i + j];
-    *reinterpret_cast<u32x4_any *>(p + i) = Elem<O>::pack(v);
+    store_as(p + i, Elem<O>::V, Elem<O>::pack(v), stream);
   }
 }
 
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(double *partials, int n,
 }
 
 template <typename T, typename O>
-__device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coef) {
+__device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coef, bool stream) {
   int c = threadIdx.x * 8;
   for (; c + (kRuns - 1) * 2048 + 8 <= n; c += kRuns * 2048) {
     float f[kRuns][8];
@@ -130,7 +130,7 @@ __device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coe
     for (int r = 0; r < kRuns; ++r) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[r][i] *= coef;
-      store8(out + c + r * 2048, f[r]);
+      store8(out + c + r * 2048, f[r], stream);
     }
   }
   for (; c < n; c += 2048) {
@@ -139,7 +139,7 @@ __device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coe
       load8(p + c, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= coef;
-      store8(out + c, f);
+      store8(out + c, f, stream);
     } else {
       for (int i = c; i < n; ++i) out[i] = Elem<O>::put(Elem<T>::get(p[i]) * coef);
     }
@@ -147,7 +147,7 @@ __device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coe
 }
 
 __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, const float *norm,
-                                                         double max_norm, double eps) {
+                                                         double max_norm, double eps, bool stream) {
   double c = max_norm / ((double)*norm + eps);
   c = c >= 1.0 ? 1.0 : c;                        // a NaN stays
   const float coef = (float)c;
@@ -163,10 +163,10 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, cons
     uint16_t *hd = static_cast<uint16_t *>(g.out[i]) + at;
     float *fd = static_cast<float *>(g.out[i]) + at;
     switch (g.bf16[i]) {
-      case 0: piece_scale(fs, fd, n, coef); break;
-      case 1: piece_scale(hs, fd, n, coef); break;
-      case 2: piece_scale(fs, hd, n, coef); break;
-      default: piece_scale(hs, hd, n, coef); break;
+      case 0: piece_scale(fs, fd, n, coef, stream); break;
+      case 1: piece_scale(hs, fd, n, coef, stream); break;
+      case 2: piece_scale(fs, hd, n, coef, stream); break;
+      default: piece_scale(hs, hd, n, coef, stream); break;
     }
   }
 }
@@ -221,9 +221,14 @@ hipError_t launch_grad_norm(const ufp4_grad *items, int64_t n_items, double *par
 
 hipError_t launch_grad_clip(const ufp4_grad *items, int64_t n_items, const float *norm,
                             double max_norm, double eps, hipStream_t st) {
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < n_items; ++i)
+    bytes += items[i].n * (items[i].out_dtype == UFP4_OUT_BF16 ? 2 : 4);
+  const bool stream = bytes >= kStreamBytes;
   return each_table(items, n_items, [&](const GradTable &g, int32_t pieces) {
     const int grid = pieces < kGradGrid ? pieces : kGradGrid;
-    hipLaunchKernelGGL(grad_scale_kernel, dim3(grid), dim3(256), 0, st, g, norm, max_norm, eps);
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(grid), dim3(256), 0, st, g, norm, max_norm, eps,
+                       stream);
     return hipGetLastError();
   });
 }

@@ -37,9 +37,8 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
 
 // Rows held in registers: TPR threads (one wave or a workgroup of four) hold a
 // row as NV vectors each, so x and the residual are read once and everything
-// else happens in registers.  A workgroup walks over rows with the weight kept
-// in registers and the next row's loads in flight.  TAIL: the row length is
-// not a multiple of the vector.
+// else happens in registers.  TAIL: the row length is not a multiple of the
+// vector.
 template <int NV, typename T, bool TAIL>
 struct RowVecs {
   static constexpr int V = Elem<T>::V;
@@ -57,12 +56,8 @@ struct RowVecs {
   }
 };
 template <typename T, bool TAIL>
-__device__ __forceinline__ void row_store(T *p, int c, int cols, u32x4 v) {
-  if (c >= cols) return;
-  if (TAIL)
-    store_vec(p + c, cols - c, v);
-  else
-    *reinterpret_cast<u32x4_any *>(p + c) = v;
+__device__ __forceinline__ void row_store(T *p, int c, int cols, u32x4 v, bool stream) {
+  if (c < cols) store_as(p + c, TAIL ? cols - c : Elem<T>::V, v, stream);
 }
 
 // The weights of one vector's columns: packed as the rows are when the types
@@ -115,15 +110,12 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(const NormArgs a) {
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
-  RowVecs<NV, T, TAIL> nx, nr;
-  if (row < a.rows) {
-    nx.load(x + row * a.ld_x, first, STEP, cols);
-    if (res != nullptr) nr.load(res + row * a.ld_res, first, STEP, cols);
-  }
   // with one wave per row the waves leave the loop on their own; with four,
   // all four have the same row
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-    RowVecs<NV, T, TAIL> h = nx;
+    RowVecs<NV, T, TAIL> h, r0;
+    h.load(x + row * a.ld_x, first, STEP, cols);
+    if (res != nullptr) r0.load(res + row * a.ld_res, first, STEP, cols);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -131,20 +123,16 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(const NormArgs a) {
       Elem<T>::unpack(h.v[i], f);
       if (res != nullptr) {
         float r[V];
-        Elem<T>::unpack(nr.v[i], r);
+        Elem<T>::unpack(r0.v[i], r);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] += r[j];
         h.v[i] = Elem<T>::pack(f);
         Elem<T>::unpack(h.v[i], f);
-        row_store<T, TAIL>(static_cast<T *>(a.h) + row * a.cols, first + i * STEP, cols, h.v[i]);
+        row_store<T, TAIL>(static_cast<T *>(a.h) + row * a.cols, first + i * STEP, cols, h.v[i],
+                           a.stream);
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
-    }
-    const int64_t next = row + step;
-    if (next < a.rows) {
-      nx.load(x + next * a.ld_x, first, STEP, cols);
-      if (res != nullptr) nr.load(res + next * a.ld_res, first, STEP, cols);
     }
     sum = group_sum<WAVES>(sum, s_sum[turn]);
     const float rstd = 1.0f / sqrtf(sum / (float)cols + a.eps);
@@ -162,7 +150,7 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(const NormArgs a) {
       }
       if (a.y != nullptr)
         row_store<T, TAIL>(static_cast<T *>(a.y) + row * a.cols, first + i * STEP, cols,
-                           Elem<T>::pack(f));
+                           Elem<T>::pack(f), a.stream);
     }
     if (a.q == nullptr) continue;
     top = group_max<WAVES>(top, s_max[turn]);
@@ -281,24 +269,12 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   const T *dy = static_cast<const T *>(a.dy), *h = static_cast<const T *>(a.h);
   const T *dh = static_cast<const T *>(a.dh);
-  RowVecs<NV, T, TAIL> ny, nh;
-  float nrstd = 0.0f;
-  if (row < a.rows) {
-    ny.load(dy + row * a.ld_dy, first, STEP, cols);
-    nh.load(h + row * a.ld_h, first, STEP, cols);
-    nrstd = a.rstd[row];
-  }
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-    const RowVecs<NV, T, TAIL> vy = ny, vh = nh;
-    const float rstd = nrstd;
-    RowVecs<NV, T, TAIL> vd;
+    RowVecs<NV, T, TAIL> vd, vy, vh;
+    vy.load(dy + row * a.ld_dy, first, STEP, cols);
+    vh.load(h + row * a.ld_h, first, STEP, cols);
+    const float rstd = a.rstd[row];
     if (dh != nullptr) vd.load(dh + row * a.ld_dh, first, STEP, cols);
-    const int64_t next = row + step;
-    if (next < a.rows) {
-      ny.load(dy + next * a.ld_dy, first, STEP, cols);
-      nh.load(h + next * a.ld_h, first, STEP, cols);
-      nrstd = a.rstd[next];
-    }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -328,7 +304,7 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
         for (int j = 0; j < V; ++j) f[j] += g[j];
       }
       row_store<T, TAIL>(static_cast<T *>(a.dx) + row * a.cols, first + i * STEP, cols,
-                         Elem<T>::pack(f));
+                         Elem<T>::pack(f), a.stream);
     }
   }
   float *partial = a.partial + (int64_t)blockIdx.x * a.cols;
@@ -458,29 +434,42 @@ static RowShape row_shape(int64_t cols, int v) {
   if (n <= 2048) return {256, 8};
   return {0, 0};
 }
-constexpr int kNormGrid = 2048;      // 8 workgroups of 4 waves per CU
-constexpr int kNormBwdGrid = 1024;
+// Workgroups of the backward pass.  Each writes a row of partial sums, so more
+// of them cost traffic and a longer second half; fewer leave the memory idle
+// (16384 x 6144 bf16: 256 workgroups 168 us, 512 160 us, 1024 175 us; 8192 x
+// 2048: 34, 28 and 30 us).
+constexpr int kNormBwdGrid = 512;
+// The backward pass also keeps dw's sums: four vectors per lane would leave one
+// wave per SIMD (8192 x 2048 bf16: 40 us, a workgroup per row 30 us).
+static RowShape bwd_shape(int64_t cols, int v) {
+  const int64_t n = (cols + v - 1) / v;
+  return n > 128 && n <= 256 ? RowShape{256, 1} : row_shape(cols, v);
+}
 static int64_t row_groups(int64_t rows, int tpr) { return (rows * tpr + 255) / 256; }
 
-#define UFP4_ROW_SHAPES(F) F(64, 1) F(64, 2) F(64, 4) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
+#define UFP4_FWD_SHAPES(F) \
+  F(64, 1) F(64, 2) F(64, 4) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
+#define UFP4_BWD_SHAPES(F) \
+  F(64, 1) F(64, 2) F(256, 1) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
 
 template <typename T, typename W, bool TAIL>
 static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
   const int64_t groups = row_groups(a.rows, s.tpr);
-  const dim3 grid((unsigned)(groups < kNormGrid ? groups : kNormGrid));
+  const dim3 grid(row_grid(groups));
 #define UFP4_NORM(TPR, NV)                                                                   \
   if (s.tpr == TPR && s.nv == NV) {                                                          \
     hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, NV, TAIL>), grid, dim3(256), 0, st, a);    \
     return hipGetLastError();                                                                \
   }
-  UFP4_ROW_SHAPES(UFP4_NORM)
+  UFP4_FWD_SHAPES(UFP4_NORM)
 #undef UFP4_NORM
   return hipErrorInvalidValue;
 }
 
 template <typename T, typename W>
-static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
+static hipError_t norm_fwd(NormArgs a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
+  a.stream = a.rows * a.cols * (int64_t)sizeof(T) >= kStreamBytes;
   const RowShape s = row_shape(a.cols, Elem<T>::V);
   if (s.tpr != 0)
     return a.cols % Elem<T>::V ? norm_fwd_rows<T, W, true>(a, s, st)
@@ -498,7 +487,7 @@ hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t st) {
 // kernel, or the looping kernel's slices of rows.  The element type is not
 // known here, so this is the larger of the two types' needs.
 static int bwd_slices(int64_t rows, int64_t cols, int v) {
-  const RowShape s = row_shape(cols, v);
+  const RowShape s = bwd_shape(cols, v);
   int64_t n = s.tpr != 0 ? row_groups(rows, s.tpr) : (rows + 63) / 64;
   const int64_t most = s.tpr != 0 ? kNormBwdGrid : 256;
   if (n > most) n = most;
@@ -517,15 +506,16 @@ static hipError_t norm_bwd_rows(const NormBwdArgs &a, RowShape s, int slices, hi
                        st, a);                                                               \
     return hipGetLastError();                                                                \
   }
-  UFP4_ROW_SHAPES(UFP4_NORM)
+  UFP4_BWD_SHAPES(UFP4_NORM)
 #undef UFP4_NORM
   return hipErrorInvalidValue;
 }
 
 template <typename T, typename W>
-static hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t st) {
+static hipError_t norm_bwd(NormBwdArgs a, hipStream_t st) {
+  a.stream = a.rows * a.cols * (int64_t)sizeof(T) >= kStreamBytes;
   const int slices = bwd_slices(a.rows, a.cols, Elem<T>::V);
-  const RowShape s = row_shape(a.cols, Elem<T>::V);
+  const RowShape s = bwd_shape(a.cols, Elem<T>::V);
   if (s.tpr != 0) {
     const hipError_t e = a.cols % Elem<T>::V ? norm_bwd_rows<T, W, true>(a, s, slices, st)
                                              : norm_bwd_rows<T, W, false>(a, s, slices, st);
