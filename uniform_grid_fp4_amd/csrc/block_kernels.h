@@ -85,8 +85,7 @@ struct ExchangeArgs {
   int k;
   void *out;                // xs, dx, y, dys
   float *d_gates;
-  bool stream;              // the rows in expert order by streaming accesses
-  bool stream_out;          // and the output in token order
+  bool stream;              // everything but x, dy and residual by streaming accesses
 };
 hipError_t launch_dispatch(const ExchangeArgs &a, hipStream_t st);
 // The gate-weighted sum with a residual; gates nullptr: plain sum (dispatch's

@@ -21,9 +21,9 @@ constexpr int kGroups = 16;                      // tokens in flight per workgro
 constexpr int kPer = kRouteTokens / kGroups;     // tokens per group of 16 lanes
 
 // Workspace of a call with nblk workgroups, E experts:
-//   uint32 base [nblk][E + 1]  choices per workgroup and expert (last: choices
-//                              that do not exist), then their exclusive sums
-//   float  psum [nblk][E]      sums of p
+//   uint32 base [E + 1][nblk]  choices per expert (last: choices that do not
+//                              exist) and workgroup, then their exclusive sums
+//   float  psum [E][nblk]      sums of p
 //   double z    [nblk], uint32 live [nblk]
 //   uint32 total[E + 2]        choices per expert, missing choices, tokens
 //   double ptotal[E + 1]       sums of p, and of lse^2
@@ -72,6 +72,23 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   const bool never = !(l > -INFINITY);
   return never ? 0u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
 }
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
+// exp for the softmax: x = l - max <= 0.  x log2(e) as a rounded product and
+// its remainder, so that the error stays near one unit in the last place for
+// every x (the plain product's rounding would grow with |x|).  Below -150
+// nothing is left in FP32; a NaN is taken to 0 there and is accounted for by
+// the callers, which add the row's NaN to its sum.
+__device__ __forceinline__ float exp_below(float x) {
+  x = fmaxf(x, -150.0f);
+  constexpr float kLog2eHi = 1.44269504f, kLog2eLo = 1.92596303e-8f, kLn2 = 0.693147181f;
+  const float h = x * kLog2eHi;
+  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return __builtin_fmaf(e * r, kLn2, e);
+}
 
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
   v = min(v, row_rotate<8>(v));
@@ -106,28 +123,41 @@ struct Hold {
   }
 };
 
-// Exclusive sums of v over 1024 or fewer entries in LDS by one workgroup of
-// 256 threads; returns the total.  s_tmp: 256 words.
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t below = (uint32_t)__shfl_up((int)v, o, 64);
+    if (lane >= o) v += below;
+  }
+  return v;
+}
+
+// Exclusive sums of v[0..n), n <= 1024, in LDS by a workgroup of 256 threads,
+// four entries per thread; returns the total.  s_tmp: 4 words.
 __device__ uint32_t scan_shared(uint32_t *v, int n, uint32_t *s_tmp) {
-  const int per = (n + 255) / 256, at = threadIdx.x * per;
-  uint32_t mine = 0;
-  for (int i = 0; i < per; ++i) mine += at + i < n ? v[at + i] : 0u;
-  s_tmp[threadIdx.x] = mine;
+  const int at = threadIdx.x * 4, wave = threadIdx.x >> 6;
+  uint32_t x[4], mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = at + i < n ? v[at + i] : 0u;
+    mine += x[i];
+  }
+  const uint32_t upto = wave_scan(mine);
+  if ((threadIdx.x & 63) == 63) s_tmp[wave] = upto;
   __syncthreads();
-  for (int o = 1; o < 256; o <<= 1) {
-    const uint32_t below = (int)threadIdx.x >= o ? s_tmp[threadIdx.x - o] : 0u;
-    __syncthreads();
-    s_tmp[threadIdx.x] += below;
-    __syncthreads();
+  uint32_t run = upto - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < wave) run += s_tmp[i];
+    total += s_tmp[i];
   }
-  uint32_t run = s_tmp[threadIdx.x] - mine;
-  for (int i = 0; i < per; ++i) {
-    if (at + i >= n) break;
-    const uint32_t x = v[at + i];
-    v[at + i] = run;
-    run += x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (at + i < n) v[at + i] = run;
+    run += x[i];
   }
-  const uint32_t total = s_tmp[255];
   __syncthreads();
   return total;
 }
@@ -146,7 +176,7 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, double balance,
 template <typename T, int R, bool ALONE>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const RouteWs ws) {
   extern __shared__ __align__(16) char s_dyn[];
-  __shared__ uint32_t s_scan[256];
+  __shared__ uint32_t s_scan[4];
   __shared__ uint32_t s_lost[kRouteTokens], s_live[kRouteTokens];
   __shared__ float s_lse[kRouteTokens];
   __shared__ double s_part[4];
@@ -163,8 +193,18 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   int32_t choice[kPer], found[kPer];             // lane j: the token's j-th choice
 #pragma unroll
   for (int n = 0; n < kPer; ++n) {
+    choice[n] = -1;
+    found[n] = 0;
     const int local = n * kGroups + group;
     const int64_t t = (int64_t)blockIdx.x * kRouteTokens + local;
+    if ((int64_t)blockIdx.x * kRouteTokens + n * kGroups >= a.tokens) {   // the whole workgroup
+      if (lane == 0) {
+        s_lost[local] = 0;
+        s_live[local] = 0;
+        s_lse[local] = 0.0f;
+      }
+      continue;
+    }
     const bool here = t < a.tokens;
     bool live = here && (a.valid == nullptr || a.valid[t] != 0);
     float f[R];
@@ -183,44 +223,70 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     top = row_max(top);
     nan = row_sum(nan);
     live = live && (top > -INFINITY || nan != nan);
-    // the choices: k rounds of the largest key left, the lowest expert among
+    // the choices: k rounds of the largest logit left, the lowest expert among
     // equals; lane j keeps round j's
-    uint32_t key[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) key[i] = order_key(f[i]);
     int32_t mine = -1, count = 0;
     float picked = -INFINITY;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0;
+    if constexpr (sizeof(T) == 2) {
+      // a bf16's order in 16 bits and 1023 - expert below it make keys that
+      // differ, so the next choice is the largest key below the last one:
+      // key - last wraps to the top of the range for exactly those
+      uint32_t key[R], last = 1u << 26;
 #pragma unroll
-      for (int i = 0; i < R; ++i) best = max(best, key[i]);
-      best = row_max(best);
-      uint32_t who = 0xFFFFFFFFu;
+      for (int i = 0; i < R; ++i) {
+        const uint32_t o = order_key(f[i]);
+        key[i] = o == 0u ? 0u
+                         : (((o >> 6) & 0x03FFFC00u) | (1023u - Hold<T, R>::expert(lane, i)));
+      }
+      for (int j = 0; j < k; ++j) {
+        uint32_t best = 0;
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (key[i] == best) who = min(who, (uint32_t)Hold<T, R>::expert(lane, i));
-      who = row_min(who);
+        for (int i = 0; i < R; ++i) best = max(best, key[i] - last);
+        best = row_max(best);
+        last = (best & 0x80000000u) ? best + last : 0u;
+        if (lane == j && last != 0u) {
+          mine = (int32_t)(1023u - (last & 1023u));
+          const uint32_t o = (last << 6) & 0xFFFF0000u;
+          picked = key_logit((o & 0x80000000u) ? o : o | 0xFFFFu);
+        }
+        count += last != 0u ? 1 : 0;
+      }
+    } else {
+      uint32_t key[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if ((uint32_t)Hold<T, R>::expert(lane, i) == who) key[i] = 0u;
-      if (best != 0u) ++count;
-      if (lane == j && best != 0u) {
-        mine = (int32_t)who;
-        picked = __uint_as_float((best & 0x80000000u) ? best ^ 0x80000000u : ~best);
+      for (int i = 0; i < R; ++i) key[i] = order_key(f[i]);
+      for (int j = 0; j < k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) best = max(best, key[i]);
+        best = row_max(best);
+        uint32_t who = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (key[i] == best) who = min(who, (uint32_t)Hold<T, R>::expert(lane, i));
+        who = row_min(who);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if ((uint32_t)Hold<T, R>::expert(lane, i) == who) key[i] = 0u;
+        if (lane == j && best != 0u) {
+          mine = (int32_t)who;
+          picked = key_logit(best);
+        }
+        count += best != 0u ? 1 : 0;
       }
     }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      f[i] = live && Hold<T, R>::expert(lane, i) < E ? expf(f[i] - top) : 0.0f;
+      f[i] = live && Hold<T, R>::expert(lane, i) < E ? exp_below(f[i] - top) : 0.0f;
       sum += f[i];
     }
-    sum = row_sum(sum);
+    sum = row_sum(sum) + nan;
     const float lse = live ? top + logf(sum) : -INFINITY;
     const float inv = live ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) psum[i] = __builtin_fmaf(f[i], inv, psum[i]);
-    float gate = mine >= 0 ? expf(picked - top) : 0.0f;
+    float gate = mine >= 0 ? exp_below(picked - top) : 0.0f;
     const float total = row_sum(gate);
     gate = mine < 0 ? 0.0f : (a.renorm ? gate / total + nan : gate * inv);
     choice[n] = mine;
@@ -251,13 +317,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   double z = 0.0;
   if (threadIdx.x < kRouteTokens) {
     const uint32_t own = s_lost[threadIdx.x];
-    uint32_t run = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t below = __shfl_up(run, o, 64);
-      if ((int)threadIdx.x >= o) run += below;
-    }
-    lost_all = __shfl(run, 63, 64);
+    const uint32_t run = wave_scan(own);
+    lost_all = (uint32_t)__shfl((int)run, 63, 64);
     s_lost[threadIdx.x] = run - own;
     tokens = (uint32_t)__popcll(__ballot(s_live[threadIdx.x] != 0));
     z = lanes_sum((double)s_lse[threadIdx.x] * (double)s_lse[threadIdx.x]);
@@ -271,8 +332,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       a.counts[e] = (int64_t)c;
       balance += (double)c * (double)p;
     } else {
-      ws.base[(int64_t)blockIdx.x * (E + 1) + e] = c;
-      ws.psum[(int64_t)blockIdx.x * E + e] = p;
+      ws.base[(int64_t)e * gridDim.x + blockIdx.x] = c;
+      ws.psum[(int64_t)e * gridDim.x + blockIdx.x] = p;
     }
   }
   uint32_t routed = 0;
@@ -286,7 +347,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], z, tokens);
   } else {
     if (threadIdx.x == 0) {
-      ws.base[(int64_t)blockIdx.x * (E + 1) + E] = lost_all;
+      ws.base[(int64_t)E * gridDim.x + blockIdx.x] = lost_all;
       ws.z[blockIdx.x] = z;
       ws.live[blockIdx.x] = tokens;
     }
@@ -311,62 +372,47 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   }
 }
 
-// Column c of base over the workgroups: exclusive sums in place and the total;
-// psum's columns summed in FP64.  64 runs of workgroups per column, 16 columns
-// per workgroup of 1024 threads; the last workgroup sums z and the tokens.
-__global__ __launch_bounds__(1024) void route_scan_kernel(const RouteArgs a, const RouteWs ws,
-                                                          int nblk) {
-  __shared__ uint32_t s_n[64][16];
-  __shared__ double s_d[64][16];
-  const int E = a.n_experts;
-  const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
-  const int per = (nblk + 63) / 64, b0 = min(run * per, nblk), b1 = min(b0 + per, nblk);
-  const bool tail = blockIdx.x == gridDim.x - 1;
-  const int c = blockIdx.x * 16 + col;
-  uint32_t n = 0;
+// One wave per expert (and one for the missing choices, one for z and the
+// tokens): exclusive sums of its counts over the workgroups, in place, and the
+// sum of its p in FP64.
+__global__ __launch_bounds__(64) void route_scan_kernel(const RouteArgs a, const RouteWs ws,
+                                                        int nblk) {
+  const int E = a.n_experts, c = blockIdx.x, lane = threadIdx.x;
   double d = 0.0;
-  if (tail) {
-    if (col == 0)
-      for (int b = b0; b < b1; ++b) {
-        n += ws.live[b];
-        d += ws.z[b];
+  uint32_t run = 0;
+  if (c <= E) {
+    uint32_t *base = ws.base + (int64_t)c * nblk;
+    const float *p = ws.psum + (int64_t)c * nblk;
+    for (int b = lane * 4; b - lane * 4 < nblk; b += 256) {
+      uint32_t v[4];
+      uint32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = b + i < nblk ? base[b + i] : 0u;
+        if (c < E) d += b + i < nblk ? (double)p[b + i] : 0.0;
+        mine += v[i];
       }
-  } else if (c <= E) {
-    for (int b = b0; b < b1; ++b) {
-      n += ws.base[(int64_t)b * (E + 1) + c];
-      if (c < E) d += (double)ws.psum[(int64_t)b * E + c];
-    }
-  }
-  s_n[run][col] = n;
-  s_d[run][col] = d;
-  __syncthreads();
-  if (run == 0) {
-    uint32_t total = 0;
-    double sum = 0.0;
-    for (int i = 0; i < 64; ++i) {
-      const uint32_t v = s_n[i][col];
-      s_n[i][col] = total;
-      total += v;
-      sum += s_d[i][col];
-    }
-    if (tail) {
-      if (col == 0) {
-        ws.total[E + 1] = total;
-        ws.ptotal[E] = sum;
+      const uint32_t upto = wave_scan(mine);
+      uint32_t at = run + upto - mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (b + i < nblk) base[b + i] = at;
+        at += v[i];
       }
-    } else if (c <= E) {
-      ws.total[c] = total;
-      if (c < E) ws.ptotal[c] = sum;
+      run += (uint32_t)__shfl((int)upto, 63, 64);
     }
+  } else {
+    for (int b = lane; b < nblk; b += 64) {
+      run += ws.live[b];
+      d += ws.z[b];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) run += (uint32_t)__shfl_xor((int)run, o, 64);
   }
-  __syncthreads();
-  if (tail || c > E) return;
-  uint32_t at = s_n[run][col];
-  for (int b = b0; b < b1; ++b) {
-    uint32_t *p = ws.base + (int64_t)b * (E + 1) + c;
-    const uint32_t v = *p;
-    *p = at;
-    at += v;
+  d = lanes_sum(d);
+  if (lane == 0) {
+    ws.total[c] = run;
+    if (c != E) ws.ptotal[c > E ? E : c] = d;
   }
 }
 
@@ -374,7 +420,7 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(const RouteArgs a, con
 // counts, offsets and losses.
 __global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, const RouteWs ws) {
   __shared__ uint32_t s_off[kRouteMaxExperts];
-  __shared__ uint32_t s_scan[256];
+  __shared__ uint32_t s_scan[4];
   __shared__ double s_part[4];
   const int E = a.n_experts, k = a.k;
   const bool first = blockIdx.x == 0;
@@ -398,13 +444,14 @@ __global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, con
       write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], ws.ptotal[E],
                    ws.total[E + 1]);
   }
-  const uint32_t *base = ws.base + (int64_t)blockIdx.x * (E + 1);
+  const uint32_t *base = ws.base + blockIdx.x;
+  const int64_t nblk = gridDim.x;
   const int64_t i0 = (int64_t)blockIdx.x * kRouteTokens * k;
   const int64_t i1 = min(i0 + (int64_t)kRouteTokens * k, a.tokens * k);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
     const int32_t e = a.experts[i], place = a.slots[i];
-    a.slots[i] = e >= 0 ? (int32_t)(s_off[e] + base[e] + (uint32_t)place)
-                        : (int32_t)~(routed + base[E] + (uint32_t)~place);
+    a.slots[i] = e >= 0 ? (int32_t)(s_off[e] + base[e * nblk] + (uint32_t)place)
+                        : (int32_t)~(routed + base[E * nblk] + (uint32_t)~place);
   }
 }
 
@@ -456,17 +503,20 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     if (mine >= 0) s_add[mine] = a.renorm ? g * (dg - s) : g * dg;
     // p from the row's own maximum and sum: exp(l - lse) would carry lse's
     // rounding, which for large logits is larger than the logits' distances
-    float top = -INFINITY;
+    float top = -INFINITY, nan = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) top = fmaxf(top, f[i]);
+    for (int i = 0; i < R; ++i) {
+      top = fmaxf(top, f[i]);
+      nan = f[i] != f[i] ? f[i] : nan;
+    }
     top = row_max(top);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      f[i] = live && Hold<T, R>::expert(lane, i) < E ? expf(f[i] - top) : 0.0f;
+      f[i] = live && Hold<T, R>::expert(lane, i) < E ? exp_below(f[i] - top) : 0.0f;
       sum += f[i];
     }
-    const float inv = live ? 1.0f / row_sum(sum) : 0.0f;
+    const float inv = live ? 1.0f / (row_sum(sum) + row_sum(nan)) : 0.0f;
     float pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -475,17 +525,30 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     }
     pc = row_sum(pc);
     const float shift = (live ? z_of * lse : 0.0f) - pc - (a.renorm ? 0.0f : s);
-    __syncthreads();
+    // the group's row in LDS is one wave's: its accesses stay in order
+    __builtin_amdgcn_wave_barrier();
+    if (here) {
+      T *out = static_cast<T *>(a.d_logits) + t * E;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int e = Hold<T, R>::expert(lane, i);
-      if (here && e < E)
-        static_cast<T *>(a.d_logits)[t * E + e] =
-            Elem<T>::put(__builtin_fmaf(f[i], c[i] + shift, s_add[e]));
+      for (int i = 0; i < R; i += Hold<T, R>::W) {
+        constexpr int W = Hold<T, R>::W;
+        const int e = Hold<T, R>::expert(lane, i);
+        float d[Elem<T>::V];
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          d[j] = e + j < E ? __builtin_fmaf(f[i + j], c[i + j] + shift, s_add[e + j]) : 0.0f;
+        if (W == Elem<T>::V && e + W <= E) {
+          *reinterpret_cast<u32x4_any *>(out + e) = Elem<T>::pack(d);
+        } else {
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            if (e + j < E) out[e + j] = Elem<T>::put(d[j]);
+        }
+      }
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();
     if (mine >= 0) s_add[mine] = 0.0f;
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -501,8 +564,8 @@ static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   }
   hipLaunchKernelGGL((route_kernel<T, R, false>), dim3((unsigned)nblk), dim3(256), lds, st, a,
                      ws);
-  hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((a.n_experts + 1 + 15) / 16 + 1)),
-                     dim3(1024), 0, st, a, ws, (int)nblk);
+  hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)(a.n_experts + 2)), dim3(64), 0, st, a, ws,
+                     (int)nblk);
   hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)nblk), dim3(256), 0, st, a, ws);
   return hipGetLastError();
 }
@@ -511,7 +574,7 @@ template <typename T, int R>
 static hipError_t route_back(const RouteArgs &a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const int64_t nblk = (a.tokens + kGroups - 1) / kGroups;
-  const unsigned grid = (unsigned)(nblk < 4096 ? nblk : 4096);
+  const unsigned grid = (unsigned)(nblk < 2048 ? nblk : 2048);
   hipLaunchKernelGGL((route_bwd_kernel<T, R>), dim3(grid), dim3(256),
                      (size_t)kGroups * 4u * (size_t)a.n_experts, st, a, nblk);
   return hipGetLastError();
