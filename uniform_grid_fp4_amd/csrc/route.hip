@@ -69,8 +69,8 @@ size_t route_workspace_bytes(int64_t tokens, int n_experts) {
 // -inf and NaN, which are never chosen.
 __device__ __forceinline__ uint32_t order_key(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);
-  const bool never = !(l > -INFINITY);
-  return never ? 0u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
+  const uint32_t o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return l > -INFINITY ? o : 0u;
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
@@ -99,25 +99,30 @@ __device__ __forceinline__ uint32_t row_min(uint32_t v) {
 
 // Expert held by lane l in register i: sixteen lanes take runs of W
 // consecutive experts (one 16-byte load where the runs are that long).
-template <typename T, int R>
+// FULL: there are exactly 16 R experts, and no lane has to ask whether its own
+// exist.
+template <typename T, int R, bool FULL>
 struct Hold {
   static constexpr int W = R < Elem<T>::V ? R : Elem<T>::V;
   __device__ static __forceinline__ int expert(int lane, int i) {
     return (i / W) * (16 * W) + lane * W + i % W;
+  }
+  __device__ static __forceinline__ bool exists(int lane, int i, int e) {
+    return FULL || expert(lane, i) < e;
   }
   // The token's logits; -inf past the last expert.
   __device__ static __forceinline__ void load(const T *p, int e, int lane, float (&f)[R]) {
 #pragma unroll
     for (int i = 0; i < R; i += W) {
       const int at = expert(lane, i);
-      if (W == Elem<T>::V && at + W <= e) {
+      if (W == Elem<T>::V && (FULL || at + W <= e)) {
         float v[Elem<T>::V];
         Elem<T>::unpack(*reinterpret_cast<const u32x4_any *>(p + at), v);
 #pragma unroll
         for (int j = 0; j < W; ++j) f[i + j] = v[j];
       } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[i + j] = at + j < e ? Elem<T>::get(p[at + j]) : -INFINITY;
+        for (int j = 0; j < W; ++j) f[i + j] = FULL || at + j < e ? Elem<T>::get(p[at + j]) : -INFINITY;
       }
     }
   }
@@ -173,14 +178,15 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, double balance,
 
 // Choices, gates and, for the workgroup's 64 tokens, places and counts; with
 // ALONE (one workgroup) everything else too.  Dynamic LDS: 28 bytes per expert.
-template <typename T, int R, bool ALONE>
+template <typename T, int R, bool FULL, bool ALONE>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const RouteWs ws) {
   extern __shared__ __align__(16) char s_dyn[];
   __shared__ uint32_t s_scan[4];
   __shared__ uint32_t s_lost[kRouteTokens], s_live[kRouteTokens];
   __shared__ float s_lse[kRouteTokens];
   __shared__ double s_part[4];
-  const int E = a.n_experts, k = a.k;
+  const int E = FULL ? 16 * R : a.n_experts, k = a.k;
+  using H = Hold<T, R, FULL>;
   unsigned long long *s_mask = reinterpret_cast<unsigned long long *>(s_dyn);
   float *s_p = reinterpret_cast<float *>(s_dyn + 8 * E);
   uint32_t *s_off = reinterpret_cast<uint32_t *>(s_dyn + 24 * E);
@@ -190,6 +196,21 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
 #pragma unroll
   for (int i = 0; i < R; ++i) psum[i] = 0.0f;
   __syncthreads();
+  // a token's logits, all -inf (and false) for one that takes no part
+  const auto fetch = [&](int64_t t, float (&f)[R]) {
+    const bool live = t < a.tokens && (a.valid == nullptr || a.valid[t] != 0);
+    if (live) {
+      H::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) f[i] = -INFINITY;
+    }
+    return live;
+  };
+  // the next token's loads run under this one's work where registers allow
+  constexpr bool kAhead = R <= 16 && !ALONE;
+  float ahead[kAhead ? R : 1];
+  bool ahead_live = false;
   int32_t choice[kPer], found[kPer];             // lane j: the token's j-th choice
 #pragma unroll
   for (int n = 0; n < kPer; ++n) {
@@ -206,22 +227,26 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       continue;
     }
     const bool here = t < a.tokens;
-    bool live = here && (a.valid == nullptr || a.valid[t] != 0);
     float f[R];
-    if (live) {
-      Hold<T, R>::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
-    } else {
+    bool live;
+    if constexpr (kAhead) {
+      if (n == 0) ahead_live = fetch(t, ahead);
+      live = ahead_live;
 #pragma unroll
-      for (int i = 0; i < R; ++i) f[i] = -INFINITY;
+      for (int i = 0; i < R; ++i) f[i] = ahead[i];
+      if (n + 1 < kPer) ahead_live = fetch(t + kGroups, ahead);
+    } else {
+      live = fetch(t, f);
     }
-    float top = -INFINITY, nan = 0.0f;
+    float top = -INFINITY;
+    bool has_nan = false;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       top = fmaxf(top, f[i]);
-      nan = f[i] != f[i] ? f[i] : nan;
+      if (i % 2 == 0) has_nan |= __builtin_isunordered(f[i], f[i + 1 < R ? i + 1 : i]);
     }
     top = row_max(top);
-    nan = row_sum(nan);
+    const float nan = row_sum(has_nan ? __builtin_nanf("") : 0.0f);
     live = live && (top > -INFINITY || nan != nan);
     // the choices: k rounds of the largest logit left, the lowest expert among
     // equals; lane j keeps round j's
@@ -234,9 +259,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       uint32_t key[R], last = 1u << 26;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const uint32_t o = order_key(f[i]);
-        key[i] = o == 0u ? 0u
-                         : (((o >> 6) & 0x03FFFC00u) | (1023u - Hold<T, R>::expert(lane, i)));
+        // (a key without an order is below every key with one: it ends the choice)
+        key[i] = (order_key(f[i]) >> 16 << 10) | (1023u - (uint32_t)H::expert(lane, i));
       }
       for (int j = 0; j < k; ++j) {
         uint32_t best = 0;
@@ -244,6 +268,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
         for (int i = 0; i < R; ++i) best = max(best, key[i] - last);
         best = row_max(best);
         last = (best & 0x80000000u) ? best + last : 0u;
+        if (last < 1024u) last = 0u;
         if (lane == j && last != 0u) {
           mine = (int32_t)(1023u - (last & 1023u));
           const uint32_t o = (last << 6) & 0xFFFF0000u;
@@ -263,11 +288,11 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
         uint32_t who = 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          if (key[i] == best) who = min(who, (uint32_t)Hold<T, R>::expert(lane, i));
+          if (key[i] == best) who = min(who, (uint32_t)H::expert(lane, i));
         who = row_min(who);
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          if ((uint32_t)Hold<T, R>::expert(lane, i) == who) key[i] = 0u;
+          if ((uint32_t)H::expert(lane, i) == who) key[i] = 0u;
         if (lane == j && best != 0u) {
           mine = (int32_t)who;
           picked = key_logit(best);
@@ -278,14 +303,18 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      f[i] = live && Hold<T, R>::expert(lane, i) < E ? exp_below(f[i] - top) : 0.0f;
+      f[i] = exp_below(f[i] - top);
+      if (!H::exists(lane, i, E)) f[i] = 0.0f;
       sum += f[i];
     }
-    sum = row_sum(sum) + nan;
+    sum = row_sum(sum) + nan;                    // a token that takes no part: unused
     const float lse = live ? top + logf(sum) : -INFINITY;
     const float inv = live ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) psum[i] = __builtin_fmaf(f[i], inv, psum[i]);
+    for (int i = 0; i < R; ++i) {
+      if (!live) f[i] = 0.0f;
+      psum[i] = __builtin_fmaf(f[i], inv, psum[i]);
+    }
     float gate = mine >= 0 ? exp_below(picked - top) : 0.0f;
     const float total = row_sum(gate);
     gate = mine < 0 ? 0.0f : (a.renorm ? gate / total + nan : gate * inv);
@@ -308,8 +337,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   for (int i = 0; i < R; ++i) {
     psum[i] += __shfl_xor(psum[i], 16, 64);
     psum[i] += __shfl_xor(psum[i], 32, 64);
-    const int e = Hold<T, R>::expert(lane, i);
-    if ((threadIdx.x & 48) == 0 && e < E) s_p[wave * E + e] = psum[i];
+    const int e = H::expert(lane, i);
+    if ((threadIdx.x & 48) == 0 && H::exists(lane, i, E)) s_p[wave * E + e] = psum[i];
   }
   __syncthreads();
   // wave 0, lane = token: missing choices before each token, tokens, z
@@ -460,10 +489,11 @@ __global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, con
 // s' = sum g dg, without s = sum g dg and s' = 0.  Dynamic LDS: per group a
 // row of E floats that takes the chosen experts' terms to the lanes that hold
 // them, zero in between.
-template <typename T, int R>
+template <typename T, int R, bool FULL>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64_t nblk) {
   extern __shared__ __align__(16) char s_dyn[];
-  const int E = a.n_experts, k = a.k;
+  const int E = FULL ? 16 * R : a.n_experts, k = a.k;
+  using H = Hold<T, R, FULL>;
   const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
   float *s_add = reinterpret_cast<float *>(s_dyn) + group * E;
   for (int e = lane; e < E; e += 16) s_add[e] = 0.0f;
@@ -475,8 +505,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
   float c[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int e = Hold<T, R>::expert(lane, i);
-    c[i] = e < E ? c_of * (float)a.counts[e] : 0.0f;
+    const int e = H::expert(lane, i);
+    c[i] = H::exists(lane, i, E) ? c_of * (float)a.counts[e] : 0.0f;
   }
   __syncthreads();
   for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < nblk * kGroups;
@@ -486,7 +516,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     const bool live = lse != -INFINITY;
     float f[R];
     if (live) {
-      Hold<T, R>::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
+      H::load(static_cast<const T *>(a.logits) + t * a.ld, E, lane, f);
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i) f[i] = -INFINITY;
@@ -501,48 +531,41 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     }
     const float s = row_sum(g * dg);
     if (mine >= 0) s_add[mine] = a.renorm ? g * (dg - s) : g * dg;
-    // p from the row's own maximum and sum: exp(l - lse) would carry lse's
-    // rounding, which for large logits is larger than the logits' distances
-    float top = -INFINITY, nan = 0.0f;
+    // p as exp(l - lse) over its own sum: lse's rounding, which for large logits
+    // is larger than the logits' distances, cancels.  No l exceeds lse, and the
+    // largest is within 2 log(experts) of it, so the sum is never lost.
+    float sum = 0.0f, pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      top = fmaxf(top, f[i]);
-      nan = f[i] != f[i] ? f[i] : nan;
-    }
-    top = row_max(top);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      f[i] = live && Hold<T, R>::expert(lane, i) < E ? exp_below(f[i] - top) : 0.0f;
+      f[i] = exp_below(f[i] - lse);
+      if (!(live && H::exists(lane, i, E))) f[i] = 0.0f;
       sum += f[i];
-    }
-    const float inv = live ? 1.0f / (row_sum(sum) + row_sum(nan)) : 0.0f;
-    float pc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      f[i] *= inv;
       pc = __builtin_fmaf(f[i], c[i], pc);
     }
-    pc = row_sum(pc);
+    // (lse - lse is NaN where lse is not finite)
+    const float inv = live ? 1.0f / row_sum(sum) + (lse - lse) : 0.0f;
+    pc = row_sum(pc) * inv;
     const float shift = (live ? z_of * lse : 0.0f) - pc - (a.renorm ? 0.0f : s);
     // the group's row in LDS is one wave's: its accesses stay in order
     __builtin_amdgcn_wave_barrier();
     if (here) {
       T *out = static_cast<T *>(a.d_logits) + t * E;
 #pragma unroll
-      for (int i = 0; i < R; i += Hold<T, R>::W) {
-        constexpr int W = Hold<T, R>::W;
-        const int e = Hold<T, R>::expert(lane, i);
+      for (int i = 0; i < R; i += H::W) {
+        constexpr int W = H::W;
+        const int e = H::expert(lane, i);
         float d[Elem<T>::V];
+        if (W == Elem<T>::V && (FULL || e + W <= E)) {
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-          d[j] = e + j < E ? __builtin_fmaf(f[i + j], c[i + j] + shift, s_add[e + j]) : 0.0f;
-        if (W == Elem<T>::V && e + W <= E) {
+          for (int j = 0; j < W; ++j)
+            d[j] = __builtin_fmaf(f[i + j] * inv, c[i + j] + shift, s_add[e + j]);
           *reinterpret_cast<u32x4_any *>(out + e) = Elem<T>::pack(d);
         } else {
 #pragma unroll
           for (int j = 0; j < W; ++j)
-            if (e + j < E) out[e + j] = Elem<T>::put(d[j]);
+            if (FULL || e + j < E)
+              out[e + j] =
+                  Elem<T>::put(__builtin_fmaf(f[i + j] * inv, c[i + j] + shift, s_add[e + j]));
         }
       }
     }
@@ -552,17 +575,17 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
   }
 }
 
-template <typename T, int R>
+template <typename T, int R, bool FULL>
 static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   const int64_t nblk = route_blocks(a.tokens);
   RouteWs ws{};
   if (nblk > 1) route_layout(nblk, a.n_experts, a.workspace, &ws);
   const size_t lds = 28u * (size_t)a.n_experts;
   if (nblk == 1) {
-    hipLaunchKernelGGL((route_kernel<T, R, true>), dim3(1), dim3(256), lds, st, a, ws);
+    hipLaunchKernelGGL((route_kernel<T, R, FULL, true>), dim3(1), dim3(256), lds, st, a, ws);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((route_kernel<T, R, false>), dim3((unsigned)nblk), dim3(256), lds, st, a,
+  hipLaunchKernelGGL((route_kernel<T, R, FULL, false>), dim3((unsigned)nblk), dim3(256), lds, st, a,
                      ws);
   hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)(a.n_experts + 2)), dim3(64), 0, st, a, ws,
                      (int)nblk);
@@ -570,12 +593,12 @@ static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int R>
+template <typename T, int R, bool FULL>
 static hipError_t route_back(const RouteArgs &a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const int64_t nblk = (a.tokens + kGroups - 1) / kGroups;
   const unsigned grid = (unsigned)(nblk < 2048 ? nblk : 2048);
-  hipLaunchKernelGGL((route_bwd_kernel<T, R>), dim3(grid), dim3(256),
+  hipLaunchKernelGGL((route_bwd_kernel<T, R, FULL>), dim3(grid), dim3(256),
                      (size_t)kGroups * 4u * (size_t)a.n_experts, st, a, nblk);
   return hipGetLastError();
 }
@@ -583,8 +606,10 @@ static hipError_t route_back(const RouteArgs &a, hipStream_t st) {
 // Logits per lane: the smallest power of two that holds the experts.
 template <typename T>
 static hipError_t route_any(const RouteArgs &a, bool back, hipStream_t st) {
-#define UFP4_ROUTE(R) \
-  if (a.n_experts <= 16 * R) return back ? route_back<T, R>(a, st) : route_fwd<T, R>(a, st)
+#define UFP4_ROUTE(R)                                                                          \
+  if (a.n_experts == 16 * R)                                                                   \
+    return back ? route_back<T, R, true>(a, st) : route_fwd<T, R, true>(a, st);                \
+  if (a.n_experts < 16 * R) return back ? route_back<T, R, false>(a, st) : route_fwd<T, R, false>(a, st)
   UFP4_ROUTE(1);
   UFP4_ROUTE(2);
   UFP4_ROUTE(4);
