@@ -166,16 +166,17 @@ def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     ldr, h = 0, x
     if residual is not None:
         ldr = _rows2d(residual, "residual", x)
-        h = torch.empty((rows, cols), dtype=x.dtype, device=dev) if out_h is None else \
+        h = x.new_empty((rows, cols)) if out_h is None else \
             _exact(out_h, "out_h", x.dtype, (rows, cols), dev)
     elif out_h is not None:
         raise ValueError("out_h is given without a residual")
-    out = torch.empty((rows, cols), dtype=x.dtype, device=dev) if y else None
-    rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    out = x.new_empty((rows, cols)) if y else None
     q = scale = None
     if q8:
         q = torch.empty((rows, cols), dtype=E4M3, device=dev)
-        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd, scale = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
+    else:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
     st = lib().ufp4_rmsnorm(_p(x), ld, _p(residual), ldr, _p(weight), _CODE[x.dtype], wd, rows,
                             cols, eps, _p(h) if residual is not None else None, _p(out), _p(q),
                             _p(scale), _p(rstd), _stream(dev))
@@ -201,8 +202,7 @@ def ufp4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     rows, cols = h.shape
     dev = h.device
     _exact(rstd, "rstd", torch.float32, (rows,), dev)
-    dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
-    dw = torch.empty((cols,), dtype=weight.dtype, device=dev)
+    dx, dw = h.new_empty((rows, cols)), weight.new_empty((cols,))
     ws, nbytes = _workspace(workspace, lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols), dev)
     st = lib().ufp4_rmsnorm_bwd(_p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
                                 _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes,
@@ -291,7 +291,7 @@ def ufp4_moe_route_bwd(logits: torch.Tensor, r: Routing, d_gates: Optional[torch
         _exact(d_gates, "d_gates", torch.float32, (t, k), dev)
     if d_losses is not None:
         _exact(d_losses, "d_losses", torch.float32, (2,), dev)
-    out = torch.empty((t, e), dtype=logits.dtype, device=dev)
+    out = logits.new_empty((t, e))
     d = r.desc()
     st = lib().ufp4_moe_route_bwd(_p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
                                   ctypes.byref(d), _p(d_gates), _p(d_losses), _p(out),
@@ -315,10 +315,19 @@ def _slots(slots: torch.Tensor, tokens: Optional[int], device) -> Tuple[int, int
 
 def _expert_rows(xs: torch.Tensor, name: str, slots: torch.Tensor) -> Tuple[int, int, int]:
     """(tokens, k, columns) of a dense [tokens * k, columns] tensor."""
-    _rows2d(xs, name)
+    ld = _rows2d(xs, name)
     t, k = _slots(slots, None, xs.device)
-    _exact(xs, name, xs.dtype, (t * k, xs.shape[1]), xs.device)
-    return t, k, xs.shape[1]
+    rows, cols = xs.shape
+    if rows != t * k or ld != cols:
+        raise ValueError(f"{name} is dense [{t * k}, columns], got {tuple(xs.shape)} with strides "
+                         f"{xs.stride()}")
+    return t, k, cols
+
+
+def _token_rows(t: torch.Tensor, name: str, shape, like: torch.Tensor) -> int:
+    """The row stride of a tensor of `shape` and of `like`'s type and device."""
+    _like(t, name, like.dtype, shape, like.device)
+    return _rows2d(t, name)
 
 
 def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
@@ -327,7 +336,7 @@ def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     ld = _rows2d(x, "x")
     t, k = _slots(slots, x.shape[0], x.device)
     cols = x.shape[1]
-    xs = torch.empty((t * k, cols), dtype=x.dtype, device=x.device)
+    xs = x.new_empty((t * k, cols))
     st = lib().ufp4_moe_dispatch(_p(x), ld, _p(slots), _CODE[x.dtype], t, k, cols, _p(xs),
                                  _stream(x.device))
     U._check(st, "ufp4_moe_dispatch")
@@ -337,7 +346,7 @@ def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
 def ufp4_moe_dispatch_bwd(dxs: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     """The gradient of dispatch's input: each token's sum over its choices."""
     t, k, cols = _expert_rows(dxs, "dxs", slots)
-    dx = torch.empty((t, cols), dtype=dxs.dtype, device=dxs.device)
+    dx = dxs.new_empty((t, cols))
     st = lib().ufp4_moe_dispatch_bwd(_p(dxs), _p(slots), _CODE[dxs.dtype], t, k, cols, _p(dx),
                                      _stream(dxs.device))
     U._check(st, "ufp4_moe_dispatch_bwd")
@@ -351,13 +360,8 @@ def ufp4_moe_combine(ys: torch.Tensor, slots: torch.Tensor, gates: torch.Tensor,
     _exact(gates, "gates", torch.float32, (t, k), ys.device)
     ldr = 0
     if residual is not None:
-        ldr = _rows2d(residual, "residual")
-        if residual.shape != (t, cols) or residual.device != ys.device:
-            raise ValueError(f"residual is [{t}, {cols}] on {ys.device}, got "
-                             f"{tuple(residual.shape)} on {residual.device}")
-        if residual.dtype != ys.dtype:
-            raise TypeError(f"residual has type {residual.dtype}, expected {ys.dtype}")
-    y = torch.empty((t, cols), dtype=ys.dtype, device=ys.device)
+        ldr = _token_rows(residual, "residual", (t, cols), ys)
+    y = ys.new_empty((t, cols))
     st = lib().ufp4_moe_combine(_p(ys), _p(slots), _p(gates), _p(residual), ldr, _CODE[ys.dtype],
                                 t, k, cols, _p(y), _stream(ys.device))
     U._check(st, "ufp4_moe_combine")
@@ -369,15 +373,10 @@ def ufp4_moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
     """(dys, d_gates) of ufp4_moe_combine; dy itself is the residual's
     gradient."""
     t, k, cols = _expert_rows(ys, "ys", slots)
-    ldy = _rows2d(dy, "dy")
-    if dy.shape != (t, cols) or dy.device != ys.device:
-        raise ValueError(f"dy is [{t}, {cols}] on {ys.device}, got {tuple(dy.shape)} on "
-                         f"{dy.device}")
-    if dy.dtype != ys.dtype:
-        raise TypeError(f"dy has type {dy.dtype}, expected {ys.dtype}")
+    ldy = _token_rows(dy, "dy", (t, cols), ys)
     _exact(gates, "gates", torch.float32, (t, k), ys.device)
     dys = torch.empty_like(ys)
-    dg = torch.empty((t, k), dtype=torch.float32, device=ys.device)
+    dg = gates.new_empty((t, k))
     st = lib().ufp4_moe_combine_bwd(_p(dy), ldy, _p(ys), _p(slots), _p(gates), _CODE[ys.dtype], t,
                                     k, cols, _p(dys), _p(dg), _stream(ys.device))
     U._check(st, "ufp4_moe_combine_bwd")
@@ -400,12 +399,13 @@ def _dense(t: torch.Tensor) -> bool:
 
 
 _T = torch.Tensor
-_dtype_of, _shape_of, _device_of = (operator.attrgetter(a) for a in ("dtype", "shape", "device"))
+_dtype_of = operator.attrgetter("dtype")
+_PAIR = (0, 1 | 1 << 32)                          # a type and the same type as the output
 
 
 def _codes(tensors, name):
     try:
-        return [_CODE[d] for d in map(_dtype_of, tensors)]
+        return list(map(_CODE.__getitem__, map(_dtype_of, tensors)))
     except KeyError as e:
         raise TypeError(f"{name} are float32 or bfloat16, got {e.args[0]}") from None
 
@@ -418,31 +418,31 @@ def _grad_list(tensors, out):
     if n == 0:
         raise ValueError("no tensors")
     codes = _codes(tensors, "tensors")
-    devices = set(map(_device_of, tensors))
-    dev = devices.pop()
-    if devices or dev.type != "cuda":
+    gpu = set(map(_T.get_device, tensors))
+    if len(gpu) != 1 or -1 in gpu:
         raise ValueError("the tensors are on one GPU")
     plain = all(map(_T.is_contiguous, tensors))
     if not plain and not all(map(_dense, tensors)):
         raise ValueError("a tensor is not dense in memory")
-    data = list(map(_T.data_ptr, tensors))
-    ends, ocodes = data, codes
+    data, sizes = list(map(_T.data_ptr, tensors)), list(map(_T.numel, tensors))
+    ends, types = data, map(_PAIR.__getitem__, codes)
     if out is not None:
         if len(out) != n:
             raise ValueError(f"{len(out)} outputs for {n} tensors")
         ocodes = _codes(out, "outputs")
-        if list(map(_shape_of, out)) != list(map(_shape_of, tensors)):
-            raise ValueError("an output has another shape than its tensor")
-        if set(map(_device_of, out)) != {dev}:
-            raise ValueError(f"the outputs are on {dev}")
+        if ocodes != codes:
+            types = [c | o << 32 for c, o in zip(codes, ocodes)]
+        if list(map(_T.numel, out)) != sizes:
+            raise ValueError("an output has another size than its tensor")
+        if set(map(_T.get_device, out)) != gpu:
+            raise ValueError("the outputs are on the tensors' GPU")
         if not (plain and all(map(_T.is_contiguous, out))) and \
-                any(o.stride() != t.stride() for o, t in zip(out, tensors)):
-            raise ValueError("an output has other strides than its tensor")
+                any(o.shape != t.shape or o.stride() != t.stride() for o, t in zip(out, tensors)):
+            raise ValueError("an output has another shape or other strides than its tensor")
         ends = list(map(_T.data_ptr, out))
     # ufp4_grad is four 64-bit words, the two types in the last
-    words = array("Q", chain.from_iterable(zip(
-        data, ends, map(_T.numel, tensors), [c | o << 32 for c, o in zip(codes, ocodes)])))
-    return words, n, dev
+    words = array("Q", chain.from_iterable(zip(data, ends, sizes, types)))
+    return words, n, tensors[0].device
 
 
 def _norm_of(d, n, dev, workspace):
@@ -465,8 +465,9 @@ def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
                     out: Optional[Sequence[torch.Tensor]] = None, eps: float = 1e-6,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Scale all tensors by min(1, max_norm / (norm + eps)), in place or into
-    `out` (same shapes; bf16 or float32), and return the norm before it.  The
-    coefficient stays on the GPU: nothing waits."""
+    `out` (as many elements each, contiguous, or of the tensors' shapes and
+    strides; bf16 or float32), and return the norm before it.  The coefficient
+    stays on the GPU: nothing waits."""
     d, n, dev = _grad_list(tensors, out)
     norm = _norm_of(d, n, dev, workspace)
     st = lib().ufp4_grad_clip(d.buffer_info()[0], n, _p(norm), max_norm, eps, _stream(dev))
