@@ -116,8 +116,8 @@ __device__ __forceinline__ void store_as(T *p, int64_t n, u32x4 w, bool stream) 
 // all lanes get the same bits.
 template <int ROT>
 __device__ __forceinline__ float row_rotate(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
-      0, (int)__float_as_uint(v), 0x120 + ROT, 0xF, 0xF, false));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(
+      (int)__float_as_uint(v), 0x120 + ROT, 0xF, 0xF, true));
 }
 __device__ __forceinline__ float row_sum(float v) {
   v += row_rotate<8>(v);
@@ -128,7 +128,7 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 template <int ROT>
 __device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROT, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + ROT, 0xF, 0xF, true);
 }
 // fmaxf drops a NaN operand; callers that must keep NaN test for it apart.
 __device__ __forceinline__ float row_max(float v) {
@@ -144,16 +144,31 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, row_rotate<2>(v));
   return max(v, row_rotate<1>(v));
 }
-__device__ __forceinline__ float lanes_sum(float v) {
-  v = row_sum(v);
-  v += __shfl_xor(v, 16, 64);
-  v += __shfl_xor(v, 32, 64);
-  return v;
+// The four rows of a wave: v_permlane16_swap_b32 of a value with itself gives
+// every pair of rows the first's and the second's value, v_permlane32_swap_b32
+// every pair of halves.
+struct Pair {
+  uint32_t a, b;
+};
+__device__ __forceinline__ Pair row_pairs(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return {p[0], p[1]};
 }
+__device__ __forceinline__ Pair half_pairs(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return {p[0], p[1]};
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  Pair p = row_pairs(__float_as_uint(v));
+  v = __uint_as_float(p.a) + __uint_as_float(p.b);
+  p = half_pairs(__float_as_uint(v));
+  return __uint_as_float(p.a) + __uint_as_float(p.b);
+}
+__device__ __forceinline__ float lanes_sum(float v) { return rows_sum(row_sum(v)); }
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  v = row_max(v);
-  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-  return max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  Pair p = row_pairs(row_max(v));
+  p = half_pairs(max(p.a, p.b));
+  return max(p.a, p.b);
 }
 __device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll

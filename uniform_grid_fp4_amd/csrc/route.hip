@@ -65,29 +65,21 @@ size_t route_workspace_bytes(int64_t tokens, int n_experts) {
   return nblk == 1 ? 0 : route_layout(nblk, n_experts, nullptr, nullptr);
 }
 
-// A logit as an unsigned number of the same order, equal for -0 and +0; 0 for
-// -inf and NaN, which are never chosen.
+// A logit as an unsigned number of the same order, equal for -0 and +0.
 __device__ __forceinline__ uint32_t order_key(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);
-  const uint32_t o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return l > -INFINITY ? o : 0u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
+constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // order_key(-inf): nothing at or below is chosen
 
-// exp for the softmax: x = l - max <= 0.  x log2(e) as a rounded product and
-// its remainder, so that the error stays near one unit in the last place for
-// every x (the plain product's rounding would grow with |x|).  Below -150
-// nothing is left in FP32; a NaN is taken to 0 there and is accounted for by
-// the callers, which add the row's NaN to its sum.
-__device__ __forceinline__ float exp_below(float x) {
-  x = fmaxf(x, -150.0f);
-  constexpr float kLog2eHi = 1.44269504f, kLog2eLo = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const float h = x * kLog2eHi;
-  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -h));
-  const float e = __builtin_amdgcn_exp2f(h);
-  return __builtin_fmaf(e * r, kLn2, e);
+// exp(l - from) for the softmax sums, l <= from.  The argument's rounding makes
+// a term off by |l - from| 2^-23 of itself; terms far from the maximum, where
+// that grows, are small.
+__device__ __forceinline__ float exp_term(float l, float from) {
+  return __builtin_amdgcn_exp2f((l - from) * 1.44269504f);
 }
 
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
@@ -239,15 +231,21 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       live = fetch(t, f);
     }
     float top = -INFINITY;
-    bool has_nan = false;
+#pragma unroll
+    for (int i = 0; i < R; ++i) top = fmaxf(top, f[i]);
+    top = row_max(top);
+    // terms of the sum; a row without a finite logit sums to 0, a NaN shows in
+    // the sum
+    const float from = top > -INFINITY ? top : 0.0f;
+    float e[R], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      top = fmaxf(top, f[i]);
-      if (i % 2 == 0) has_nan |= __builtin_isunordered(f[i], f[i + 1 < R ? i + 1 : i]);
+      e[i] = exp_term(f[i], from);
+      sum += e[i];
     }
-    top = row_max(top);
-    const float nan = row_sum(has_nan ? __builtin_nanf("") : 0.0f);
-    live = live && (top > -INFINITY || nan != nan);
+    sum = row_sum(sum);
+    const bool odd = sum != sum;                 // a NaN, or infinities
+    live = live && (top > -INFINITY || odd);
     // the choices: k rounds of the largest logit left, the lowest expert among
     // equals; lane j keeps round j's
     int32_t mine = -1, count = 0;
@@ -256,19 +254,26 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
       // a bf16's order in 16 bits and 1023 - expert below it make keys that
       // differ, so the next choice is the largest key below the last one:
       // key - last wraps to the top of the range for exactly those
+      // (a lane's own keys leave out the lane's bits, which its `last` takes off)
+      const uint32_t mine_bits = (uint32_t)(15 - lane) * H::W;
       uint32_t key[R], last = 1u << 26;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        // (a key without an order is below every key with one: it ends the choice)
-        key[i] = (order_key(f[i]) >> 16 << 10) | (1023u - (uint32_t)H::expert(lane, i));
+      for (int i = 0; i < R; ++i)
+        key[i] = (order_key(f[i]) >> 16 << 10) | (1023u - (uint32_t)H::expert(15, i));
+      if (__any(odd)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (f[i] != f[i]) key[i] = 0u;
       }
       for (int j = 0; j < k; ++j) {
+        uint32_t below = last - mine_bits;
+        asm("" : "+v"(below));                   // one subtraction per key, not two
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < R; ++i) best = max(best, key[i] - last);
+        for (int i = 0; i < R; ++i) best = max(best, key[i] - below);
         best = row_max(best);
         last = (best & 0x80000000u) ? best + last : 0u;
-        if (last < 1024u) last = 0u;
+        if (last <= (kKeyMinusInf >> 16 << 10 | 1023u)) last = 0u;
         if (lane == j && last != 0u) {
           mine = (int32_t)(1023u - (last & 1023u));
           const uint32_t o = (last << 6) & 0xFFFF0000u;
@@ -279,12 +284,13 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     } else {
       uint32_t key[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) key[i] = order_key(f[i]);
+      for (int i = 0; i < R; ++i) key[i] = f[i] != f[i] ? 0u : order_key(f[i]);
       for (int j = 0; j < k; ++j) {
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) best = max(best, key[i]);
         best = row_max(best);
+        if (best <= kKeyMinusInf) best = 0u;
         uint32_t who = 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -300,24 +306,13 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
         count += best != 0u ? 1 : 0;
       }
     }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      f[i] = exp_below(f[i] - top);
-      if (!H::exists(lane, i, E)) f[i] = 0.0f;
-      sum += f[i];
-    }
-    sum = row_sum(sum) + nan;                    // a token that takes no part: unused
     const float lse = live ? top + logf(sum) : -INFINITY;
     const float inv = live ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (!live) f[i] = 0.0f;
-      psum[i] = __builtin_fmaf(f[i], inv, psum[i]);
-    }
-    float gate = mine >= 0 ? exp_below(picked - top) : 0.0f;
+    for (int i = 0; i < R; ++i) psum[i] = __builtin_fmaf(e[i], inv, psum[i]);
+    float gate = mine >= 0 ? expf(picked - top) : 0.0f;
     const float total = row_sum(gate);
-    gate = mine < 0 ? 0.0f : (a.renorm ? gate / total + nan : gate * inv);
+    gate = mine < 0 ? 0.0f : odd ? sum : (a.renorm ? gate / total : gate * inv);
     choice[n] = mine;
     found[n] = count;
     if (here && lane < k) {
@@ -335,8 +330,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   // p sums: the wave's four groups, then the waves through LDS
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    psum[i] += __shfl_xor(psum[i], 16, 64);
-    psum[i] += __shfl_xor(psum[i], 32, 64);
+    psum[i] = rows_sum(psum[i]);
     const int e = H::expert(lane, i);
     if ((threadIdx.x & 48) == 0 && H::exists(lane, i, E)) s_p[wave * E + e] = psum[i];
   }
@@ -534,16 +528,15 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     // p as exp(l - lse) over its own sum: lse's rounding, which for large logits
     // is larger than the logits' distances, cancels.  No l exceeds lse, and the
     // largest is within 2 log(experts) of it, so the sum is never lost.
+    const float from = live ? lse : 0.0f;
     float sum = 0.0f, pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      f[i] = exp_below(f[i] - lse);
-      if (!(live && H::exists(lane, i, E))) f[i] = 0.0f;
+      f[i] = exp_term(f[i], from);
       sum += f[i];
       pc = __builtin_fmaf(f[i], c[i], pc);
     }
-    // (lse - lse is NaN where lse is not finite)
-    const float inv = live ? 1.0f / row_sum(sum) + (lse - lse) : 0.0f;
+    const float inv = live ? 1.0f / row_sum(sum) : 0.0f;
     pc = row_sum(pc) * inv;
     const float shift = (live ? z_of * lse : 0.0f) - pc - (a.renorm ? 0.0f : s);
     // the group's row in LDS is one wave's: its accesses stay in order
