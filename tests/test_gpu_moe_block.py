@@ -47,6 +47,27 @@ def test_norm_layer():
     assert (err <= lim).all()
 
 
+def test_broadcast_gradients():
+    """Gradients that arrive broadcast (of a sum over everything, and of one
+    over the rows) equal the same gradients written out."""
+    layer = M.RMSNorm(64, device=DEV)
+    slots = B.ufp4_moe_route(bf(6, 8, seed=3), 2).slots
+    gates = torch.rand((6, 2), device=DEV)
+    for grad in (torch.ones((), dtype=torch.bfloat16, device=DEV).expand(6, 64),
+                 bf(64, seed=4).expand(6, 64), bf(6, 1, seed=5).expand(6, 64)):
+        got = []
+        for dy in (grad, grad.contiguous()):
+            x, r = bf(6, 64, seed=1).requires_grad_(), bf(6, 64, seed=2).requires_grad_()
+            layer.weight.grad = None
+            y, h = layer(x, r)
+            xs = M.dispatch(y, slots)
+            out = M.combine(xs, slots, gates, h)
+            torch.autograd.backward([out, h], [dy, dy])
+            got.append([x.grad, r.grad, layer.weight.grad])
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
 def test_router_and_exchange_layers():
     x, valid = bf(70, 64, seed=5).requires_grad_(), torch.arange(70, device=DEV) < 60
     router = M.MoERouter(64, 12, 3, device=DEV)

@@ -171,6 +171,10 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, cons
   }
 }
 
+// Pieces of one launch: the largest tensor accepted has 2^30, and a piece index
+// plus the grid stays within 32 bits.
+constexpr int64_t kMaxPieces = int64_t(1) << 30;
+
 // Calls launch(table, pieces) for each table that the list fills.
 template <typename F>
 static hipError_t each_table(const ufp4_grad *items, int64_t n_items, F launch) {
@@ -179,7 +183,7 @@ static hipError_t each_table(const ufp4_grad *items, int64_t n_items, F launch) 
   for (int64_t i = 0; i <= n_items; ++i) {
     const int64_t mine = i < n_items ? (items[i].n + kPiece - 1) / kPiece : 0;
     if (g.items > 0 &&
-        (i == n_items || g.items == kGradPerLaunch || pieces + mine > INT32_MAX)) {
+        (i == n_items || g.items == kGradPerLaunch || pieces + mine > kMaxPieces)) {
       g.first[g.items] = (int32_t)pieces;
       const hipError_t e = launch(g, (int32_t)pieces);
       if (e != hipSuccess) return e;

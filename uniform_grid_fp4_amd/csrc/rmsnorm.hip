@@ -35,10 +35,11 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
                                                    true);
 }
 
-// Rows held in registers: TPR threads (one wave or a workgroup of four) hold a
-// row as NV vectors each, so x and the residual are read once and everything
+// Rows held in registers: TPR threads (one wave, or a workgroup) hold a row as
+// NV vectors each, so x and the residual are read once and everything
 // else happens in registers.  TAIL: the row length is not a multiple of the
 // vector.
+constexpr int group_size(int tpr) { return tpr < 256 ? 256 : tpr; }
 template <int NV, typename T, bool TAIL>
 struct RowVecs {
   static constexpr int V = Elem<T>::V;
@@ -98,10 +99,10 @@ struct WeightVec<uint16_t, uint16_t, TAIL> {
 };
 
 template <typename T, typename W, int TPR, int NV, bool TAIL>
-__global__ __launch_bounds__(256) void rmsnorm_kernel(const NormArgs a) {
-  constexpr int V = Elem<T>::V, ROWS = 256 / TPR, WAVES = TPR / 64, STEP = TPR * V;
-  __shared__ float s_sum[2][4];
-  __shared__ uint32_t s_max[2][4];
+__global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs a) {
+  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, WAVES = TPR / 64, STEP = TPR * V;
+  __shared__ float s_sum[2][WAVES];
+  __shared__ uint32_t s_max[2][WAVES];
   const int cols = (int)a.cols;
   const int first = (threadIdx.x % TPR) * V;
   WeightVec<T, W, TAIL> w[NV];
@@ -252,9 +253,9 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
 // rows) and goes to partial[workgroup][cols] at the end, the four waves of a
 // wave-per-row workgroup added in wave order.
 template <typename T, typename W, int TPR, int NV, bool TAIL>
-__global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  constexpr int V = Elem<T>::V, ROWS = 256 / TPR, WAVES = TPR / 64, STEP = TPR * V;
-  __shared__ float s_sum[2][4];
+__global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, WAVES = TPR / 64, STEP = TPR * V;
+  __shared__ float s_sum[2][WAVES];
   const int cols = (int)a.cols;
   const int first = (threadIdx.x % TPR) * V;
   WeightVec<T, W, TAIL> w[NV];
@@ -416,9 +417,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_final_kernel(const NormBwdArg
 // A launch holds fewer than 2^32 threads; rows beyond the grid are looped over.
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
 
-// Threads per row and vectors per thread for a row of so many vectors: a wave
-// takes up to 4 vectors per lane, longer rows a workgroup, up to 8 vectors per
-// thread; (0, 0) beyond (the looping kernels).
+// Threads per row and vectors per thread for a row of so many 16-byte vectors
+// of v elements: a wave takes up to 4 vectors per lane, longer rows a workgroup
+// of 256 to 1024 threads with up to 4 each; (0, 0) beyond (the looping kernels).
+// 1024 threads leave 128 registers each, too few for bf16's backward.
 struct RowShape {
   int tpr, nv;
 };
@@ -430,27 +432,30 @@ static RowShape row_shape(int64_t cols, int v) {
   if (n <= 512) return {256, 2};
   if (n <= 768) return {256, 3};
   if (n <= 1024) return {256, 4};
-  if (n <= 1536) return {256, 6};
-  if (n <= 2048) return {256, 8};
+  if (n <= 1536) return {512, 3};
+  if (n <= 2048) return {512, 4};
+  if (n <= 3072 && v == Elem<float>::V) return {1024, 3};
   return {0, 0};
 }
-// Workgroups of the backward pass.  Each writes a row of partial sums, so more
-// of them cost traffic and a longer second half; fewer leave the memory idle
-// (16384 x 6144 bf16: 256 workgroups 168 us, 512 160 us, 1024 175 us; 8192 x
-// 2048: 34, 28 and 30 us).
-constexpr int kNormBwdGrid = 512;
 // The backward pass also keeps dw's sums: four vectors per lane would leave one
 // wave per SIMD (8192 x 2048 bf16: 40 us, a workgroup per row 30 us).
 static RowShape bwd_shape(int64_t cols, int v) {
   const int64_t n = (cols + v - 1) / v;
   return n > 128 && n <= 256 ? RowShape{256, 1} : row_shape(cols, v);
 }
-static int64_t row_groups(int64_t rows, int tpr) { return (rows * tpr + 255) / 256; }
+// Workgroups of the backward pass.  Each writes a row of partial sums, so more
+// of them cost traffic and a longer second half; fewer leave the memory idle
+// (16384 x 6144 bf16: 256 workgroups 168 us, 512 160 us, 1024 175 us; 8192 x
+// 2048: 34, 28 and 30 us).
+constexpr int kNormBwdGrid = 512;
+static int64_t row_groups(int64_t rows, int tpr) {
+  const int per = group_size(tpr) / tpr;
+  return (rows + per - 1) / per;
+}
 
-#define UFP4_FWD_SHAPES(F) \
-  F(64, 1) F(64, 2) F(64, 4) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
-#define UFP4_BWD_SHAPES(F) \
-  F(64, 1) F(64, 2) F(256, 1) F(256, 2) F(256, 3) F(256, 4) F(256, 6) F(256, 8)
+#define UFP4_LONG_SHAPES(F) F(256, 2) F(256, 3) F(256, 4) F(512, 3) F(512, 4)
+#define UFP4_FWD_SHAPES(F) F(64, 1) F(64, 2) F(64, 4) UFP4_LONG_SHAPES(F)
+#define UFP4_BWD_SHAPES(F) F(64, 1) F(64, 2) F(256, 1) UFP4_LONG_SHAPES(F)
 
 template <typename T, typename W, bool TAIL>
 static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
@@ -458,10 +463,14 @@ static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
   const dim3 grid(row_grid(groups));
 #define UFP4_NORM(TPR, NV)                                                                   \
   if (s.tpr == TPR && s.nv == NV) {                                                          \
-    hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, NV, TAIL>), grid, dim3(256), 0, st, a);    \
+    hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, NV, TAIL>), grid, dim3(group_size(TPR)),   \
+                       0, st, a);                                                            \
     return hipGetLastError();                                                                \
   }
   UFP4_FWD_SHAPES(UFP4_NORM)
+  if constexpr (sizeof(T) == 4) {
+    UFP4_NORM(1024, 3)
+  }
 #undef UFP4_NORM
   return hipErrorInvalidValue;
 }
@@ -502,11 +511,14 @@ template <typename T, typename W, bool TAIL>
 static hipError_t norm_bwd_rows(const NormBwdArgs &a, RowShape s, int slices, hipStream_t st) {
 #define UFP4_NORM(TPR, NV)                                                                   \
   if (s.tpr == TPR && s.nv == NV) {                                                          \
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, W, TPR, NV, TAIL>), dim3(slices), dim3(256), 0, \
-                       st, a);                                                               \
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, W, TPR, NV, TAIL>), dim3(slices),              \
+                       dim3(group_size(TPR)), 0, st, a);                                     \
     return hipGetLastError();                                                                \
   }
   UFP4_BWD_SHAPES(UFP4_NORM)
+  if constexpr (sizeof(T) == 4) {
+    UFP4_NORM(1024, 3)
+  }
 #undef UFP4_NORM
   return hipErrorInvalidValue;
 }

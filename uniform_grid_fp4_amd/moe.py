@@ -22,8 +22,10 @@ from .layers import UFP4ExpertLinear
 
 
 def _flat(t: torch.Tensor) -> torch.Tensor:
+    """t as rows with unit column stride that do not overlap (a broadcast
+    tensor, such as the gradient of a sum, is written out)."""
     t = t.reshape(-1, t.shape[-1])
-    return t if t.stride(-1) == 1 else t.contiguous()
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
 
 
 class _NormFn(torch.autograd.Function):
