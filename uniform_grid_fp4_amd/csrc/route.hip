@@ -17,8 +17,12 @@
 
 namespace ufp4 {
 
-constexpr int kGroups = 16;                      // tokens in flight per workgroup
-constexpr int kPer = kRouteTokens / kGroups;     // tokens per group of 16 lanes
+constexpr int kBwdGroups = 16;                   // tokens in flight, backward
+// Threads of the forward kernel: with 1024 each group of 16 lanes has one token
+// and the latencies of the choices run side by side (16384 x 64: 7.5 us, with
+// 256 threads 11.4 us); the registers of long rows allow 256 and four tokens in
+// turn.  A single workgroup with few tokens has no use for more than 256.
+constexpr int route_threads(int r, bool alone) { return alone || r > 16 ? 256 : 1024; }
 
 // Workspace of a call with nblk workgroups, E experts:
 //   uint32 base [E + 1][nblk]  choices per expert (last: choices that do not
@@ -169,9 +173,12 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, double balance,
 }
 
 // Choices, gates and, for the workgroup's 64 tokens, places and counts; with
-// ALONE (one workgroup) everything else too.  Dynamic LDS: 28 bytes per expert.
+// ALONE (one workgroup) everything else too.  Dynamic LDS: 12 bytes per expert and 4 for each wave.
 template <typename T, int R, bool FULL, bool ALONE>
-__global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const RouteWs ws) {
+__global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const RouteArgs a,
+                                                                       const RouteWs ws) {
+  constexpr int kThreads = route_threads(R, ALONE), kWaves = kThreads / 64;
+  constexpr int kGroups = kThreads / 16, kPer = kRouteTokens / kGroups;   // tokens per group
   extern __shared__ __align__(16) char s_dyn[];
   __shared__ uint32_t s_scan[4];
   __shared__ uint32_t s_lost[kRouteTokens], s_live[kRouteTokens];
@@ -180,10 +187,10 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
   const int E = FULL ? 16 * R : a.n_experts, k = a.k;
   using H = Hold<T, R, FULL>;
   unsigned long long *s_mask = reinterpret_cast<unsigned long long *>(s_dyn);
-  float *s_p = reinterpret_cast<float *>(s_dyn + 8 * E);
-  uint32_t *s_off = reinterpret_cast<uint32_t *>(s_dyn + 24 * E);
+  uint32_t *s_off = reinterpret_cast<uint32_t *>(s_dyn + 8 * E);
+  float *s_p = reinterpret_cast<float *>(s_dyn + 12 * E);         // [kWaves][E]
   const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < E; e += 256) s_mask[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) s_mask[e] = 0;
   float psum[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) psum[i] = 0.0f;
@@ -199,10 +206,6 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     }
     return live;
   };
-  // the next token's loads run under this one's work where registers allow
-  constexpr bool kAhead = R <= 16 && !ALONE;
-  float ahead[kAhead ? R : 1];
-  bool ahead_live = false;
   int32_t choice[kPer], found[kPer];             // lane j: the token's j-th choice
 #pragma unroll
   for (int n = 0; n < kPer; ++n) {
@@ -220,16 +223,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     }
     const bool here = t < a.tokens;
     float f[R];
-    bool live;
-    if constexpr (kAhead) {
-      if (n == 0) ahead_live = fetch(t, ahead);
-      live = ahead_live;
-#pragma unroll
-      for (int i = 0; i < R; ++i) f[i] = ahead[i];
-      if (n + 1 < kPer) ahead_live = fetch(t + kGroups, ahead);
-    } else {
-      live = fetch(t, f);
-    }
+    bool live = fetch(t, f);
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R; ++i) top = fmaxf(top, f[i]);
@@ -347,9 +341,11 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, const Rou
     z = lanes_sum((double)s_lse[threadIdx.x] * (double)s_lse[threadIdx.x]);
   }
   double balance = 0.0;
-  for (int e = threadIdx.x; e < E; e += 256) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
     const uint32_t c = (uint32_t)__popcll(s_mask[e]);
-    const float p = ((s_p[e] + s_p[E + e]) + s_p[2 * E + e]) + s_p[3 * E + e];
+    float p = s_p[e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) p += s_p[w * E + e];
     if (ALONE) {
       s_off[e] = c;
       a.counts[e] = (int64_t)c;
@@ -503,8 +499,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
     c[i] = H::exists(lane, i, E) ? c_of * (float)a.counts[e] : 0.0f;
   }
   __syncthreads();
-  for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < nblk * kGroups;
-       t += (int64_t)gridDim.x * kGroups) {
+  for (int64_t t = (int64_t)blockIdx.x * kBwdGroups + group; t < nblk * kBwdGroups;
+       t += (int64_t)gridDim.x * kBwdGroups) {
     const bool here = t < a.tokens;
     const float lse = here ? a.lse[t] : -INFINITY;
     const bool live = lse != -INFINITY;
@@ -568,18 +564,22 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, int64
   }
 }
 
+static size_t route_lds(int r, bool alone, int n_experts) {
+  return (size_t)(12 + route_threads(r, alone) / 64 * 4) * (size_t)n_experts;
+}
+
 template <typename T, int R, bool FULL>
 static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   const int64_t nblk = route_blocks(a.tokens);
   RouteWs ws{};
   if (nblk > 1) route_layout(nblk, a.n_experts, a.workspace, &ws);
-  const size_t lds = 28u * (size_t)a.n_experts;
-  if (nblk == 1) {
-    hipLaunchKernelGGL((route_kernel<T, R, FULL, true>), dim3(1), dim3(256), lds, st, a, ws);
+    if (nblk == 1) {
+    hipLaunchKernelGGL((route_kernel<T, R, FULL, true>), dim3(1),
+                       dim3(route_threads(R, true)), route_lds(R, true, a.n_experts), st, a, ws);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((route_kernel<T, R, FULL, false>), dim3((unsigned)nblk), dim3(256), lds, st, a,
-                     ws);
+  hipLaunchKernelGGL((route_kernel<T, R, FULL, false>), dim3((unsigned)nblk),
+                     dim3(route_threads(R, false)), route_lds(R, false, a.n_experts), st, a, ws);
   hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)(a.n_experts + 2)), dim3(64), 0, st, a, ws,
                      (int)nblk);
   hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)nblk), dim3(256), 0, st, a, ws);
@@ -589,10 +589,10 @@ static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
 template <typename T, int R, bool FULL>
 static hipError_t route_back(const RouteArgs &a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
-  const int64_t nblk = (a.tokens + kGroups - 1) / kGroups;
+  const int64_t nblk = (a.tokens + kBwdGroups - 1) / kBwdGroups;
   const unsigned grid = (unsigned)(nblk < 2048 ? nblk : 2048);
   hipLaunchKernelGGL((route_bwd_kernel<T, R, FULL>), dim3(grid), dim3(256),
-                     (size_t)kGroups * 4u * (size_t)a.n_experts, st, a, nblk);
+                     (size_t)kBwdGroups * 4u * (size_t)a.n_experts, st, a, nblk);
   return hipGetLastError();
 }
 
