@@ -1,7 +1,13 @@
 // Token exchange with expert order (gfx950): dispatch, combine and their
 // backward passes.  A token's k choices hold the rows given by its slots
 // (negative: ~row is a row without a choice).  All four move whole rows and
-// compute next to nothing: they are bound by memory.
+// compute next to nothing: they are bound by memory.  Each row is read or
+// written once, by threads that hold one 16-byte vector of a token's row and go
+// over its choices, so the token's own row is read once whatever k is, and the
+// sums (FP32, in the order of the choices) need no atomics.  16384 tokens, 6144
+// columns, k = 8, bf16, from HBM: dispatch 366 us (1.81 GB, 4.9 TB/s; 309 us with
+// x in the cache), combine with residual 363 us (2.01 GB, 5.5 TB/s), dispatch's
+// backward 305 us (1.81 GB, 5.9 TB/s), combine's 650 us (3.42 GB, 5.3 TB/s).
 #include "block_device.h"
 #include "block_kernels.h"
 

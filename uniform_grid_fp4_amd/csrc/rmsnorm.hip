@@ -3,6 +3,11 @@
 //   h = round(x + r),  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd w
 //   dx = rstd (g - xhat mean(g xhat)) + dh,  g = dy w,  xhat = h rstd
 //   dw = sum over rows of dy xhat
+// About 12 operations per element forward and 16 backward against 6 to 10
+// bytes: bound by memory.  Sums are FP32 along a row (a lane's chain is a 64th
+// of it or less) and over the rows of dw; h is rounded once to the stream's
+// type, and the statistics are those of the rounded h that the backward sees;
+// y, q and the gradients are rounded once from FP32.
 #include "block_device.h"
 #include "block_kernels.h"
 
@@ -38,7 +43,13 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
 // Rows held in registers: TPR threads (one wave, or a workgroup) hold a row as
 // NV vectors each, so x and the residual are read once and everything
 // else happens in registers.  TAIL: the row length is not a multiple of the
-// vector.
+// vector.  A row per workgroup at a time, with the hardware starting the next
+// workgroup as one ends: a grid that fills the GPU once and walks over rows with
+// the next row's loads in flight took 350 us where this takes 317 us (32768 x
+// 6144 bf16 with residual and E4M3), 305 us with streaming stores: 1.81 GB at
+// 5.9 TB/s, the rate that the fastest of these kernels reach; a plain copy of 2 GB
+// reaches 4.9 TB/s here.  8192 x 2048 takes 22-25 us (134 MB, 5.4-6.1 TB/s,
+// partly from the 256 MB cache), one row 3.3 us.
 constexpr int group_size(int tpr) { return tpr < 256 ? 256 : tpr; }
 template <int NV, typename T, bool TAIL>
 struct RowVecs {
@@ -251,7 +262,10 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
 // Backward with rows held in registers as above: dx, and the workgroup's share
 // of dw, which stays in registers over all its rows (in the order of the
 // rows) and goes to partial[workgroup][cols] at the end, the four waves of a
-// wave-per-row workgroup added in wave order.
+// wave-per-row workgroup added in wave order.  Reads dy, h and dh once: 8192 x
+// 2048 bf16 27 us and 4 us for dw's second half (134 MB, 4.3 TB/s); 16384 x
+// 6144 162 us (805 MB, 5.0 TB/s), bound by memory.  Loading the next row ahead
+// changed nothing (the other workgroup of the CU covers the wait).
 template <typename T, typename W, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
   constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, WAVES = TPR / 64, STEP = TPR * V;

@@ -12,6 +12,15 @@
 // independent of the order in which the lanes ran.  A second kernel scans the
 // counts over the workgroups and sums their probabilities, a third turns
 // places into rows.  Few tokens (one workgroup) take a single launch.
+//
+// 65536 x 256 bf16 logits, top 8 (34 MB): choices 28 us, of which the k rounds
+// take 9 us and instruction issue most of the rest (about 600 vector
+// instructions for four tokens), scan 6.7 us, places 5.8 us; backward 17 us for
+// 67 MB (3.9 TB/s).  16384 x 64 FP32, top 6: 7.2, 3.2, 4.2 and 4.8 us, one token
+// 4.6 us: latency and launches.
+//
+// Sums over a row are FP32; sums of p over tokens are FP32 within a workgroup
+// and FP64 across, z and the losses FP64.
 #include "block_device.h"
 #include "block_kernels.h"
 
