@@ -29,15 +29,40 @@ struct Choices {
   }
 };
 
+// Units of work: LPT lanes take LPT vectors of one token's row.  A wave (64) per
+// unit keeps the token, its slots and every branch on them scalar; rows of up to
+// 16 vectors take a DPP row of lanes each, four tokens to a wave (31549 tokens
+// of 64 columns, k = 8, all four directions: 52 us, a workgroup per token 327 us).
+template <int LPT>
+__device__ __forceinline__ int64_t first_unit() {
+  int in = threadIdx.x / LPT;
+  if (LPT >= 64) in = __builtin_amdgcn_readfirstlane(in);
+  return (int64_t)blockIdx.x * (256 / LPT) + in;
+}
+template <int LPT>
+__device__ __forceinline__ int64_t unit_step() {
+  return (int64_t)gridDim.x * (256 / LPT);
+}
+
+// Where a lane's vector starts: the one that passes the end of the row is taken
+// back to end with it, so that no lane goes element by element (24002 tokens of
+// 575 columns, k = 4, all four directions: 149 us, masked accesses 221 us).  Elements that two lanes then hold get the same
+// value from both.  Rows shorter than a vector keep the masked accesses.
+template <int V>
+__device__ __forceinline__ int64_t vec_start(int64_t c, int64_t cols) {
+  return cols >= V ? min(c, cols - V) : c;
+}
+
 // Thread = one vector of one token's row, written to its k rows.
-template <typename T, int KB>
+template <typename T, int KB, int LPT>
 __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int64_t chunks) {
   constexpr int V = Elem<T>::V;
   const int64_t rows = a.tokens * a.k;
-  for (int64_t b = blockIdx.x; b < a.tokens * chunks; b += gridDim.x) {
-    const int64_t t = b / chunks;
-    const int64_t c = ((b - t * chunks) * 256 + threadIdx.x) * V;
+  for (int64_t u = first_unit<LPT>(); u < a.tokens * chunks; u += unit_step<LPT>()) {
+    const int64_t t = u / chunks;
+    int64_t c = ((u - t * chunks) * LPT + threadIdx.x % LPT) * V;
     if (c >= a.cols) continue;
+    c = vec_start<V>(c, a.cols);
     const u32x4 v = load_vec(static_cast<const T *>(a.in) + t * a.ld_in + c, a.cols - c);
     for (int j0 = 0; j0 < a.k; j0 += KB) {
       const Choices<KB> ch(a, t, j0);
@@ -54,14 +79,15 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const ExchangeArgs a, int
 
 // Thread = one vector of one token's row: the (weighted) sum of its k rows,
 // KB of them in flight at once.
-template <typename T, bool GATED, int KB>
+template <typename T, bool GATED, int KB, int LPT>
 __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int64_t chunks) {
   constexpr int V = Elem<T>::V;
   const int64_t rows = a.tokens * a.k;
-  for (int64_t b = blockIdx.x; b < a.tokens * chunks; b += gridDim.x) {
-    const int64_t t = b / chunks;
-    const int64_t c = ((b - t * chunks) * 256 + threadIdx.x) * V;
+  for (int64_t u = first_unit<LPT>(); u < a.tokens * chunks; u += unit_step<LPT>()) {
+    const int64_t t = u / chunks;
+    int64_t c = ((u - t * chunks) * LPT + threadIdx.x % LPT) * V;
     if (c >= a.cols) continue;
+    c = vec_start<V>(c, a.cols);
     const T *in = static_cast<const T *>(a.in) + c;
     float sum[V];
 #pragma unroll
@@ -100,15 +126,19 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
   }
 }
 
-// One workgroup per token at a time: dys = g dy in each choice's row, and the
-// dot products of its row of ys with dy, which is read once per KB choices.
-template <typename T, int KB>
+// LPT lanes per token at a time, LPT vectors of its row after the other: dys =
+// g dy in each choice's row, and the dot products of its row of ys with dy,
+// which is read once per KB choices.  Up to 192 vectors a wave does it without a
+// barrier (1408 columns, k = 6: 140 us, a workgroup 147 us); longer rows take a
+// workgroup (2048 columns: 163 us, a wave 187 us).
+template <typename T, int KB, int LPT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) {
   constexpr int V = Elem<T>::V;
   __shared__ float s_dot[2][KB][4];
   const int64_t rows = a.tokens * a.k;
+  const int lane = threadIdx.x % LPT;
   int turn = 0;
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+  for (int64_t t = first_unit<LPT>(); t < a.tokens; t += unit_step<LPT>()) {
     const T *dy = static_cast<const T *>(a.dy) + t * a.ld_dy;
     for (int j0 = 0; j0 < a.k; j0 += KB, turn ^= 1) {
       const Choices<KB> ch(a, t, j0);
@@ -118,7 +148,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
         dot[j] = 0.0f;
         g[j] = ch.slot[j] >= 0 ? a.gates[t * a.k + j0 + j] : 0.0f;
       }
-      for (int64_t c = threadIdx.x * V; c < a.cols; c += 256 * V) {
+      for (int64_t c0 = lane * V; c0 < a.cols; c0 += LPT * V) {
+        const int64_t c = vec_start<V>(c0, a.cols);
         float d[V];
         u32x4 v[KB];
         const u32x4 vd = load_vec(dy + c, a.cols - c);
@@ -139,7 +170,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
             Elem<T>::unpack(v[j], f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              dot[j] = __builtin_fmaf(f[i], d[i], dot[j]);
+              dot[j] = c + i >= c0 ? __builtin_fmaf(f[i], d[i], dot[j]) : dot[j];
               f[i] = d[i] * g[j];
             }
           } else {
@@ -150,15 +181,25 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) 
                    a.stream);
         }
       }
+      if constexpr (LPT == 256) {
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        dot[j] = lanes_sum(dot[j]);
-        if ((threadIdx.x & 63) == 0) s_dot[turn][j][threadIdx.x >> 6] = dot[j];
-      }
-      __syncthreads();
-      if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < a.k) {
-        const float *s = s_dot[turn][threadIdx.x];
-        a.d_gates[t * a.k + j0 + threadIdx.x] = ((s[0] + s[1]) + s[2]) + s[3];
+        for (int j = 0; j < KB; ++j) {
+          dot[j] = lanes_sum(dot[j]);
+          if ((threadIdx.x & 63) == 0) s_dot[turn][j][threadIdx.x >> 6] = dot[j];
+        }
+        __syncthreads();
+        if (lane < KB && j0 + lane < a.k) {
+          const float *s = s_dot[turn][lane];
+          a.d_gates[t * a.k + j0 + lane] = ((s[0] + s[1]) + s[2]) + s[3];
+        }
+      } else {
+        float mine = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const float sum = LPT == 64 ? lanes_sum(dot[j]) : row_sum(dot[j]);
+          mine = lane == j ? sum : mine;
+        }
+        if (lane < KB && j0 + lane < a.k) a.d_gates[t * a.k + j0 + lane] = mine;
       }
     }
   }
@@ -169,19 +210,33 @@ static unsigned grid_of(int64_t blocks) {
   return (unsigned)(blocks < (1 << 23) ? blocks : (1 << 23));
 }
 
+template <typename T, int KB, int LPT>
+static hipError_t exchange_units(const ExchangeArgs &a, int what, hipStream_t st) {
+  constexpr int64_t kUnits = 256 / LPT;
+  const int64_t per = LPT * Elem<T>::V, chunks = (a.cols + per - 1) / per;
+  const dim3 grid(grid_of((a.tokens * chunks + kUnits - 1) / kUnits)), block(256);
+  if (what == 0)
+    hipLaunchKernelGGL((dispatch_kernel<T, KB, LPT>), grid, block, 0, st, a, chunks);
+  else if (what == 1)
+    hipLaunchKernelGGL((combine_kernel<T, false, KB, LPT>), grid, block, 0, st, a, chunks);
+  else if (what == 2)
+    hipLaunchKernelGGL((combine_kernel<T, true, KB, LPT>), grid, block, 0, st, a, chunks);
+  else
+    hipLaunchKernelGGL((combine_bwd_kernel<T, KB, LPT>),
+                       dim3(grid_of((a.tokens + kUnits - 1) / kUnits)), block, 0, st, a);
+  return hipGetLastError();
+}
+
 template <typename T, int KB>
 static hipError_t exchange_of(const ExchangeArgs &a, int what, hipStream_t st) {
-  const int64_t per = 256 * Elem<T>::V, chunks = (a.cols + per - 1) / per;
-  const dim3 grid(grid_of(a.tokens * chunks)), block(256);
-  if (what == 0)
-    hipLaunchKernelGGL((dispatch_kernel<T, KB>), grid, block, 0, st, a, chunks);
-  else if (what == 1)
-    hipLaunchKernelGGL((combine_kernel<T, false, KB>), grid, block, 0, st, a, chunks);
-  else if (what == 2)
-    hipLaunchKernelGGL((combine_kernel<T, true, KB>), grid, block, 0, st, a, chunks);
-  else
-    hipLaunchKernelGGL((combine_bwd_kernel<T, KB>), dim3(grid_of(a.tokens)), block, 0, st, a);
-  return hipGetLastError();
+  const int64_t vecs = (a.cols + Elem<T>::V - 1) / Elem<T>::V;
+  if (vecs <= 16) return exchange_units<T, KB, 16>(a, what, st);
+  if (what == 3 && vecs > 192) {
+    hipLaunchKernelGGL((combine_bwd_kernel<T, KB, 256>), dim3(grid_of(a.tokens)), dim3(256), 0, st,
+                       a);
+    return hipGetLastError();
+  }
+  return exchange_units<T, KB, 64>(a, what, st);
 }
 
 // Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds k.

@@ -40,8 +40,8 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
                                                    true);
 }
 
-// Rows held in registers: TPR threads (one wave, or a workgroup) hold a row as
-// NV vectors each, so x and the residual are read once and everything
+// Rows held in registers: TPR threads (16 lanes, a wave, or a workgroup) hold a
+// row as NV vectors each, so x and the residual are read once and everything
 // else happens in registers.  TAIL: the row length is not a multiple of the
 // vector.  A row per workgroup at a time, with the hardware starting the next
 // workgroup as one ends: a grid that fills the GPU once and walks over rows with
@@ -50,6 +50,19 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
 // 5.9 TB/s, the rate that the fastest of these kernels reach; a plain copy of 2 GB
 // reaches 4.9 TB/s here.  8192 x 2048 takes 22-25 us (134 MB, 5.4-6.1 TB/s,
 // partly from the 256 MB cache), one row 3.3 us.
+// Sum / maximum over the TPR threads that hold a row: a DPP row, a wave, or the
+// workgroup.
+template <int TPR>
+__device__ __forceinline__ float span_sum(float v, float *s) {
+  if constexpr (TPR == 16) return row_sum(v);
+  else return group_sum<TPR / 64>(v, s);
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t span_max(uint32_t v, uint32_t *s) {
+  if constexpr (TPR == 16) return row_max(v);
+  else return group_max<TPR / 64>(v, s);
+}
+
 constexpr int group_size(int tpr) { return tpr < 256 ? 256 : tpr; }
 template <int NV, typename T, bool TAIL>
 struct RowVecs {
@@ -111,9 +124,9 @@ struct WeightVec<uint16_t, uint16_t, TAIL> {
 
 template <typename T, typename W, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs a) {
-  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, WAVES = TPR / 64, STEP = TPR * V;
-  __shared__ float s_sum[2][WAVES];
-  __shared__ uint32_t s_max[2][WAVES];
+  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, STEP = TPR * V;
+  __shared__ float s_sum[2][16];
+  __shared__ uint32_t s_max[2][16];
   const int cols = (int)a.cols;
   const int first = (threadIdx.x % TPR) * V;
   WeightVec<T, W, TAIL> w[NV];
@@ -122,8 +135,7 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
-  // with one wave per row the waves leave the loop on their own; with four,
-  // all four have the same row
+  // 16 lanes or a wave leave the loop on their own; a workgroup has one row
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
     RowVecs<NV, T, TAIL> h, r0;
     h.load(x + row * a.ld_x, first, STEP, cols);
@@ -146,7 +158,7 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
 #pragma unroll
       for (int j = 0; j < V; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
     }
-    sum = group_sum<WAVES>(sum, s_sum[turn]);
+    sum = span_sum<TPR>(sum, s_sum[turn]);
     const float rstd = 1.0f / sqrtf(sum / (float)cols + a.eps);
     if (first == 0) a.rstd[row] = rstd;
     uint32_t top = 0;
@@ -165,7 +177,7 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
                            Elem<T>::pack(f), a.stream);
     }
     if (a.q == nullptr) continue;
-    top = group_max<WAVES>(top, s_max[turn]);
+    top = span_max<TPR>(top, s_max[turn]);
     const RowScale s = row_scale(top);
     if (first == 0) a.scale[row] = s.scale;
     uint8_t *q = a.q + row * a.cols;
@@ -268,8 +280,8 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
 // changed nothing (the other workgroup of the CU covers the wait).
 template <typename T, typename W, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, WAVES = TPR / 64, STEP = TPR * V;
-  __shared__ float s_sum[2][WAVES];
+  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, STEP = TPR * V;
+  __shared__ float s_sum[2][16];
   const int cols = (int)a.cols;
   const int first = (threadIdx.x % TPR) * V;
   WeightVec<T, W, TAIL> w[NV];
@@ -304,7 +316,7 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
         sum = __builtin_fmaf(g[j] * wf[j], f[j], sum);
       }
     }
-    const float mean = group_sum<WAVES>(sum, s_sum[turn]) / (float)cols;
+    const float mean = span_sum<TPR>(sum, s_sum[turn]) / (float)cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[V], g[V], wf[V];
@@ -333,7 +345,7 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
       }
     return;
   }
-  __shared__ float s_acc[ROWS == 1 ? 1 : ROWS][64 * V + 1];
+  __shared__ float s_acc[ROWS][STEP + 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     __syncthreads();
@@ -432,7 +444,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_final_kernel(const NormBwdArg
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
 
 // Threads per row and vectors per thread for a row of so many 16-byte vectors
-// of v elements: a wave takes up to 4 vectors per lane, longer rows a workgroup
+// of v elements: 16 lanes take up to 16, a wave up to 4 per lane, longer rows a workgroup
 // of 256 to 1024 threads with up to 4 each; (0, 0) beyond (the looping kernels).
 // 1024 threads leave 128 registers each, too few for bf16's backward.
 struct RowShape {
@@ -440,6 +452,7 @@ struct RowShape {
 };
 static RowShape row_shape(int64_t cols, int v) {
   const int64_t n = (cols + v - 1) / v;
+  if (n <= 16) return {16, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
   if (n <= 256) return {64, 4};
@@ -468,8 +481,8 @@ static int64_t row_groups(int64_t rows, int tpr) {
 }
 
 #define UFP4_LONG_SHAPES(F) F(256, 2) F(256, 3) F(256, 4) F(512, 3) F(512, 4)
-#define UFP4_FWD_SHAPES(F) F(64, 1) F(64, 2) F(64, 4) UFP4_LONG_SHAPES(F)
-#define UFP4_BWD_SHAPES(F) F(64, 1) F(64, 2) F(256, 1) UFP4_LONG_SHAPES(F)
+#define UFP4_FWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(64, 4) UFP4_LONG_SHAPES(F)
+#define UFP4_BWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(256, 1) UFP4_LONG_SHAPES(F)
 
 template <typename T, typename W, bool TAIL>
 static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
