@@ -78,7 +78,8 @@ def check_forward(x, w, res, q8=True, out_h=None):
 
 SHAPES = [(1, 1), (1, 2048), (3, 7), (2, 8), (5, 63), (4, 64), (3, 65), (7, 511), (2, 1024),
           (33, 1411), (3, 2049), (2, 4104), (2, 6144), (3, 8192), (2, 12289), (2, 16384),
-          (1, 40000), (300, 96), (600, 5000), (530, 9000), (3, 11000)]
+          (1, 40000), (300, 96), (600, 5000), (530, 9000), (3, 11000), (700, 15),
+          (1500, 121), (600, 2047), (520, 6143)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -124,6 +125,31 @@ def test_residual_stream_in_place():
             assert got.h.data_ptr() == (x, res)[which].data_ptr()
             for u, v in zip(want, got):
                 assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+
+
+@pytest.mark.parametrize("cols", [5, 127, 1003, 2047, 6143, 9001, 17001])
+def test_in_place_where_lanes_share_elements(cols):
+    """Rows that end inside a vector, updated in place: the forward's h into x or
+    the residual, and (through the C call) dx into dy or dh."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for which in (0, 1):
+            x, res, w, dy, dh = inputs(40, cols, dtype, dtype, cols)
+            want = B.ufp4_rmsnorm(x, w, res, q8=True)
+            got = B.ufp4_rmsnorm(x, w, res, q8=True, out_h=(x, res)[which])
+            for u, v in zip(want, got):
+                assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+            dx, dw = B.ufp4_rmsnorm_bwd(dy, want.h, w, want.rstd, dh)
+            dw2 = torch.empty_like(dw)
+            n = B.ufp4_rmsnorm_bwd_workspace_size(40, cols)
+            ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+            code = B._CODE[dtype]
+            into = (dy, dh)[which]
+            st = B.lib().ufp4_rmsnorm_bwd(dy.data_ptr(), cols, want.h.data_ptr(), cols,
+                                          w.data_ptr(), want.rstd.data_ptr(), dh.data_ptr(), cols,
+                                          code, code, 40, cols, into.data_ptr(), dw2.data_ptr(),
+                                          ws.data_ptr(), n, B._stream(torch.device("cuda:0")))
+            assert st == 0
+            assert torch.equal(into, dx) and torch.equal(dw2, dw)
 
 
 def test_zero_rows_and_zero_inputs():

@@ -64,6 +64,21 @@ __device__ __forceinline__ uint32_t span_max(uint32_t v, uint32_t *s) {
 }
 
 constexpr int group_size(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Where the vector that begins at column c0 lies: with TAIL, one that passes the
+// end of the row is taken back to end with it.  Its first c0 - start elements
+// belong to another lane; they count in no sum, and both lanes store the same
+// values there.  (Masked accesses, element by element in one lane, made the
+// whole row wait: 16384 x 2047 bf16 backward 139 us, this way 55 us.)
+template <bool TAIL, int V>
+__device__ __forceinline__ int vec_start(int c0, int cols) {
+  return TAIL ? min(c0, cols - V) : c0;
+}
+// Whether element j of the vector of c0 is another lane's.
+template <bool TAIL, int V>
+__device__ __forceinline__ bool elsewhere(int c0, int cols, int j) {
+  return TAIL && vec_start<TAIL, V>(c0, cols) + j < c0;
+}
+
 template <int NV, typename T, bool TAIL>
 struct RowVecs {
   static constexpr int V = Elem<T>::V;
@@ -71,18 +86,17 @@ struct RowVecs {
   __device__ __forceinline__ void load(const T *p, int first, int step, int cols) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first + i * step;
-      if (TAIL) {
-        v[i] = c < cols ? load_vec(p + c, cols - c) : u32x4(0);
-      } else {
-        v[i] = c < cols ? *reinterpret_cast<const u32x4_any *>(p + c) : u32x4(0);
-      }
+      const int c0 = first + i * step;
+      v[i] = c0 < cols
+                 ? (u32x4)*reinterpret_cast<const u32x4_any *>(p + vec_start<TAIL, V>(c0, cols))
+                 : u32x4(0);
     }
   }
 };
 template <typename T, bool TAIL>
-__device__ __forceinline__ void row_store(T *p, int c, int cols, u32x4 v, bool stream) {
-  if (c < cols) store_as(p + c, TAIL ? cols - c : Elem<T>::V, v, stream);
+__device__ __forceinline__ void row_store(T *p, int c0, int cols, u32x4 v, bool stream) {
+  constexpr int V = Elem<T>::V;
+  if (c0 < cols) store_as(p + vec_start<TAIL, V>(c0, cols), V, v, stream);
 }
 
 // The weights of one vector's columns: packed as the rows are when the types
@@ -91,16 +105,16 @@ template <typename T, typename W, bool TAIL>
 struct WeightVec {
   static constexpr int V = Elem<T>::V;
   float f[V];
-  __device__ __forceinline__ void load(const W *w, int c, int cols) {
+  __device__ __forceinline__ void load(const W *w, int c0, int cols) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = 0.0f;
-    if (c >= cols) return;
+    if (c0 >= cols) return;
     constexpr int VW = Elem<W>::V;
+    w += vec_start<TAIL, V>(c0, cols);
 #pragma unroll
     for (int i = 0; i < V; i += VW) {
       float g[VW];
-      Elem<W>::unpack(TAIL ? load_vec(w + c + i, cols - c - i)
-                           : (u32x4)*reinterpret_cast<const u32x4_any *>(w + c + i), g);
+      Elem<W>::unpack(*reinterpret_cast<const u32x4_any *>(w + i), g);
 #pragma unroll
       for (int j = 0; j < VW; ++j) f[i + j] = g[j];
     }
@@ -113,11 +127,10 @@ struct WeightVec {
 template <bool TAIL>
 struct WeightVec<uint16_t, uint16_t, TAIL> {
   u32x4 v;
-  __device__ __forceinline__ void load(const uint16_t *w, int c, int cols) {
-    if (TAIL)
-      v = c < cols ? load_vec(w + c, cols - c) : u32x4(0);
-    else
-      v = c < cols ? *reinterpret_cast<const u32x4_any *>(w + c) : u32x4(0);
+  __device__ __forceinline__ void load(const uint16_t *w, int c0, int cols) {
+    v = c0 < cols
+            ? (u32x4)*reinterpret_cast<const u32x4_any *>(w + vec_start<TAIL, 8>(c0, cols))
+            : u32x4(0);
   }
   __device__ __forceinline__ void get(float (&g)[8]) const { Elem<uint16_t>::unpack(v, g); }
 };
@@ -152,11 +165,11 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
         for (int j = 0; j < V; ++j) f[j] += r[j];
         h.v[i] = Elem<T>::pack(f);
         Elem<T>::unpack(h.v[i], f);
-        row_store<T, TAIL>(static_cast<T *>(a.h) + row * a.cols, first + i * STEP, cols, h.v[i],
-                           a.stream);
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
+      for (int j = 0; j < V; ++j)
+        sum = elsewhere<TAIL, V>(first + i * STEP, cols, j) ? sum
+                                                            : __builtin_fmaf(f[j], f[j], sum);
     }
     sum = span_sum<TPR>(sum, s_sum[turn]);
     const float rstd = 1.0f / sqrtf(sum / (float)cols + a.eps);
@@ -165,6 +178,11 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[V], g[V];
+      // only now, when every lane of the row has read its own: h may be x or the
+      // residual, and two lanes may share elements
+      if (res != nullptr)
+        row_store<T, TAIL>(static_cast<T *>(a.h) + row * a.cols, first + i * STEP, cols, h.v[i],
+                           a.stream);
       Elem<T>::unpack(h.v[i], f);
       w[i].get(g);
 #pragma unroll
@@ -188,17 +206,11 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
       w[i].get(g);
 #pragma unroll
       for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * g[j];
-      const int c = first + i * STEP;
+      const int c0 = first + i * STEP;
       uint32_t b[V / 4];
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) b[j] = e4m3x4(f + 4 * j, s);
-      if (!TAIL || c + V <= cols) {
-        if (c < cols) __builtin_memcpy(q + c, b, V);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (c + j < cols) q[c + j] = (uint8_t)(b[j / 4] >> (8 * (j % 4)));
-      }
+      if (c0 < cols) __builtin_memcpy(q + vec_start<TAIL, V>(c0, cols), b, V);
     }
   }
 }
@@ -312,9 +324,16 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         f[j] *= rstd;
+        if (elsewhere<TAIL, V>(first + i * STEP, cols, j)) g[j] = f[j] = 0.0f;
         acc[i][j] = __builtin_fmaf(g[j], f[j], acc[i][j]);
         sum = __builtin_fmaf(g[j] * wf[j], f[j], sum);
       }
+    }
+    // dx may be dy or dh: with shared elements every lane's dh has to be here
+    // before another's dx is stored
+    if (TAIL && dh != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) asm volatile("" ::"v"(vd.v[i]));
     }
     const float mean = span_sum<TPR>(sum, s_sum[turn]) / (float)cols;
 #pragma unroll
@@ -340,8 +359,9 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int c = first + i * STEP + j;
-        if (c < cols) partial[c] = acc[i][j];
+        const int c0 = first + i * STEP;
+        if (c0 < cols && !elsewhere<TAIL, V>(c0, cols, j))
+          partial[vec_start<TAIL, V>(c0, cols) + j] = acc[i][j];
       }
     return;
   }
@@ -350,7 +370,11 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
   for (int i = 0; i < NV; ++i) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_acc[threadIdx.x / TPR][first + j] = acc[i][j];
+    for (int j = 0; j < V; ++j) {
+      const int c0 = first + i * STEP;
+      if (c0 < cols && !elsewhere<TAIL, V>(c0, cols, j))
+        s_acc[threadIdx.x / TPR][vec_start<TAIL, V>(c0, cols) + j - i * STEP] = acc[i][j];
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < STEP && i * STEP + c < cols; c += 256) {
       float t = s_acc[0][c];
@@ -445,12 +469,14 @@ static unsigned row_grid(int64_t rows) { return (unsigned)(rows < (1 << 20) ? ro
 
 // Threads per row and vectors per thread for a row of so many 16-byte vectors
 // of v elements: 16 lanes take up to 16, a wave up to 4 per lane, longer rows a workgroup
-// of 256 to 1024 threads with up to 4 each; (0, 0) beyond (the looping kernels).
+// of 256 to 1024 threads with up to 4 each; (0, 0) beyond, and for less than a vector (the looping
+// kernels).
 // 1024 threads leave 128 registers each, too few for bf16's backward.
 struct RowShape {
   int tpr, nv;
 };
 static RowShape row_shape(int64_t cols, int v) {
+  if (cols < v) return {0, 0};
   const int64_t n = (cols + v - 1) / v;
   if (n <= 16) return {16, 1};
   if (n <= 64) return {64, 1};
