@@ -82,7 +82,8 @@ def route(bwd=False, r=None, **kw):
     a = dict(x=A, ld=64, dt=F32, valid=None, t=8, e=64, k=4, renorm=1, ws=A, n=1 << 20, dg=None,
              dl=None, out=A)
     a.update(kw)
-    ref = ctypes.byref(r if r is not None else routing())
+    r = r if r is not None else routing()
+    ref = ctypes.addressof(r)
     if bwd:
         return B.lib().ufp4_moe_route_bwd(a["x"], a["ld"], a["dt"], a["t"], a["e"], a["k"],
                                           a["renorm"], ref, a["dg"], a["dl"], a["out"], None)

@@ -54,7 +54,7 @@ def lib() -> ctypes.CDLL:
         return _lib
     L = U.lib()
     P, I64, I32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    R, G = ctypes.POINTER(RoutingDesc), ctypes.c_void_p
+    R, G = ctypes.c_void_p, ctypes.c_void_p
     L.ufp4_rmsnorm.argtypes = [P, I64, P, I64, P, I32, I32, I64, I64, ctypes.c_float, P, P, P, P,
                                P, P]
     L.ufp4_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, P, I64, I32, I32, I64, I64, P, P, P, S, P]
@@ -123,6 +123,12 @@ def _weight(w: torch.Tensor, x: torch.Tensor) -> int:
     return _CODE[w.dtype]
 
 
+def _new(like: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of that shape and type (empty_like is the cheapest
+    allocation, but keeps strides)."""
+    return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -166,11 +172,11 @@ def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     ldr, h = 0, x
     if residual is not None:
         ldr = _rows2d(residual, "residual", x)
-        h = x.new_empty((rows, cols)) if out_h is None else \
+        h = _new(x) if out_h is None else \
             _exact(out_h, "out_h", x.dtype, (rows, cols), dev)
     elif out_h is not None:
         raise ValueError("out_h is given without a residual")
-    out = x.new_empty((rows, cols)) if y else None
+    out = _new(x) if y else None
     q = scale = None
     if q8:
         q = torch.empty((rows, cols), dtype=E4M3, device=dev)
@@ -202,7 +208,7 @@ def ufp4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     rows, cols = h.shape
     dev = h.device
     _exact(rstd, "rstd", torch.float32, (rows,), dev)
-    dx, dw = h.new_empty((rows, cols)), weight.new_empty((cols,))
+    dx, dw = _new(h), torch.empty_like(weight)
     ws, nbytes = _workspace(workspace, lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols), dev)
     st = lib().ufp4_rmsnorm_bwd(_p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
                                 _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes,
@@ -236,8 +242,9 @@ class Routing(NamedTuple):
     losses: torch.Tensor       # float32 [2]: balance, z
     renorm: bool
 
-    def desc(self) -> RoutingDesc:
-        return RoutingDesc(*(t.data_ptr() for t in self[:8]))
+    def words(self) -> array:
+        """ufp4_routing: the eight pointers."""
+        return array("Q", map(torch.Tensor.data_ptr, self[:8]))
 
 
 def ufp4_moe_route_workspace_size(tokens: int, n_experts: int) -> int:
@@ -267,9 +274,9 @@ def ufp4_moe_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] =
                 torch.empty((2,), dtype=f32, device=dev), bool(renorm))
     need = lib().ufp4_moe_route_workspace_size(t, e)
     ws, nbytes = (None, 0) if need == 0 else _workspace(workspace, need, dev)
-    d = r.desc()
+    d = r.words()
     st = lib().ufp4_moe_route(_p(logits), ld, _CODE[logits.dtype], _p(valid), t, e, k, int(renorm),
-                              ctypes.byref(d), _p(ws), nbytes, _stream(dev))
+                              d.buffer_info()[0], _p(ws), nbytes, _stream(dev))
     U._check(st, "ufp4_moe_route")
     return r
 
@@ -291,10 +298,10 @@ def ufp4_moe_route_bwd(logits: torch.Tensor, r: Routing, d_gates: Optional[torch
         _exact(d_gates, "d_gates", torch.float32, (t, k), dev)
     if d_losses is not None:
         _exact(d_losses, "d_losses", torch.float32, (2,), dev)
-    out = logits.new_empty((t, e))
-    d = r.desc()
+    out = _new(logits)
+    d = r.words()
     st = lib().ufp4_moe_route_bwd(_p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
-                                  ctypes.byref(d), _p(d_gates), _p(d_losses), _p(out),
+                                  d.buffer_info()[0], _p(d_gates), _p(d_losses), _p(out),
                                   _stream(dev))
     U._check(st, "ufp4_moe_route_bwd")
     return out
@@ -376,7 +383,7 @@ def ufp4_moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
     ldy = _token_rows(dy, "dy", (t, cols), ys)
     _exact(gates, "gates", torch.float32, (t, k), ys.device)
     dys = torch.empty_like(ys)
-    dg = gates.new_empty((t, k))
+    dg = torch.empty_like(gates)
     st = lib().ufp4_moe_combine_bwd(_p(dy), ldy, _p(ys), _p(slots), _p(gates), _CODE[ys.dtype], t,
                                     k, cols, _p(dys), _p(dg), _stream(ys.device))
     U._check(st, "ufp4_moe_combine_bwd")
