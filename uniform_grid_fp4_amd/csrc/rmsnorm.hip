@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
 // of dw, which stays in registers over all its rows (in the order of the
 // rows) and goes to partial[workgroup][cols] at the end, the four waves of a
 // wave-per-row workgroup added in wave order.  Reads dy, h and dh once: 8192 x
-// 2048 bf16 27 us and 4 us for dw's second half (134 MB, 4.3 TB/s); 16384 x
+// 2048 bf16 26 us and 4 us for dw's second half (134 MB, 4.5 TB/s); 16384 x
 // 6144 162 us (805 MB, 5.0 TB/s), bound by memory.  Loading the next row ahead
 // changed nothing (the other workgroup of the CU covers the wait).
 template <typename T, typename W, int TPR, int NV, bool TAIL>
