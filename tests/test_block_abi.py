@@ -45,6 +45,7 @@ def norm(**kw):
     (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1),
     (dict(rows=-1), -2), (dict(cols=0), -2), (dict(ld=63), -2), (dict(ldr=63), -2),
     (dict(cols=(1 << 24) + 1, ld=BIG, ldr=BIG), -2), (dict(rows=(1 << 40) + 1), -2),
+    (dict(rows=1 << 40, cols=1 << 24, ld=BIG, ldr=BIG), -2),   # the product passes 63 bits
     (dict(rows=0, x=None, h=None, rstd=None), 0),          # nothing to do
 ])
 def test_rmsnorm_rejects(kw, expect):
@@ -66,7 +67,7 @@ def norm_bwd(**kw):
     (dict(ws=A + 8), -1), (dict(dy=A + 1), -1), (dict(dh=A + 1), -1), (dict(dx=A + 1), -1),
     (dict(dw=A + 1), -1), (dict(dt=7), -1), (dict(dt=F32, wdt=BF16), -1),
     (dict(ldy=3), -2), (dict(ldh=3), -2), (dict(ldd=3), -2), (dict(cols=-1), -2),
-    (dict(rows=-2), -2),
+    (dict(rows=-2), -2), (dict(rows=1 << 40, cols=1 << 24, ldy=BIG, ldh=BIG, ldd=BIG), -2),
 ])
 def test_rmsnorm_bwd_rejects(kw, expect):
     assert norm_bwd(**kw) == expect

@@ -27,7 +27,7 @@ constexpr int64_t kMaxLd = int64_t(1) << 40;
 constexpr int64_t kMaxElems = int64_t(1) << 44;
 
 ufp4_status check_norm_shape(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols <= 0 || rows > kMaxRows || cols > kMaxCols || rows * cols > kMaxElems)
+  if (rows < 0 || cols <= 0 || rows > kMaxRows || cols > kMaxCols || rows > kMaxElems / cols)
     return UFP4_ERR_SHAPE;
   return UFP4_OK;
 }
