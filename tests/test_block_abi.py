@@ -18,6 +18,18 @@ A = 0x10000                # an address that is never dereferenced
 BIG = 1 << 40
 
 
+class RoutingDesc(ctypes.Structure):
+    """Mirror of ufp4_routing."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("experts", "gates", "slots", "lse", "counts",
+                                               "offsets", "n_tokens", "losses")]
+
+
+class GradDesc(ctypes.Structure):
+    """Mirror of ufp4_grad."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 def test_library_exports_every_declared_symbol():
     src = open(os.path.join(ROOT, "include", "ufp4_block.h")).read()
     decl = sorted(set(re.findall(r"^(?:ufp4_status|size_t)\s+(ufp4_\w+)\(", src, re.M)))
@@ -74,9 +86,9 @@ def test_rmsnorm_bwd_rejects(kw, expect):
 
 
 def routing(**kw):
-    a = {n: A for n, _ in B.RoutingDesc._fields_}
+    a = {n: A for n, _ in RoutingDesc._fields_}
     a.update(kw)
-    return B.RoutingDesc(**a)
+    return RoutingDesc(**a)
 
 
 def route(bwd=False, r=None, **kw):
@@ -156,7 +168,7 @@ def test_exchange_rejects_bad_gates():
 def grad(**kw):
     a = dict(data=A, out=A, n=8, dtype=F32, out_dtype=F32)
     a.update(kw)
-    return B.GradDesc(*a.values())
+    return GradDesc(*a.values())
 
 
 @pytest.mark.parametrize("g,norm_status,clip_status", [
@@ -167,7 +179,7 @@ def grad(**kw):
 ])
 def test_grads_reject(g, norm_status, clip_status):
     L = B.lib()
-    d = (B.GradDesc * 2)(grad(), g)
+    d = (GradDesc * 2)(grad(), g)
     p = ctypes.addressof(d)
     if norm_status is not None:
         assert L.ufp4_grad_norm(p, 2, A, 1 << 20, A, None) == norm_status
@@ -176,7 +188,7 @@ def test_grads_reject(g, norm_status, clip_status):
 
 def test_grad_call_arguments():
     L = B.lib()
-    p = ctypes.addressof((B.GradDesc * 1)(grad()))
+    p = ctypes.addressof((GradDesc * 1)(grad()))
     n = int(L.ufp4_grad_norm_workspace_size())
     assert L.ufp4_grad_norm(p, -1, A, n, A, None) == -2
     assert L.ufp4_grad_norm(None, 1, A, n, A, None) == -1

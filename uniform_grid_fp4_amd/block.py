@@ -32,18 +32,6 @@ E4M3 = torch.float8_e4m3fn
 _CODE = U._OUT_CODE                               # element types: float32, bfloat16
 
 
-class RoutingDesc(ctypes.Structure):
-    """Mirror of ufp4_routing."""
-    _fields_ = [(n, ctypes.c_void_p) for n in ("experts", "gates", "slots", "lse", "counts",
-                                               "offsets", "n_tokens", "losses")]
-
-
-class GradDesc(ctypes.Structure):
-    """Mirror of ufp4_grad."""
-    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
-
-
 _lib = None
 
 
@@ -54,7 +42,7 @@ def lib() -> ctypes.CDLL:
         return _lib
     L = U.lib()
     P, I64, I32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    R, G = ctypes.c_void_p, ctypes.c_void_p
+    R, G = P, P                                      # ufp4_routing, ufp4_grad: arrays of words
     L.ufp4_rmsnorm.argtypes = [P, I64, P, I64, P, I32, I32, I64, I64, ctypes.c_float, P, P, P, P,
                                P, P]
     L.ufp4_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, P, I64, I32, I32, I64, I64, P, P, P, S, P]

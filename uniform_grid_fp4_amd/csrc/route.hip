@@ -582,7 +582,7 @@ static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   const int64_t nblk = route_blocks(a.tokens);
   RouteWs ws{};
   if (nblk > 1) route_layout(nblk, a.n_experts, a.workspace, &ws);
-    if (nblk == 1) {
+  if (nblk == 1) {
     hipLaunchKernelGGL((route_kernel<T, R, FULL, true>), dim3(1),
                        dim3(route_threads(R, true)), route_lds(R, true, a.n_experts), st, a, ws);
     return hipGetLastError();
