@@ -79,7 +79,7 @@ def check_forward(x, w, res, q8=True, out_h=None):
 SHAPES = [(1, 1), (1, 2048), (3, 7), (2, 8), (5, 63), (4, 64), (3, 65), (7, 511), (2, 1024),
           (33, 1411), (3, 2049), (2, 4104), (2, 6144), (3, 8192), (2, 12289), (2, 16384),
           (1, 40000), (300, 96), (600, 5000), (530, 9000), (3, 11000), (700, 15),
-          (1500, 121), (600, 2047), (520, 6143)]
+          (1500, 121), (600, 2047), (520, 6143), (600, 1073), (40, 1536)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)

@@ -481,6 +481,7 @@ static RowShape row_shape(int64_t cols, int v) {
   if (n <= 16) return {16, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
+  if (n <= 192) return {64, 3};
   if (n <= 256) return {64, 4};
   if (n <= 512) return {256, 2};
   if (n <= 768) return {256, 3};
@@ -490,11 +491,14 @@ static RowShape row_shape(int64_t cols, int v) {
   if (n <= 3072 && v == Elem<float>::V) return {1024, 3};
   return {0, 0};
 }
-// The backward pass also keeps dw's sums: four vectors per lane would leave one
-// wave per SIMD (8192 x 2048 bf16: 40 us, a workgroup per row 30 us).
+// The backward pass also keeps dw's sums, and a wave with four vectors per lane
+// has few registers left for its loads: 193 to 256 vectors take a workgroup
+// with one each (8192 x 2048 bf16 26.7 us, a wave per row 27.8; 3000 x 2047 17
+// and 22 us).  With fewer too many of its threads would idle (30000 x 1280: 77
+// us, a wave per row 57 us).
 static RowShape bwd_shape(int64_t cols, int v) {
   const int64_t n = (cols + v - 1) / v;
-  return n > 128 && n <= 256 ? RowShape{256, 1} : row_shape(cols, v);
+  return n > 192 && n <= 256 ? RowShape{256, 1} : row_shape(cols, v);
 }
 // Workgroups of the backward pass.  Each writes a row of partial sums, so more
 // of them cost traffic and a longer second half; fewer leave the memory idle
@@ -507,8 +511,8 @@ static int64_t row_groups(int64_t rows, int tpr) {
 }
 
 #define UFP4_LONG_SHAPES(F) F(256, 2) F(256, 3) F(256, 4) F(512, 3) F(512, 4)
-#define UFP4_FWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(64, 4) UFP4_LONG_SHAPES(F)
-#define UFP4_BWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(256, 1) UFP4_LONG_SHAPES(F)
+#define UFP4_FWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(64, 3) F(64, 4) UFP4_LONG_SHAPES(F)
+#define UFP4_BWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(64, 3) F(256, 1) UFP4_LONG_SHAPES(F)
 
 template <typename T, typename W, bool TAIL>
 static hipError_t norm_fwd_rows(const NormArgs &a, RowShape s, hipStream_t st) {
