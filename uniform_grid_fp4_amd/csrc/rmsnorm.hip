@@ -476,19 +476,12 @@ struct RowShape {
   int tpr, nv;
 };
 static RowShape row_shape(int64_t cols, int v) {
+  constexpr RowShape kShapes[] = {{16, 1},  {64, 1},  {64, 2},  {64, 3},  {64, 4},  {256, 2},
+                                  {256, 3}, {256, 4}, {512, 3}, {512, 4}, {1024, 3}};
   if (cols < v) return {0, 0};
   const int64_t n = (cols + v - 1) / v;
-  if (n <= 16) return {16, 1};
-  if (n <= 64) return {64, 1};
-  if (n <= 128) return {64, 2};
-  if (n <= 192) return {64, 3};
-  if (n <= 256) return {64, 4};
-  if (n <= 512) return {256, 2};
-  if (n <= 768) return {256, 3};
-  if (n <= 1024) return {256, 4};
-  if (n <= 1536) return {512, 3};
-  if (n <= 2048) return {512, 4};
-  if (n <= 3072 && v == Elem<float>::V) return {1024, 3};
+  for (const RowShape &s : kShapes)
+    if (n <= s.tpr * s.nv && (s.tpr < 1024 || v == Elem<float>::V)) return s;
   return {0, 0};
 }
 // The backward pass also keeps dw's sums, and a wave with four vectors per lane
