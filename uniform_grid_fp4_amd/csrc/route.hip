@@ -32,6 +32,9 @@ constexpr int kBwdGroups = 16;                   // tokens in flight, backward
 // 256 threads 11.4 us); the registers of long rows allow 256 and four tokens in
 // turn.  A single workgroup with few tokens has no use for more than 256.
 constexpr int route_threads(int r, bool alone) { return alone || r > 16 ? 256 : 1024; }
+// Workgroups per launch: a launch holds fewer than 2^32 threads, and 2^28 tokens
+// or more take several, each from its first block of kRouteTokens tokens on.
+constexpr int64_t kRouteGrid = int64_t(1) << 21;
 
 // Workspace of a call with nblk workgroups, E experts:
 //   uint32 base [E + 1][nblk]  choices per expert (last: choices that do not
@@ -47,6 +50,7 @@ struct RouteWs {
   uint32_t *live;
   uint32_t *total;
   double *ptotal;
+  int64_t nblk;
 };
 __host__ __device__ inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 __host__ __device__ inline size_t route_layout(int64_t nblk, int e, void *p, RouteWs *w) {
@@ -66,6 +70,7 @@ __host__ __device__ inline size_t route_layout(int64_t nblk, int e, void *p, Rou
     w->live = static_cast<uint32_t *>(parts[3]);
     w->total = static_cast<uint32_t *>(parts[4]);
     w->ptotal = static_cast<double *>(parts[5]);
+    w->nblk = nblk;
   }
   return used;
 }
@@ -185,7 +190,8 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, double balance,
 // ALONE (one workgroup) everything else too.  Dynamic LDS: 12 bytes per expert and 4 for each wave.
 template <typename T, int R, bool FULL, bool ALONE>
 __global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const RouteArgs a,
-                                                                       const RouteWs ws) {
+                                                                       const RouteWs ws,
+                                                                       int64_t block0) {
   constexpr int kThreads = route_threads(R, ALONE), kWaves = kThreads / 64;
   constexpr int kGroups = kThreads / 16, kPer = kRouteTokens / kGroups;   // tokens per group
   extern __shared__ __align__(16) char s_dyn[];
@@ -194,6 +200,7 @@ __global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const Ro
   __shared__ float s_lse[kRouteTokens];
   __shared__ double s_part[4];
   const int E = FULL ? 16 * R : a.n_experts, k = a.k;
+  const int64_t block = ALONE ? 0 : block0 + blockIdx.x;
   using H = Hold<T, R, FULL>;
   unsigned long long *s_mask = reinterpret_cast<unsigned long long *>(s_dyn);
   uint32_t *s_off = reinterpret_cast<uint32_t *>(s_dyn + 8 * E);
@@ -221,8 +228,8 @@ __global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const Ro
     choice[n] = -1;
     found[n] = 0;
     const int local = n * kGroups + group;
-    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + local;
-    if ((int64_t)blockIdx.x * kRouteTokens + n * kGroups >= a.tokens) {   // the whole workgroup
+    const int64_t t = block * kRouteTokens + local;
+    if (block * kRouteTokens + n * kGroups >= a.tokens) {   // the whole workgroup
       if (lane == 0) {
         s_lost[local] = 0;
         s_live[local] = 0;
@@ -360,8 +367,8 @@ __global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const Ro
       a.counts[e] = (int64_t)c;
       balance += (double)c * (double)p;
     } else {
-      ws.base[(int64_t)e * gridDim.x + blockIdx.x] = c;
-      ws.psum[(int64_t)e * gridDim.x + blockIdx.x] = p;
+      ws.base[e * ws.nblk + block] = c;
+      ws.psum[e * ws.nblk + block] = p;
     }
   }
   uint32_t routed = 0;
@@ -375,16 +382,16 @@ __global__ __launch_bounds__(route_threads(R, ALONE)) void route_kernel(const Ro
       write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], z, tokens);
   } else {
     if (threadIdx.x == 0) {
-      ws.base[(int64_t)E * gridDim.x + blockIdx.x] = lost_all;
-      ws.z[blockIdx.x] = z;
-      ws.live[blockIdx.x] = tokens;
+      ws.base[E * ws.nblk + block] = lost_all;
+      ws.z[block] = z;
+      ws.live[block] = tokens;
     }
     __syncthreads();                             // s_lost
   }
 #pragma unroll
   for (int n = 0; n < kPer; ++n) {
     const int local = n * kGroups + group;
-    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + local;
+    const int64_t t = block * kRouteTokens + local;
     if (t >= a.tokens || lane >= k) continue;
     const int e = choice[n];
     uint32_t place;
@@ -444,14 +451,16 @@ __global__ __launch_bounds__(64) void route_scan_kernel(const RouteArgs a, const
   }
 }
 
-// Places to rows, for the 64 tokens of a workgroup; workgroup 0 writes the
-// counts, offsets and losses.
-__global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, const RouteWs ws) {
+// Places to rows, for the 64 tokens of a workgroup; the first block's workgroup
+// writes the counts, offsets and losses.
+__global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, const RouteWs ws,
+                                                          int64_t block0) {
   __shared__ uint32_t s_off[kRouteMaxExperts];
   __shared__ uint32_t s_scan[4];
   __shared__ double s_part[4];
   const int E = a.n_experts, k = a.k;
-  const bool first = blockIdx.x == 0;
+  const int64_t block = block0 + blockIdx.x;
+  const bool first = block == 0;
   double balance = 0.0;
   for (int e = threadIdx.x; e < E; e += 256) {
     const uint32_t c = ws.total[e];
@@ -472,9 +481,9 @@ __global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a, con
       write_totals(a, ((s_part[0] + s_part[1]) + s_part[2]) + s_part[3], ws.ptotal[E],
                    ws.total[E + 1]);
   }
-  const uint32_t *base = ws.base + blockIdx.x;
-  const int64_t nblk = gridDim.x;
-  const int64_t i0 = (int64_t)blockIdx.x * kRouteTokens * k;
+  const uint32_t *base = ws.base + block;
+  const int64_t nblk = ws.nblk;
+  const int64_t i0 = block * kRouteTokens * k;
   const int64_t i1 = min(i0 + (int64_t)kRouteTokens * k, a.tokens * k);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
     const int32_t e = a.experts[i], place = a.slots[i];
@@ -577,6 +586,11 @@ static size_t route_lds(int r, bool alone, int n_experts) {
   return (size_t)(12 + route_threads(r, alone) / 64 * 4) * (size_t)n_experts;
 }
 
+static dim3 route_grid(int64_t nblk, int64_t from) {
+  const int64_t left = nblk - from;
+  return dim3((unsigned)(left < kRouteGrid ? left : kRouteGrid));
+}
+
 template <typename T, int R, bool FULL>
 static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   const int64_t nblk = route_blocks(a.tokens);
@@ -584,15 +598,27 @@ static hipError_t route_fwd(const RouteArgs &a, hipStream_t st) {
   if (nblk > 1) route_layout(nblk, a.n_experts, a.workspace, &ws);
   if (nblk == 1) {
     hipLaunchKernelGGL((route_kernel<T, R, FULL, true>), dim3(1),
-                       dim3(route_threads(R, true)), route_lds(R, true, a.n_experts), st, a, ws);
+                       dim3(route_threads(R, true)), route_lds(R, true, a.n_experts), st, a, ws,
+                       int64_t(0));
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((route_kernel<T, R, FULL, false>), dim3((unsigned)nblk),
-                     dim3(route_threads(R, false)), route_lds(R, false, a.n_experts), st, a, ws);
+  // What the choices did not write must not be read: the first launch that fails
+  // ends the call.
+  for (int64_t b = 0; b < nblk; b += kRouteGrid) {
+    hipLaunchKernelGGL((route_kernel<T, R, FULL, false>), route_grid(nblk, b),
+                       dim3(route_threads(R, false)), route_lds(R, false, a.n_experts), st, a, ws,
+                       b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)(a.n_experts + 2)), dim3(64), 0, st, a, ws,
                      (int)nblk);
-  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)nblk), dim3(256), 0, st, a, ws);
-  return hipGetLastError();
+  hipError_t e = hipGetLastError();
+  for (int64_t b = 0; e == hipSuccess && b < nblk; b += kRouteGrid) {
+    hipLaunchKernelGGL(route_place_kernel, route_grid(nblk, b), dim3(256), 0, st, a, ws, b);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 template <typename T, int R, bool FULL>
