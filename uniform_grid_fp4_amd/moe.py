@@ -181,9 +181,10 @@ class UFP4MoEBlock(torch.nn.Module):
 def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float,
                     eps: float = 1e-6) -> torch.Tensor:
     """Scale the parameters' gradients in place so that their global norm is at
-    most max_norm; returns the norm before it (a float32 scalar on the GPU)."""
-    params = [parameters] if isinstance(parameters, torch.Tensor) else parameters
+    most max_norm; returns the norm before it (a float32 scalar on the
+    parameters' device; zero if none of them has a gradient)."""
+    params = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in params if p.grad is not None]
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), device=params[0].device if params else None)
     return B.ufp4_clip_grads(grads, max_norm, eps=eps)
