@@ -18,6 +18,7 @@ import torch
 
 from . import block as B
 from . import ufp4 as U
+from .autograd import first_order
 from .layers import UFP4ExpertLinear
 
 
@@ -42,7 +43,8 @@ class _NormFn(torch.autograd.Function):
         h, weight, rstd = ctx.saved_tensors
         if dy is None:                               # only the stream itself was used
             return dh, dh, None, None
-        dx, dw = B.ufp4_rmsnorm_bwd(_flat(dy), h, weight, rstd, None if dh is None else _flat(dh))
+        dx, dw = first_order(B.ufp4_rmsnorm_bwd, _flat(dy), h, weight, rstd,
+                             None if dh is None else _flat(dh))
         return dx, (dx if ctx.summed else None), dw, None
 
 
@@ -62,8 +64,8 @@ class _RouteFn(torch.autograd.Function):
             return None, None, None, None
         logits, *saved = ctx.saved_tensors
         c = lambda t: None if t is None else t.contiguous()
-        return B.ufp4_moe_route_bwd(logits, B.Routing(*saved, ctx.renorm), c(d_gates),
-                                    c(d_losses)), None, None, None
+        return first_order(B.ufp4_moe_route_bwd, logits, B.Routing(*saved, ctx.renorm), c(d_gates),
+                           c(d_losses)), None, None, None
 
 
 class _DispatchFn(torch.autograd.Function):
@@ -74,7 +76,7 @@ class _DispatchFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dxs):
-        return B.ufp4_moe_dispatch_bwd(dxs.contiguous(), *ctx.saved_tensors), None
+        return first_order(B.ufp4_moe_dispatch_bwd, dxs.contiguous(), *ctx.saved_tensors), None
 
 
 class _CombineFn(torch.autograd.Function):
@@ -87,7 +89,7 @@ class _CombineFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         ys, slots, gates = ctx.saved_tensors
-        dys, dg = B.ufp4_moe_combine_bwd(_flat(dy), ys, slots, gates)
+        dys, dg = first_order(B.ufp4_moe_combine_bwd, _flat(dy), ys, slots, gates)
         return dys, None, dg, (dy if ctx.summed else None)
 
 
