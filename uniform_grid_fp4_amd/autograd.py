@@ -15,17 +15,17 @@ class _FirstOnly(torch.autograd.Function):
         raise RuntimeError("the UFP4 layers have no second derivatives")
 
 
-def first_order(call, *args):
+def first_order(call, *args, also: bool = False):
     """call(*args), a tensor or a tuple of them.  Where a backward pass is itself
-    recorded (create_graph) and an argument depends on what may be
-    differentiated, the results raise when they are differentiated: left
-    unrecorded, their part of a second derivative would be missing without a
-    word."""
+    recorded (create_graph) and an argument, or with `also` what the call has
+    kept, depends on what may be differentiated, the results raise when they are
+    differentiated: left unrecorded, their part of a second derivative would be
+    missing without a word."""
     if not torch.is_grad_enabled():
         return call(*args)
     with torch.no_grad():
         out = call(*args)
-    if not any(isinstance(a, torch.Tensor) and a.requires_grad for a in args):
+    if not (also or any(isinstance(a, torch.Tensor) and a.requires_grad for a in args)):
         return out
     refuse = lambda t: None if t is None else _FirstOnly.apply(t.detach().requires_grad_())
     return refuse(out) if isinstance(out, torch.Tensor) else tuple(map(refuse, out))

@@ -27,6 +27,7 @@ import numpy as np
 import torch
 
 from . import ufp4 as U
+from .autograd import first_order
 
 
 def draw_sign_masks(seed: int):
@@ -60,15 +61,25 @@ class _LinearFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        _, md, mw = ctx.masks
-        _, rd, rw = ctx.rht
-        dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
-                                             grid=ctx.grid, rnd=ctx.rnd_dy, seed=ctx.seed)
-        xtq, wtq = ctx.q
-        ctx.q = None
-        dx = U.ufp4_gemm_out(U.DGRAD, dyq, wtq, torch.bfloat16)
-        dw = U.ufp4_gemm_out(U.WGRAD, dytq, xtq, torch.bfloat16)
+        dx, dw = first_order(_linear_grads, ctx, dy, also=_both(ctx))
         return dx, dw, None, None, None, None, None
+
+
+def _linear_grads(ctx, dy):
+    _, md, mw = ctx.masks
+    _, rd, rw = ctx.rht
+    dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
+                                         grid=ctx.grid, rnd=ctx.rnd_dy, seed=ctx.seed)
+    xtq, wtq = ctx.q
+    ctx.q = None
+    dx = U.ufp4_gemm_out(U.DGRAD, dyq, wtq, torch.bfloat16)
+    dw = U.ufp4_gemm_out(U.WGRAD, dytq, xtq, torch.bfloat16)
+    return dx, dw
+
+
+def _both(ctx) -> bool:
+    """Whether X and W are both differentiated: dX depends on W, and dW on X."""
+    return all(ctx.needs_input_grad[:2])
 
 
 def _bf16_rows(t: torch.Tensor) -> torch.Tensor:
@@ -121,17 +132,21 @@ class _ExpertFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        _, md, mw = ctx.masks
-        _, rd, rw = ctx.rht
-        dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
-                                             grid=ctx.grid, rnd=ctx.rnd_dy, seed=ctx.seed,
-                                             group_offsets=ctx.offsets)
-        xtq, wtq = ctx.q
-        ctx.q = None
-        dx = U.ufp4_grouped_gemm_out(U.DGRAD, ctx.offsets, dyq, wtq, torch.bfloat16)
-        dw = U.ufp4_grouped_gemm_out(U.WGRAD, ctx.offsets, dytq, xtq, torch.bfloat16)
-        dw = dw.reshape(-1, dw.shape[-1])
+        dx, dw = first_order(_expert_grads, ctx, dy, also=_both(ctx))
         return dx, dw, None, None, None, None, None, None, None
+
+
+def _expert_grads(ctx, dy):
+    _, md, mw = ctx.masks
+    _, rd, rw = ctx.rht
+    dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
+                                         grid=ctx.grid, rnd=ctx.rnd_dy, seed=ctx.seed,
+                                         group_offsets=ctx.offsets)
+    xtq, wtq = ctx.q
+    ctx.q = None
+    dx = U.ufp4_grouped_gemm_out(U.DGRAD, ctx.offsets, dyq, wtq, torch.bfloat16)
+    dw = U.ufp4_grouped_gemm_out(U.WGRAD, ctx.offsets, dytq, xtq, torch.bfloat16)
+    return dx, dw.reshape(-1, dw.shape[-1])
 
 
 class UFP4ExpertLinear(torch.nn.Module):
