@@ -17,7 +17,8 @@
  * floating-point atomics).  Element types are ufp4_out_dtype codes
  * (UFP4_OUT_F32, UFP4_OUT_BF16).  Floating-point buffers are aligned to their
  * element size and may start at any element: the kernels' 16-byte accesses
- * need no more.  Strides (ld_*) are in elements, at least the row length.
+ * need no more.  Strides (ld_*) are in elements, at least the row length, and
+ * rows times the stride at most 2^60.
  * Statistics, sums and gradients are accumulated in FP32 (FP64 where stated)
  * and rounded once to the output's type, to nearest even.  Zero rows or
  * tokens are accepted: such a call writes what it has to write (zero sums).

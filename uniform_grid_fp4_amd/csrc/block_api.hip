@@ -25,13 +25,16 @@ constexpr int64_t kMaxRows = int64_t(1) << 40;
 constexpr int64_t kMaxCols = int64_t(1) << 24;
 constexpr int64_t kMaxLd = int64_t(1) << 40;
 constexpr int64_t kMaxElems = int64_t(1) << 44;
+constexpr int64_t kMaxSpan = int64_t(1) << 60;     // elements from the first row to the last
 
 ufp4_status check_norm_shape(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0 || rows > kMaxRows || cols > kMaxCols || rows > kMaxElems / cols)
     return UFP4_ERR_SHAPE;
   return UFP4_OK;
 }
-bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > kMaxLd; }
+bool bad_ld(int64_t ld, int64_t rows, int64_t cols) {
+  return ld < cols || ld > kMaxLd || (rows > 1 && ld > kMaxSpan / rows);
+}
 
 ufp4_status check_exchange(int32_t dtype, int64_t tokens, int32_t k, int64_t cols) {
   if (!known_type(dtype)) return UFP4_ERR_INVALID_ARG;
@@ -44,7 +47,7 @@ ufp4_status check_route(const void *logits, int64_t ld, int32_t dtype, int64_t t
                         int32_t n_experts, int32_t k, int32_t renorm, const ufp4_routing *r) {
   if (!known_type(dtype) || (renorm != 0 && renorm != 1) || r == nullptr)
     return UFP4_ERR_INVALID_ARG;
-  if (tokens < 0 || n_experts < 1 || k < 1 || k > n_experts || bad_ld(ld, n_experts))
+  if (tokens < 0 || n_experts < 1 || k < 1 || k > n_experts || bad_ld(ld, tokens, n_experts))
     return UFP4_ERR_SHAPE;
   if (n_experts > kRouteMaxExperts || k > kRouteMaxK || tokens > INT32_MAX / k)
     return UFP4_ERR_UNSUPPORTED;
@@ -105,7 +108,7 @@ ufp4_status ufp4_rmsnorm(const void *x, int64_t ld_x, const void *residual, int6
     return UFP4_ERR_INVALID_ARG;
   const ufp4_status s = check_norm_shape(rows, cols);
   if (s != UFP4_OK) return s;
-  if (bad_ld(ld_x, cols) || (residual != nullptr && bad_ld(ld_residual, cols)))
+  if (bad_ld(ld_x, rows, cols) || (residual != nullptr && bad_ld(ld_residual, rows, cols)))
     return UFP4_ERR_SHAPE;
   const uintptr_t e = size_of(dtype);
   if (!good(weight, size_of(weight_dtype))) return UFP4_ERR_INVALID_ARG;
@@ -148,7 +151,8 @@ ufp4_status ufp4_rmsnorm_bwd(const void *dy, int64_t ld_dy, const void *h, int64
     return UFP4_ERR_INVALID_ARG;
   const ufp4_status s = check_norm_shape(rows, cols);
   if (s != UFP4_OK) return s;
-  if (bad_ld(ld_dy, cols) || bad_ld(ld_h, cols) || (dh != nullptr && bad_ld(ld_dh, cols)))
+  if (bad_ld(ld_dy, rows, cols) || bad_ld(ld_h, rows, cols) ||
+      (dh != nullptr && bad_ld(ld_dh, rows, cols)))
     return UFP4_ERR_SHAPE;
   const uintptr_t e = size_of(dtype), we = size_of(weight_dtype);
   if (!good(weight, we) || !good(dw, we) || !good_or_null(dh, e)) return UFP4_ERR_INVALID_ARG;
@@ -216,7 +220,7 @@ ufp4_status ufp4_moe_dispatch(const void *x, int64_t ld_x, const int32_t *slots,
                               hipStream_t stream) {
   const ufp4_status s = check_exchange(dtype, tokens, k, cols);
   if (s != UFP4_OK) return s;
-  if (bad_ld(ld_x, cols)) return UFP4_ERR_SHAPE;
+  if (bad_ld(ld_x, tokens, cols)) return UFP4_ERR_SHAPE;
   if (tokens == 0) return UFP4_OK;
   const uintptr_t e = size_of(dtype);
   if (!good(x, e) || !good(slots, 4) || !good(xs, e)) return UFP4_ERR_INVALID_ARG;
@@ -257,7 +261,7 @@ ufp4_status ufp4_moe_combine(const void *ys, const int32_t *slots, const float *
                              hipStream_t stream) {
   const ufp4_status s = check_exchange(dtype, tokens, k, cols);
   if (s != UFP4_OK) return s;
-  if (residual != nullptr && bad_ld(ld_residual, cols)) return UFP4_ERR_SHAPE;
+  if (residual != nullptr && bad_ld(ld_residual, tokens, cols)) return UFP4_ERR_SHAPE;
   if (tokens == 0) return UFP4_OK;
   const uintptr_t e = size_of(dtype);
   if (!good(ys, e) || !good(slots, 4) || !good(gates, 4) || !good_or_null(residual, e) ||
@@ -283,7 +287,7 @@ ufp4_status ufp4_moe_combine_bwd(const void *dy, int64_t ld_dy, const void *ys,
                                  float *d_gates, hipStream_t stream) {
   const ufp4_status s = check_exchange(dtype, tokens, k, cols);
   if (s != UFP4_OK) return s;
-  if (bad_ld(ld_dy, cols)) return UFP4_ERR_SHAPE;
+  if (bad_ld(ld_dy, tokens, cols)) return UFP4_ERR_SHAPE;
   if (tokens == 0) return UFP4_OK;
   const uintptr_t e = size_of(dtype);
   if (!good(dy, e) || !good(ys, e) || !good(slots, 4) || !good(gates, 4) || !good(dys, e) ||
