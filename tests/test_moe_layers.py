@@ -89,3 +89,15 @@ def test_gradients_that_are_constant_or_exact_are_not_refused(plain):
         g, = torch.autograd.grad(stream(x).square().sum() / 2, x, create_graph=True)
         g.sum().backward()
         assert torch.equal(x.grad, torch.ones((3, 4)))
+
+
+def test_a_gradient_that_is_listed_twice_is_clipped_once(monkeypatch):
+    """Scaled by two workgroups at once, its elements would be scaled once or
+    twice, whichever came first."""
+    seen = []
+    monkeypatch.setattr(M.B, "ufp4_clip_grads", lambda grads, *a, **kw: seen.extend(grads))
+    a, b, c = (torch.nn.Parameter(torch.zeros(3)) for _ in range(3))
+    a.grad, b.grad = torch.ones(3), torch.ones(3)
+    c.grad = b.grad                                  # two parameters, one gradient
+    M.clip_grad_norm_([a, b, a, c, torch.nn.Parameter(torch.zeros(3))], 1.0)
+    assert [id(g) for g in seen] == [id(a.grad), id(b.grad)]

@@ -461,8 +461,9 @@ def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Scale all tensors by min(1, max_norm / (norm + eps)), in place or into
     `out` (as many elements each, contiguous, or of the tensors' shapes and
-    strides; bf16 or float32), and return the norm before it.  The coefficient
-    stays on the GPU: nothing waits."""
+    strides; bf16 or float32), and return the norm before it.  No two outputs may
+    overlap, nor an output another tensor.  The coefficient stays on the GPU:
+    nothing waits."""
     d, n, dev = _grad_list(tensors, out)
     norm = _norm_of(d, n, dev, workspace)
     st = lib().ufp4_grad_clip(d.buffer_info()[0], n, _p(norm), max_norm, eps, _stream(dev))

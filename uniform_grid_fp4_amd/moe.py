@@ -184,9 +184,10 @@ def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float,
                     eps: float = 1e-6) -> torch.Tensor:
     """Scale the parameters' gradients in place so that their global norm is at
     most max_norm; returns the norm before it (a float32 scalar on the
-    parameters' device; zero if none of them has a gradient)."""
+    parameters' device; zero if none of them has a gradient).  A parameter that
+    is listed twice, as a tied weight may be, counts and is scaled once."""
     params = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
-    grads = [p.grad for p in params if p.grad is not None]
+    grads = list({id(p.grad): p.grad for p in params if p.grad is not None}.values())
     if not grads:
         return torch.zeros((), device=params[0].device if params else None)
     return B.ufp4_clip_grads(grads, max_norm, eps=eps)
