@@ -132,6 +132,10 @@ def _stream(device: torch.device):
     return _raw_stream(device.index)
 
 
+# Tells autograd that a tensor, or each of a list, was written in place.
+_written = torch.autograd.graph.increment_version
+
+
 # ---------------------------------------------------------------------------
 # RMS norm
 # ---------------------------------------------------------------------------
@@ -175,6 +179,8 @@ def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
                             cols, eps, _p(h) if residual is not None else None, _p(out), _p(q),
                             _p(scale), _p(rstd), _stream(dev))
     U._check(st, "ufp4_rmsnorm")
+    if out_h is not None:
+        _written(out_h)
     return NormOut(out, h, rstd, q, scale)
 
 
@@ -468,4 +474,6 @@ def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
     norm = _norm_of(d, n, dev, workspace)
     st = lib().ufp4_grad_clip(d.buffer_info()[0], n, _p(norm), max_norm, eps, _stream(dev))
     U._check(st, "ufp4_grad_clip")
+    if out is None:
+        _written(tensors)
     return norm
