@@ -169,9 +169,11 @@ ufp4_status ufp4_moe_combine_bwd(const void *dy, int64_t ld_dy, const void *ys,
  *          in FP64, to *norm (FP32, device)
  *   clip: out = g * min(1, max_norm / (norm + eps)) in every tensor, the
  *         coefficient taken from *norm on the device (no synchronisation).
- *         A NaN norm gives NaN everywhere, an infinite one zeros (NaN where
- *         the element is not finite).  With out == data and a coefficient of
- *         1 nothing is written.
+ *         A norm + eps of at most max_norm scales nothing (also where both
+ *         are zero or infinite).  A NaN norm gives NaN everywhere, an
+ *         infinite one beyond max_norm zeros (NaN where the element is not
+ *         finite).  With out == data and a coefficient of 1 nothing is
+ *         written.
  * Each tensor is n dense elements of type dtype; out (of type out_dtype) may
  * be data itself when the types agree, and is ignored by ufp4_grad_norm.
  * Tensors must not overlap each other's outputs.  n = 0 is accepted.

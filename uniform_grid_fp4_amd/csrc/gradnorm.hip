@@ -153,9 +153,9 @@ __device__ __forceinline__ void piece_scale(const T *p, O *out, int n, float coe
 
 __global__ __launch_bounds__(256) void grad_scale_kernel(const GradTable g, const float *norm,
                                                          double max_norm, double eps, bool stream) {
-  double c = max_norm / ((double)*norm + eps);
-  c = c >= 1.0 ? 1.0 : c;                        // a NaN stays
-  const float coef = (float)c;
+  // a norm within the limit first: 0 / 0 and inf / inf are within it; a NaN stays
+  const double size = (double)*norm + eps;
+  const float coef = size <= max_norm ? 1.0f : (float)(max_norm / size);
   const int32_t pieces = g.first[g.items];
   // from the last piece to the first: what the norm read last is still cached
   for (int32_t p = pieces - 1 - (int32_t)blockIdx.x; p >= 0; p -= gridDim.x) {
