@@ -153,3 +153,19 @@ def test_router_ends_with_the_first_launch_that_fails(run, sizes, launches):
     assert got[0][:2] == [OK, launches]
     for i, (status, done, _) in enumerate(got[1:]):
         assert (status, done) == (HIP, i + 1)
+
+
+MANY = [("route", dict(t=70, e=16, k=2, dt=F32)),
+        ("norm_bwd", dict(t=300, c=2048, dt=BF16)), ("norm_bwd", dict(t=300, c=40000, dt=F32)),
+        ("norm_bwd", dict(t=0, c=64, dt=F32)), ("grad_norm", dict(t=300, c=1 << 20, dt=F32)),
+        ("grad_clip", dict(t=300, c=1 << 20, dt=BF16))]
+
+
+@pytest.mark.parametrize("op,sizes", MANY)
+def test_a_launch_that_fails_ends_the_call(run, op, sizes):
+    """Whatever the call would have launched after it works on what was not
+    written, or overwrites what a second try needs."""
+    (status, launches, _), = run([(op, sizes, -1)])
+    assert status == OK and launches > 1
+    for i, (status, done, _) in enumerate(run([(op, sizes, i) for i in range(launches)])):
+        assert (status, done) == (HIP, i + 1), i

@@ -217,6 +217,8 @@ hipError_t launch_grad_norm(const ufp4_grad *items, int64_t n_items, double *par
     if (used + grid > kGradMaxBlocks) {          // fold what is there into one partial sum
       hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, st, partials, used,
                          static_cast<float *>(nullptr));
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
       used = 1;
     }
     hipLaunchKernelGGL(grad_squares_kernel, dim3(grid), dim3(256), 0, st, g, partials + used);

@@ -586,9 +586,13 @@ static hipError_t norm_bwd(NormBwdArgs a, hipStream_t st) {
     const int64_t per = (a.rows + slices - 1) / slices;
     const unsigned chunks = (unsigned)((a.cols + 255) / 256);
     hipLaunchKernelGGL((rmsnorm_dw_kernel<T>), dim3(chunks, slices), dim3(256), 0, st, a, per);
-    if (a.rows > 0)
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.rows > 0) {
       hipLaunchKernelGGL((rmsnorm_bwd_row_kernel<T, W>), dim3(row_grid(a.rows)), dim3(256), 0,
                          st, a);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((rmsnorm_dw_final_kernel<W>), dim3((unsigned)((a.cols + 15) / 16)),
                      dim3(1024), 0, st, a, slices);
