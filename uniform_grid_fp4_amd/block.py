@@ -123,13 +123,26 @@ def _p(t: Optional[torch.Tensor]):
 
 # torch.cuda.current_stream(device).cuda_stream without the Stream object (2 us
 # a call, a tenth of a single-token norm's time).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+# torch.cuda.current_device() without its check that torch has set up the GPUs.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device: torch.device):
-    if _raw_stream is None or device.index is None:
-        return U._stream(device)
     return _raw_stream(device.index)
+
+
+def _call(name: str, device: torch.device, *args):
+    """As ufp4._call, for the calls whose host time counts."""
+    index = device.index
+    if index == _current_device():
+        st = getattr(lib(), name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, _raw_stream(index))
+    if st:
+        U._check(st, name)
 
 
 # Tells autograd that a tensor, or each of a list, was written in place.
@@ -175,10 +188,8 @@ def ufp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         rstd, scale = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
     else:
         rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-    st = lib().ufp4_rmsnorm(_p(x), ld, _p(residual), ldr, _p(weight), _CODE[x.dtype], wd, rows,
-                            cols, eps, _p(h) if residual is not None else None, _p(out), _p(q),
-                            _p(scale), _p(rstd), _stream(dev))
-    U._check(st, "ufp4_rmsnorm")
+    _call("ufp4_rmsnorm", dev, _p(x), ld, _p(residual), ldr, _p(weight), _CODE[x.dtype], wd, rows,
+          cols, eps, _p(h) if residual is not None else None, _p(out), _p(q), _p(scale), _p(rstd))
     if out_h is not None:
         _written(out_h)
     return NormOut(out, h, rstd, q, scale)
@@ -204,10 +215,8 @@ def ufp4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     _exact(rstd, "rstd", torch.float32, (rows,), dev)
     dx, dw = _new(h), torch.empty_like(weight)
     ws, nbytes = _workspace(workspace, lib().ufp4_rmsnorm_bwd_workspace_size(rows, cols), dev)
-    st = lib().ufp4_rmsnorm_bwd(_p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
-                                _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes,
-                                _stream(dev))
-    U._check(st, "ufp4_rmsnorm_bwd")
+    _call("ufp4_rmsnorm_bwd", dev, _p(dy), ldy, _p(h), ldh, _p(weight), _p(rstd), _p(dh), ldd,
+          _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(ws), nbytes)
     return dx, dw
 
 
@@ -269,9 +278,8 @@ def ufp4_moe_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] =
     need = lib().ufp4_moe_route_workspace_size(t, e)
     ws, nbytes = (None, 0) if need == 0 else _workspace(workspace, need, dev)
     d = r.words()
-    st = lib().ufp4_moe_route(_p(logits), ld, _CODE[logits.dtype], _p(valid), t, e, k, int(renorm),
-                              d.buffer_info()[0], _p(ws), nbytes, _stream(dev))
-    U._check(st, "ufp4_moe_route")
+    _call("ufp4_moe_route", dev, _p(logits), ld, _CODE[logits.dtype], _p(valid), t, e, k,
+          int(renorm), d.buffer_info()[0], _p(ws), nbytes)
     return r
 
 
@@ -294,10 +302,8 @@ def ufp4_moe_route_bwd(logits: torch.Tensor, r: Routing, d_gates: Optional[torch
         _exact(d_losses, "d_losses", torch.float32, (2,), dev)
     out = _new(logits)
     d = r.words()
-    st = lib().ufp4_moe_route_bwd(_p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
-                                  d.buffer_info()[0], _p(d_gates), _p(d_losses), _p(out),
-                                  _stream(dev))
-    U._check(st, "ufp4_moe_route_bwd")
+    _call("ufp4_moe_route_bwd", dev, _p(logits), ld, _CODE[logits.dtype], t, e, k, int(r.renorm),
+          d.buffer_info()[0], _p(d_gates), _p(d_losses), _p(out))
     return out
 
 
@@ -338,9 +344,7 @@ def ufp4_moe_dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     t, k = _slots(slots, x.shape[0], x.device)
     cols = x.shape[1]
     xs = x.new_empty((t * k, cols))
-    st = lib().ufp4_moe_dispatch(_p(x), ld, _p(slots), _CODE[x.dtype], t, k, cols, _p(xs),
-                                 _stream(x.device))
-    U._check(st, "ufp4_moe_dispatch")
+    _call("ufp4_moe_dispatch", x.device, _p(x), ld, _p(slots), _CODE[x.dtype], t, k, cols, _p(xs))
     return xs
 
 
@@ -348,9 +352,8 @@ def ufp4_moe_dispatch_bwd(dxs: torch.Tensor, slots: torch.Tensor) -> torch.Tenso
     """The gradient of dispatch's input: each token's sum over its choices."""
     t, k, cols = _expert_rows(dxs, "dxs", slots)
     dx = dxs.new_empty((t, cols))
-    st = lib().ufp4_moe_dispatch_bwd(_p(dxs), _p(slots), _CODE[dxs.dtype], t, k, cols, _p(dx),
-                                     _stream(dxs.device))
-    U._check(st, "ufp4_moe_dispatch_bwd")
+    _call("ufp4_moe_dispatch_bwd", dxs.device, _p(dxs), _p(slots), _CODE[dxs.dtype], t, k, cols,
+          _p(dx))
     return dx
 
 
@@ -363,9 +366,8 @@ def ufp4_moe_combine(ys: torch.Tensor, slots: torch.Tensor, gates: torch.Tensor,
     if residual is not None:
         ldr = _token_rows(residual, "residual", (t, cols), ys)
     y = ys.new_empty((t, cols))
-    st = lib().ufp4_moe_combine(_p(ys), _p(slots), _p(gates), _p(residual), ldr, _CODE[ys.dtype],
-                                t, k, cols, _p(y), _stream(ys.device))
-    U._check(st, "ufp4_moe_combine")
+    _call("ufp4_moe_combine", ys.device, _p(ys), _p(slots), _p(gates), _p(residual), ldr,
+          _CODE[ys.dtype], t, k, cols, _p(y))
     return y
 
 
@@ -378,9 +380,8 @@ def ufp4_moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
     _exact(gates, "gates", torch.float32, (t, k), ys.device)
     dys = torch.empty_like(ys)
     dg = torch.empty_like(gates)
-    st = lib().ufp4_moe_combine_bwd(_p(dy), ldy, _p(ys), _p(slots), _p(gates), _CODE[ys.dtype], t,
-                                    k, cols, _p(dys), _p(dg), _stream(ys.device))
-    U._check(st, "ufp4_moe_combine_bwd")
+    _call("ufp4_moe_combine_bwd", ys.device, _p(dy), ldy, _p(ys), _p(slots), _p(gates),
+          _CODE[ys.dtype], t, k, cols, _p(dys), _p(dg))
     return dys, dg
 
 
@@ -449,8 +450,7 @@ def _grad_list(tensors, out):
 def _norm_of(d, n, dev, workspace):
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, lib().ufp4_grad_norm_workspace_size(), dev)
-    st = lib().ufp4_grad_norm(d.buffer_info()[0], n, _p(ws), nbytes, _p(norm), _stream(dev))
-    U._check(st, "ufp4_grad_norm")
+    _call("ufp4_grad_norm", dev, d.buffer_info()[0], n, _p(ws), nbytes, _p(norm))
     return norm
 
 
@@ -472,8 +472,7 @@ def ufp4_clip_grads(tensors: Sequence[torch.Tensor], max_norm: float,
     nothing waits."""
     d, n, dev = _grad_list(tensors, out)
     norm = _norm_of(d, n, dev, workspace)
-    st = lib().ufp4_grad_clip(d.buffer_info()[0], n, _p(norm), max_norm, eps, _stream(dev))
-    U._check(st, "ufp4_grad_clip")
+    _call("ufp4_grad_clip", dev, d.buffer_info()[0], n, _p(norm), max_norm, eps)
     if out is None:
         _written(tensors)
     return norm

@@ -108,6 +108,18 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _call(name: str, device: torch.device, *args):
+    """The library's call of that name on the device's current stream, with the
+    device current: a default stream's handle is 0 on every device, and stands
+    for the current one's."""
+    if device.index == torch.cuda.current_device():
+        st = getattr(lib(), name)(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, _stream(device))
+    _check(st, name)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -182,10 +194,9 @@ def ufp4_rht_quantize(x: torch.Tensor, axis: int = BLOCKS_ALONG_COLS, rht: bool 
     rows, kp, n_groups = _quant_shape(x, axis, group_offsets, kpad, n_groups)
     codes, scales, d = _out_desc(out, rows, kp, x.device)
     n_rows, n_cols = x.shape
-    st = lib().ufp4_rht_quantize(_ptr(x), n_rows, n_cols, x.stride(0), axis,
-                                 _ptr(group_offsets), n_groups, int(rht), sign_mask, grid, rnd,
-                                 seed, stream_id, ctypes.byref(d), _stream(x.device))
-    _check(st, "ufp4_rht_quantize")
+    _call("ufp4_rht_quantize", x.device, _ptr(x), n_rows, n_cols, x.stride(0), axis,
+          _ptr(group_offsets), n_groups, int(rht), sign_mask, grid, rnd, seed, stream_id,
+          ctypes.byref(d))
     return Quantized(codes, scales, rows, d.k, kp, d.grid, d.rht, d.sign_mask)
 
 
@@ -207,11 +218,9 @@ def ufp4_rht_quantize_dual(x: torch.Tensor, rowwise: Tuple[bool, int, int],
     sr = QuantSide(int(rowwise[0]), rowwise[1], rowwise[2], 0)
     sc = QuantSide(int(colwise[0]), colwise[1], colwise[2], 0)
     n_rows, n_cols = x.shape
-    st = lib().ufp4_rht_quantize_dual(_ptr(x), n_rows, n_cols, x.stride(0), col_axis,
-                                      _ptr(group_offsets), n_groups, grid, rnd, seed,
-                                      ctypes.byref(sr), ctypes.byref(sc), ctypes.byref(dr),
-                                      ctypes.byref(dc), _stream(x.device))
-    _check(st, "ufp4_rht_quantize_dual")
+    _call("ufp4_rht_quantize_dual", x.device, _ptr(x), n_rows, n_cols, x.stride(0), col_axis,
+          _ptr(group_offsets), n_groups, grid, rnd, seed, ctypes.byref(sr), ctypes.byref(sc),
+          ctypes.byref(dr), ctypes.byref(dc))
     return (Quantized(codes_r, scales_r, rr, dr.k, kr, dr.grid, dr.rht, dr.sign_mask),
             Quantized(codes_c, scales_c, rc, dc.k, kc, dc.grid, dc.rht, dc.sign_mask))
 
@@ -248,9 +257,8 @@ def ufp4_quant_stats(x: torch.Tensor, q: Quantized, axis: int = BLOCKS_ALONG_COL
     assert x.dim() == 2 and x.dtype == torch.bfloat16 and x.is_cuda and x.stride(1) == 1
     ws, nbytes, out = _stats_buffers(x.device, workspace)
     d = q.desc()
-    st = lib().ufp4_quant_stats(_ptr(x), x.shape[0], x.shape[1], x.stride(0), axis,
-                                ctypes.byref(d), _ptr(ws), nbytes, _ptr(out), _stream(x.device))
-    _check(st, "ufp4_quant_stats")
+    _call("ufp4_quant_stats", x.device, _ptr(x), x.shape[0], x.shape[1], x.stride(0), axis,
+          ctypes.byref(d), _ptr(ws), nbytes, _ptr(out))
     return _stats_dict(out)
 
 
@@ -265,9 +273,8 @@ def ufp4_quant_stats_noalloc(x: torch.Tensor, q: Quantized, axis: int = BLOCKS_A
         out = torch.empty(24, dtype=torch.int64, device=x.device)
     assert out.dtype == torch.int64 and out.numel() == 24 and out.is_contiguous()
     d = q.desc()
-    st = lib().ufp4_quant_stats_noalloc(_ptr(x), x.shape[0], x.shape[1], x.stride(0), axis,
-                                        ctypes.byref(d), _ptr(out), _stream(x.device))
-    _check(st, "ufp4_quant_stats_noalloc")
+    _call("ufp4_quant_stats_noalloc", x.device, _ptr(x), x.shape[0], x.shape[1], x.stride(0),
+          axis, ctypes.byref(d), _ptr(out))
     return _stats_dict(out)
 
 
@@ -277,40 +284,34 @@ def ufp4_output_stats(ref: torch.Tensor, test: torch.Tensor,
     assert ref.shape == test.shape and ref.dim() == 2
     assert ref.dtype == test.dtype == torch.float32 and ref.stride(1) == test.stride(1) == 1
     ws, nbytes, out = _stats_buffers(ref.device, workspace)
-    st = lib().ufp4_output_stats(_ptr(ref), ref.stride(0), _ptr(test), test.stride(0),
-                                 ref.shape[0], ref.shape[1], _ptr(ws), nbytes, _ptr(out),
-                                 _stream(ref.device))
-    _check(st, "ufp4_output_stats")
+    _call("ufp4_output_stats", ref.device, _ptr(ref), ref.stride(0), _ptr(test), test.stride(0),
+          ref.shape[0], ref.shape[1], _ptr(ws), nbytes, _ptr(out))
     return _stats_dict(out)
 
 
 def ufp4_dequantize(q: Quantized, inverse_rht: bool = False) -> torch.Tensor:
     out = torch.empty((q.rows, q.kpad), dtype=torch.float32, device=q.codes.device)
     d = q.desc()
-    st = lib().ufp4_dequantize(ctypes.byref(d), int(inverse_rht), _ptr(out), q.kpad,
-                               _stream(out.device))
-    _check(st, "ufp4_dequantize")
+    _call("ufp4_dequantize", out.device, ctypes.byref(d), int(inverse_rht), _ptr(out), q.kpad)
     return out
 
 
-def _dense(fn, name, a: Quantized, b: Quantized, out: Optional[torch.Tensor], *extra):
+def _dense(name, a: Quantized, b: Quantized, out: Optional[torch.Tensor], *extra):
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.float32, device=a.codes.device)
     da, db = a.desc(), b.desc()
-    st = fn(ctypes.byref(da), ctypes.byref(db), _ptr(out), out.stride(0), *extra,
-            _stream(out.device))
-    _check(st, name)
+    _call(name, out.device, ctypes.byref(da), ctypes.byref(db), _ptr(out), out.stride(0), *extra)
     return out
 
 
 def ufp4_gemm_fprop(xq: Quantized, wq: Quantized, out: Optional[torch.Tensor] = None):
     """Y = X_hat W_hat^T, [T, F] FP32."""
-    return _dense(lib().ufp4_gemm_fprop, "ufp4_gemm_fprop", xq, wq, out)
+    return _dense("ufp4_gemm_fprop", xq, wq, out)
 
 
 def ufp4_gemm_dgrad(dyq: Quantized, wtq: Quantized, out: Optional[torch.Tensor] = None):
     """dX = dY_hat (W^T)_hat^T, [T, H] FP32."""
-    return _dense(lib().ufp4_gemm_dgrad, "ufp4_gemm_dgrad", dyq, wtq, out)
+    return _dense("ufp4_gemm_dgrad", dyq, wtq, out)
 
 
 def ufp4_gemm_wgrad(dytq: Quantized, xtq: Quantized, out: Optional[torch.Tensor] = None,
@@ -318,7 +319,7 @@ def ufp4_gemm_wgrad(dytq: Quantized, xtq: Quantized, out: Optional[torch.Tensor]
     """dW = (dY^T)_hat (X^T)_hat^T, [F, H] FP32."""
     ws = _ptr(workspace)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    return _dense(lib().ufp4_gemm_wgrad, "ufp4_gemm_wgrad", dytq, xtq, out, ws, nbytes)
+    return _dense("ufp4_gemm_wgrad", dytq, xtq, out, ws, nbytes)
 
 
 def ufp4_grouped_gemm(kind: int, group_offsets: torch.Tensor, a: Quantized, b: Quantized,
@@ -338,10 +339,8 @@ def ufp4_grouped_gemm(kind: int, group_offsets: torch.Tensor, a: Quantized, b: Q
     da, db = a.desc(), b.desc()
     ws = _ptr(workspace)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib().ufp4_grouped_gemm(kind, n_groups, _ptr(group_offsets), ctypes.byref(da),
-                                 ctypes.byref(db), _ptr(out), ldc, ws, nbytes,
-                                 _stream(out.device))
-    _check(st, "ufp4_grouped_gemm")
+    _call("ufp4_grouped_gemm", out.device, kind, n_groups, _ptr(group_offsets), ctypes.byref(da),
+          ctypes.byref(db), _ptr(out), ldc, ws, nbytes)
     return out
 
 
@@ -357,9 +356,8 @@ def ufp4_gemm_out(kind: int, a: Quantized, b: Quantized, dtype=torch.bfloat16,
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
     assert out.dtype in _OUT_CODE and out.stride(1) == 1
     da, db = a.desc(), b.desc()
-    st = lib().ufp4_gemm_out(kind, ctypes.byref(da), ctypes.byref(db), _ptr(out),
-                             _OUT_CODE[out.dtype], out.stride(0), _stream(out.device))
-    _check(st, "ufp4_gemm_out")
+    _call("ufp4_gemm_out", out.device, kind, ctypes.byref(da), ctypes.byref(db), _ptr(out),
+          _OUT_CODE[out.dtype], out.stride(0))
     return out
 
 
@@ -375,10 +373,8 @@ def ufp4_grouped_gemm_out(kind: int, group_offsets: torch.Tensor, a: Quantized, 
         out = torch.empty(shape, dtype=dtype, device=a.codes.device)
     assert out.dtype in _OUT_CODE and out.is_contiguous()
     da, db = a.desc(), b.desc()
-    st = lib().ufp4_grouped_gemm_out(kind, n_groups, _ptr(group_offsets), ctypes.byref(da),
-                                     ctypes.byref(db), _ptr(out), _OUT_CODE[out.dtype], ldc,
-                                     _stream(out.device))
-    _check(st, "ufp4_grouped_gemm_out")
+    _call("ufp4_grouped_gemm_out", out.device, kind, n_groups, _ptr(group_offsets),
+          ctypes.byref(da), ctypes.byref(db), _ptr(out), _OUT_CODE[out.dtype], ldc)
     return out
 
 
