@@ -50,6 +50,9 @@ def _recipe(rht, sr_dy):
 class _LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, masks, grid, seed, rht, rnd_dy):
+        ctx.w_shape = w.shape
+        if x.shape[0] == 0:
+            return x.new_empty((0, w.shape[0]))
         mf, md, mw = masks
         rf, rd, rw = rht
         xq, xtq = U.ufp4_rht_quantize_dual(x, (rf, mf, 0), (rw, mw, 0), grid=grid)
@@ -65,7 +68,14 @@ class _LinearFn(torch.autograd.Function):
         return dx, dw, None, None, None, None, None
 
 
+def _no_rows(ctx, dy):
+    """The gradients of a product without rows, which the library does not take."""
+    return dy.new_empty((0, ctx.w_shape[1])), dy.new_zeros(ctx.w_shape)
+
+
 def _linear_grads(ctx, dy):
+    if dy.shape[0] == 0:
+        return _no_rows(ctx, dy)
     _, md, mw = ctx.masks
     _, rd, rw = ctx.rht
     dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
@@ -117,6 +127,9 @@ class UFP4Linear(torch.nn.Module):
 class _ExpertFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, n_experts, masks, grid, seed, rht, rnd_dy):
+        ctx.w_shape = w.shape
+        if x.shape[0] == 0:
+            return x.new_empty((0, w.shape[0] // n_experts))
         mf, md, mw = masks
         rf, rd, rw = rht
         xq, xtq = U.ufp4_rht_quantize_dual(x, (rf, mf, 0), (rw, mw, 0), grid=grid,
@@ -137,6 +150,8 @@ class _ExpertFn(torch.autograd.Function):
 
 
 def _expert_grads(ctx, dy):
+    if dy.shape[0] == 0:
+        return _no_rows(ctx, dy)
     _, md, mw = ctx.masks
     _, rd, rw = ctx.rht
     dyq, dytq = U.ufp4_rht_quantize_dual(_bf16_rows(dy), (rd, md, 0), (rw, mw, 1),
