@@ -33,3 +33,27 @@ def test_no_rows(lead):
         assert layer.weight.grad.shape == layer.weight.shape and not layer.weight.grad.any()
     with pytest.raises(TypeError):
         Y.UFP4Linear(8, 4)(torch.zeros((0, 8)))
+
+
+def test_gradients_that_arrive_broadcast(monkeypatch):
+    """Of a sum over the rows, dY is one row with stride 0, which the library
+    does not take as rows: it is written out."""
+    seen = []
+
+    def quantize(t, *a, **kw):
+        seen.append(t)
+        return t, t.t()
+
+    monkeypatch.setattr(Y.U, "ufp4_rht_quantize_dual", quantize)
+    for layer, more in ((Y.UFP4Linear(8, 4), ()),
+                        (Y.UFP4ExpertLinear(1, 8, 4), (torch.tensor([0, 5]),))):
+        for grad in (torch.ones((), dtype=torch.bfloat16).expand(5, 4),
+                     torch.arange(4).to(torch.bfloat16).expand(5, 4),
+                     torch.arange(5).to(torch.bfloat16)[:, None].expand(5, 4)):
+            x = torch.ones((5, 8), dtype=torch.bfloat16, requires_grad=True)
+            layer(x, *more).backward(grad)
+            dy = seen[-1]
+            assert dy.stride(1) == 1 and dy.stride(0) >= 4 and torch.equal(dy, grad)
+    wide = torch.ones((5, 20), dtype=torch.bfloat16)[:, 3:11]      # rows of any stride stay
+    Y.UFP4Linear(8, 4)(wide)
+    assert seen[-2].data_ptr() == wide.data_ptr()

@@ -37,8 +37,10 @@ def draw_sign_masks(seed: int):
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as rows with unit column stride that do not overlap (a broadcast
+    tensor, such as the gradient of a sum, is written out)."""
     t = t.reshape(-1, t.shape[-1])
-    return t if t.stride(-1) == 1 else t.contiguous()
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
 
 
 def _recipe(rht, sr_dy):

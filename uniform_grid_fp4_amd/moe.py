@@ -19,14 +19,7 @@ import torch
 from . import block as B
 from . import ufp4 as U
 from .autograd import first_order
-from .layers import UFP4ExpertLinear
-
-
-def _flat(t: torch.Tensor) -> torch.Tensor:
-    """t as rows with unit column stride that do not overlap (a broadcast
-    tensor, such as the gradient of a sum, is written out)."""
-    t = t.reshape(-1, t.shape[-1])
-    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+from .layers import UFP4ExpertLinear, _rows
 
 
 class _NormFn(torch.autograd.Function):
@@ -43,8 +36,8 @@ class _NormFn(torch.autograd.Function):
         h, weight, rstd = ctx.saved_tensors
         if dy is None:                               # only the stream itself was used
             return dh, dh, None, None
-        dx, dw = first_order(B.ufp4_rmsnorm_bwd, _flat(dy), h, weight, rstd,
-                             None if dh is None else _flat(dh))
+        dx, dw = first_order(B.ufp4_rmsnorm_bwd, _rows(dy), h, weight, rstd,
+                             None if dh is None else _rows(dh))
         return dx, (dx if ctx.summed else None), dw, None
 
 
@@ -89,7 +82,7 @@ class _CombineFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         ys, slots, gates = ctx.saved_tensors
-        dys, dg = first_order(B.ufp4_moe_combine_bwd, _flat(dy), ys, slots, gates)
+        dys, dg = first_order(B.ufp4_moe_combine_bwd, _rows(dy), ys, slots, gates)
         return dys, None, dg, (dy if ctx.summed else None)
 
 
@@ -105,15 +98,15 @@ class RMSNorm(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
         if residual is None:
-            return _NormFn.apply(_flat(x), None, self.weight, self.eps).reshape(x.shape)
-        y, h = _NormFn.apply(_flat(x), _flat(residual), self.weight, self.eps)
+            return _NormFn.apply(_rows(x), None, self.weight, self.eps).reshape(x.shape)
+        y, h = _NormFn.apply(_rows(x), _rows(residual), self.weight, self.eps)
         return y.reshape(x.shape), h.reshape(x.shape)
 
     @torch.no_grad()
     def quantized(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> B.NormOut:
         """For serving: the norm's rows in E4M3 with one scale each (q, scale),
         and the residual stream h; y itself is never written."""
-        return B.ufp4_rmsnorm(_flat(x), self.weight, None if residual is None else _flat(residual),
+        return B.ufp4_rmsnorm(_rows(x), self.weight, None if residual is None else _rows(residual),
                               eps=self.eps, y=False, q8=True)
 
 
@@ -130,19 +123,19 @@ class MoERouter(torch.nn.Module):
         self.k, self.renorm = k, renorm
 
     def forward(self, x: torch.Tensor, valid: Optional[torch.Tensor] = None) -> B.Routing:
-        logits = torch.nn.functional.linear(_flat(x), self.weight)
+        logits = torch.nn.functional.linear(_rows(x), self.weight)
         return B.Routing(*_RouteFn.apply(logits, self.k, valid, self.renorm), self.renorm)
 
 
 def dispatch(x: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     """`ufp4_moe_dispatch` with its gradient."""
-    return _DispatchFn.apply(_flat(x), slots)
+    return _DispatchFn.apply(_rows(x), slots)
 
 
 def combine(ys: torch.Tensor, slots: torch.Tensor, gates: torch.Tensor,
             residual: Optional[torch.Tensor] = None) -> torch.Tensor:
     """`ufp4_moe_combine` with its gradients."""
-    return _CombineFn.apply(ys, slots, gates, None if residual is None else _flat(residual))
+    return _CombineFn.apply(ys, slots, gates, None if residual is None else _rows(residual))
 
 
 class MoEOut(NamedTuple):
