@@ -7,8 +7,9 @@ The expert layers take tokens sorted by expert with device offsets.  Here the
 router makes both: its slots carry tokens to expert order and back, its offsets
 go to the grouped GEMMs, and nothing on the way waits for the GPU, so that a
 step's launches run ahead of it (and forward passes can be captured into a HIP
-graph).  Padding tokens and experts that are masked out (-inf) cost no expert
-work of their own; the rows left over are zero rows of the last expert.
+graph).  That takes static shapes: the rows of padding tokens, and of choices
+that do not exist where experts are masked out (-inf), are zero rows of the last
+expert, which quantizes and multiplies them as any others.
 """
 from __future__ import annotations
 
