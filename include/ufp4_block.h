@@ -49,8 +49,10 @@ extern "C" {
  *   y          dense [rows, cols], or NULL.
  *   q, scale   dense E4M3 (OCP) bytes [rows, cols] and FP32 [rows], or both
  *              NULL: scale = max|y| / 448 over the row's unrounded y, and
- *              q = round(y / scale), so |q| <= 448.  A zero row has scale 0
- *              and q 0; a row that holds an infinity or a NaN is NaN.
+ *              q = round(y / scale), so |q| <= 448, from FP32 values of y and
+ *              the quotient (an exact half step may go either way).  A zero
+ *              row has scale 0 and q 0; a row that holds an infinity or a
+ *              NaN is NaN.
  *   rstd       FP32 [rows].
  * At least one of y and q.  Returns OK, INVALID_ARG (null or misaligned
  * pointer, unknown type, eps negative or NaN), SHAPE, HIP.

@@ -5,9 +5,11 @@
 // written once, by threads that hold one 16-byte vector of a token's row and go
 // over its choices, so the token's own row is read once whatever k is, and the
 // sums (FP32, in the order of the choices) need no atomics.  16384 tokens, 6144
-// columns, k = 8, bf16, from HBM: dispatch 366 us (1.81 GB, 4.9 TB/s; 309 us with
-// x in the cache), combine with residual 363 us (2.01 GB, 5.5 TB/s), dispatch's
-// backward 305 us (1.81 GB, 5.9 TB/s), combine's 650 us (3.42 GB, 5.3 TB/s).
+// columns, k = 8, bf16, no padding, from HBM: dispatch 362 us (1.81 GB, 5.0 TB/s;
+// 310 us with x in the cache), combine with residual 384 us (2.01 GB, 5.2 TB/s),
+// dispatch's backward 320 us (1.81 GB, 5.7 TB/s), combine's 684 us (3.42 GB, 5.0
+// TB/s).  2048 columns, k = 6, FP32: 189, 201, 158 and 350 us (5.0, 5.3, 5.9 and
+// 5.0 TB/s).
 #include "block_device.h"
 #include "block_kernels.h"
 
@@ -32,7 +34,7 @@ struct Choices {
 // Units of work: LPT lanes take LPT vectors of one token's row.  A wave (64) per
 // unit keeps the token, its slots and every branch on them scalar; rows of up to
 // 16 vectors take a DPP row of lanes each, four tokens to a wave (31549 tokens
-// of 64 columns, k = 8, all four directions: 52 us, a workgroup per token 327 us).
+// of 64 columns, k = 8, all four directions: 53 us, a workgroup per token 327 us).
 template <int LPT>
 __device__ __forceinline__ int64_t first_unit() {
   int in = threadIdx.x / LPT;
@@ -46,8 +48,9 @@ __device__ __forceinline__ int64_t unit_step() {
 
 // Where a lane's vector starts: the one that passes the end of the row is taken
 // back to end with it, so that no lane goes element by element (24002 tokens of
-// 575 columns, k = 4, all four directions: 149 us, masked accesses 221 us).  Elements that two lanes then hold get the same
-// value from both.  Rows shorter than a vector keep the masked accesses.
+// 575 columns, k = 4, no padding, all four directions: 197 us, masked accesses
+// 285 us).  Elements that two lanes then hold get the same value from both.  Rows
+// shorter than a vector keep the masked accesses.
 template <int V>
 __device__ __forceinline__ int64_t vec_start(int64_t c, int64_t cols) {
   return cols >= V ? min(c, cols - V) : c;
@@ -129,8 +132,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const ExchangeArgs a, int6
 // LPT lanes per token at a time, LPT vectors of its row after the other: dys =
 // g dy in each choice's row, and the dot products of its row of ys with dy,
 // which is read once per KB choices.  Up to 192 vectors a wave does it without a
-// barrier (1408 columns, k = 6: 140 us, a workgroup 147 us); longer rows take a
-// workgroup (2048 columns: 163 us, a wave 187 us).
+// barrier (16384 tokens of 1408 columns, k = 6: 118 us, a workgroup 137 us);
+// longer rows take a workgroup (2048 columns: 175 us, a wave 188 us).
 template <typename T, int KB, int LPT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const ExchangeArgs a) {
   constexpr int V = Elem<T>::V;

@@ -6,8 +6,8 @@
 // b + grid, ...  Squares and sums are FP64: an FP32 square overflows at
 // 1.8e19 and a sum over 10^9 elements needs more than 24 bits.  The FP64
 // multiply-adds run at half the memory's pace or better, so both passes are
-// bound by memory: 201M bf16 elements (403 MB) are summed in 73 us (5.5 TB/s) and
-// scaled into another buffer in 134 us (805 MB, 6.0 TB/s, part of the input
+// bound by memory: 201M bf16 elements (403 MB) are summed in 70-73 us (5.6 TB/s)
+// and scaled into another buffer in 133 us (805 MB, 6.1 TB/s, part of the input
 // still cached).  Hundreds of small tensors are bound by the host, which lists
 // them: 432 tensors take 9 launches and 50 us of GPU time in a call of 250 us.
 #include "block_device.h"

@@ -5,9 +5,10 @@
 //   dw = sum over rows of dy xhat
 // About 12 operations per element forward and 16 backward against 6 to 10
 // bytes: bound by memory.  Sums are FP32 along a row (a lane's chain is a 64th
-// of it or less) and over the rows of dw; h is rounded once to the stream's
-// type, and the statistics are those of the rounded h that the backward sees;
-// y, q and the gradients are rounded once from FP32.
+// of it or less, and one vector in rows of up to 16 vectors) and over the rows
+// of dw; h is rounded once to the stream's type, and the statistics are those of
+// the rounded h that the backward sees; y, q and the gradients are rounded once
+// from FP32.
 #include "block_device.h"
 #include "block_kernels.h"
 
@@ -33,7 +34,9 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
   return s;
 }
 // Four values to four E4M3 bytes, nearest even.  |y| <= top gives at most
-// 448 (1 + 2^-22), which rounds to 448.
+// 448 (1 + 2^-22), which rounds to 448.  y and its product with 448 / top are
+// rounded to FP32 first, so a quotient that is half a step exactly, as one in some
+// 2000 of bf16 rows is, may go to either neighbour.
 __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * s.lift * s.inv, y[1] * s.lift * s.inv, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2] * s.lift * s.inv, y[3] * s.lift * s.inv, w,
@@ -46,10 +49,11 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *y, RowScale s) {
 // vector.  A row per workgroup at a time, with the hardware starting the next
 // workgroup as one ends: a grid that fills the GPU once and walks over rows with
 // the next row's loads in flight took 350 us where this takes 317 us (32768 x
-// 6144 bf16 with residual and E4M3), 305 us with streaming stores: 1.81 GB at
-// 5.9 TB/s, the rate that the fastest of these kernels reach; a plain copy of 2 GB
-// reaches 4.9 TB/s here.  8192 x 2048 takes 22-25 us (134 MB, 5.4-6.1 TB/s,
-// partly from the 256 MB cache), one row 3.3 us.
+// 6144 bf16 with residual and E4M3), 302 us with streaming stores: 1.81 GB at
+// 6.0 TB/s, the rate that the fastest of these kernels reach; a plain copy of 2 GB
+// reaches 4.9 TB/s here.  8192 x 2048 takes 23-28 us (134 MB, 4.8-5.8 TB/s,
+// partly from the 256 MB cache), 4096 x 12288 FP32 135 us (805 MB, 6.0 TB/s), one
+// row 3.2 us.
 // Sum / maximum over the TPR threads that hold a row: a DPP row, a wave, or the
 // workgroup.
 template <int TPR>
@@ -216,7 +220,8 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_kernel(const NormArgs
 }
 
 // One workgroup per row at a time, three passes over it; a thread reads back
-// only what it wrote itself.
+// only what it wrote itself.  4096 x 16384 FP32 with residual 254 us (1.07 GB,
+// 4.2 TB/s; the second pass hits the caches), 4096 x 32768 bf16 342 us.
 template <typename T, typename W>
 __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
   constexpr int V = Elem<T>::V;
@@ -288,7 +293,7 @@ __global__ __launch_bounds__(256) void rmsnorm_row_kernel(const NormArgs a) {
 // rows) and goes to partial[workgroup][cols] at the end, the four waves of a
 // wave-per-row workgroup added in wave order.  Reads dy, h and dh once: 8192 x
 // 2048 bf16 26 us and 4 us for dw's second half (134 MB, 4.5 TB/s); 16384 x
-// 6144 162 us (805 MB, 5.0 TB/s), bound by memory.  Loading the next row ahead
+// 6144 163 and 6 us (805 MB, 4.8 TB/s), bound by memory.  Loading the next row ahead
 // changed nothing (the other workgroup of the CU covers the wait).
 template <typename T, typename W, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
@@ -385,7 +390,9 @@ __global__ __launch_bounds__(group_size(TPR)) void rmsnorm_bwd_kernel(const Norm
   }
 }
 
-// dx: one workgroup per row at a time, two passes.
+// dx: one workgroup per row at a time, two passes.  With dw's own pass over dy
+// and h before it, the backward of 4096 x 16384 FP32 takes 138 + 265 + 5 us (1.07
+// GB, 2.6 TB/s), of 4096 x 32768 bf16 163 + 376 + 9 us.
 template <typename T, typename W>
 __global__ __launch_bounds__(256) void rmsnorm_bwd_row_kernel(const NormBwdArgs a) {
   constexpr int V = Elem<T>::V;

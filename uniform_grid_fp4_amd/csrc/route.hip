@@ -13,11 +13,13 @@
 // counts over the workgroups and sums their probabilities, a third turns
 // places into rows.  Few tokens (one workgroup) take a single launch.
 //
-// 65536 x 256 bf16 logits, top 8 (34 MB): choices 28 us, of which the k rounds
-// take 9 us and instruction issue most of the rest (about 600 vector
-// instructions for four tokens), scan 6.7 us, places 5.8 us; backward 17 us for
-// 67 MB (3.9 TB/s).  16384 x 64 FP32, top 6: 7.2, 3.2, 4.2 and 4.8 us, one token
-// 4.6 us: latency and launches.
+// 65536 x 256 bf16 logits, top 8, an eighth of the tokens padding: choices 28 us
+// for 29 MB, bound by instruction issue (870 vector instructions for a wave's
+// four tokens, 14.3M in all: 23 us on 1024 SIMDs), scan 6.4 us, places 5.8 us;
+// backward 16 us for 63 MB (3.9 TB/s).  The same in FP32, whose rounds take two
+// row reductions each: 50 us (1320 instructions), 6.4, 6.1, and 22 us for 126 MB
+// (5.7 TB/s).  16384 x 64 FP32, top 6: 7.0, 3.2, 4.2 and 5.1 us, in bf16 6.5, 3.4,
+// 4.4 and 5.3 us, one token 4.5 us: latency and launches.
 //
 // Sums over a row are FP32; sums of p over tokens are FP32 within a workgroup
 // and FP64 across, z and the losses FP64.
