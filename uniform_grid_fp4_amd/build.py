@@ -16,7 +16,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libufp4.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "stats.hip",
-           "block_api.hip", "rmsnorm.hip", "route.hip", "exchange.hip", "gradnorm.hip"]
+           "block_api.hip", "rmsnorm.hip", "route.hip", "exchange.hip", "gradnorm.hip",
+           "ffn_api.hip", "layernorm.hip", "dropout.hip", "gated_bwd.hip", "int8_quantize.hip",
+           "int8_gemm.hip"]
 # The bench's MFMA issue-rate probe: a separate library, not part of the ABI.
 PROBE_LIB = os.path.join(HERE, "libufp4_probe.so")
 PROBE_SOURCES = ["probe.hip"]
@@ -58,7 +60,7 @@ def _compile(sources, out, verbose):
     with tempfile.TemporaryDirectory() as tmp:
         objs = [os.path.join(tmp, s + ".o") for s in sources]
         base = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
-        with ThreadPoolExecutor(max_workers=min(4, len(sources))) as pool:
+        with ThreadPoolExecutor(max_workers=min(8, len(sources))) as pool:
             list(pool.map(lambda so: _run([*base, "-c", os.path.join(CSRC, so[0]), "-o", so[1]],
                                           verbose), zip(sources, objs)))
         _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", out + ".tmp"],

@@ -3,7 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/ufp4.h"
+#include "../../include/ufp4_ffn.h"
 #include "ufp4_kernels.h"
 
 using namespace ufp4;
@@ -349,6 +349,47 @@ ufp4_status ufp4_grouped_gemm_out(int32_t kind, int32_t n_groups, const int64_t 
   }
   if (ldc < g.N) return UFP4_ERR_SHAPE;
   return launch_gemm(g, stream) == hipSuccess ? UFP4_OK : UFP4_ERR_HIP;
+}
+
+ufp4_status ufp4_gated_gemm(const ufp4_qtensor *x, const ufp4_qtensor *w, int32_t act,
+                            int32_t n_groups, const int64_t *d_group_offsets, int32_t out_dtype,
+                            void *y, int64_t ld_y, void *gu, int64_t ld_gu, hipStream_t stream) {
+  if (act != UFP4_ACT_SILU && act != UFP4_ACT_GELU) return UFP4_ERR_INVALID_ARG;
+  if (out_dtype != UFP4_OUT_F32 && out_dtype != UFP4_OUT_BF16) return UFP4_ERR_INVALID_ARG;
+  const uintptr_t odd = out_dtype == UFP4_OUT_BF16 ? 1u : 3u;
+  if (y == nullptr || (reinterpret_cast<uintptr_t>(y) & odd) != 0 ||
+      (reinterpret_cast<uintptr_t>(gu) & odd) != 0)
+    return UFP4_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > kMaxGroupsApi || (d_group_offsets == nullptr && n_groups != 1))
+    return UFP4_ERR_SHAPE;
+  const ufp4_status s = check_pair(x, w);
+  if (s != UFP4_OK) return s;
+  if (x->kpad > kGatedMaxK) return UFP4_ERR_UNSUPPORTED;
+  if (w->rows % (2 * (int64_t)n_groups) != 0) return UFP4_ERR_SHAPE;
+  GemmArgs g{};
+  g.a_codes = x->codes;
+  g.a_scales = x->scales;
+  g.b_codes = w->codes;
+  g.b_scales = w->scales;
+  g.M = x->rows;
+  g.N = w->rows / (2 * (int64_t)n_groups);
+  g.kpad = x->kpad;
+  g.c = y;
+  g.ldc = ld_y;
+  g.out_bf16 = out_dtype == UFP4_OUT_BF16;
+  g.mode = d_group_offsets != nullptr ? 1 : 0;
+  g.goff = d_group_offsets;
+  g.n_groups = n_groups;
+  g.grid = x->grid;
+  g.n_split = 1;
+  g.split_kb = x->kpad / 16;
+  g.act = act;
+  g.gu = gu;
+  g.ld_gu = ld_gu;
+  constexpr int64_t kMaxSpan = int64_t(1) << 60;     // elements from the first row to the last
+  if (ld_y < g.N || ld_y > kMaxSpan / g.M) return UFP4_ERR_SHAPE;
+  if (gu != nullptr && (ld_gu < 2 * g.N || ld_gu > kMaxSpan / g.M)) return UFP4_ERR_SHAPE;
+  return launch_gated_gemm(g, stream) == hipSuccess ? UFP4_OK : UFP4_ERR_HIP;
 }
 
 static_assert(sizeof(ufp4_stats) == sizeof(StatsPartial), "ufp4_stats layout");

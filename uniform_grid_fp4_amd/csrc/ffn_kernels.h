@@ -1,0 +1,104 @@
+// Host-side launch interface between the C ABI of the feed-forward operators
+// (ffn_api.hip) and their kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ufp4_ffn.h"
+
+namespace ufp4 {
+
+struct LayerNormArgs {
+  const void *x;
+  int64_t ld_x;
+  const void *res;          // nullptr: none
+  int64_t ld_res;
+  const void *w, *b;        // b nullptr: none
+  int bf16, w_bf16;         // element types of the rows and of the weight and bias
+  int64_t rows, cols;
+  float eps;
+  void *h;                  // written when there is a residual
+  void *y;
+  float *mean, *rstd;
+  bool stream;              // h and y by streaming stores
+};
+hipError_t launch_layernorm(const LayerNormArgs &a, hipStream_t st);
+
+struct LayerNormBwdArgs {
+  const void *dy;
+  int64_t ld_dy;
+  const void *h;
+  int64_t ld_h;
+  const void *w;
+  const float *mean, *rstd;
+  const void *dh;           // nullptr: none
+  int64_t ld_dh;
+  int bf16, w_bf16;
+  int64_t rows, cols;
+  void *dx;
+  bool stream;              // dx by streaming stores
+  void *dw, *db;            // db nullptr: not wanted
+  float *partial;           // [layernorm_bwd_slices(rows, cols), 2, cols]: dw's and db's sums
+};
+int layernorm_bwd_slices(int64_t rows, int64_t cols);
+hipError_t launch_layernorm_bwd(const LayerNormBwdArgs &a, hipStream_t st);
+
+struct DropoutArgs {
+  const void *x;
+  int64_t ld_x;
+  const void *res;          // nullptr: none
+  int64_t ld_res;
+  int bf16;
+  int64_t rows, cols;
+  uint32_t limit;           // an element stays if its 16 bits are at least this; 65536: none does
+  float scale;
+  uint64_t seed, offset;
+  const int64_t *d_offset;  // nullptr: 0
+  void *y;
+  bool stream;              // y by streaming stores
+};
+hipError_t launch_dropout(const DropoutArgs &a, hipStream_t st);
+
+struct GatedBwdArgs {
+  const void *dy;
+  int64_t ld_dy;
+  const void *gu;
+  int64_t ld_gu;
+  int act, bf16;
+  int64_t rows, cols;
+  void *dgu;
+  bool stream;
+};
+hipError_t launch_gated_bwd(const GatedBwdArgs &a, hipStream_t st);
+
+struct Int8QuantArgs {
+  const void *x;
+  int64_t ld_x;
+  int bf16;
+  int64_t rows, cols, kpad;
+  int8_t *q;
+  float *scale;
+};
+hipError_t launch_int8_quantize(const Int8QuantArgs &a, hipStream_t st);
+
+struct Int8GemmArgs {
+  const int8_t *a, *w;
+  const float *sa, *sw;
+  const float *bias;        // nullptr: none
+  int64_t M, N, kpad;       // N rows of w per group
+  int act;                  // gated: the output has N / 2 columns
+  int n_groups;
+  const int64_t *goff;      // nullptr: one group of all rows
+  int out_bf16;
+  void *y;
+  int64_t ld_y;
+};
+hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st);
+
+constexpr int kMaxFfnGroups = 1024;
+constexpr int64_t kInt8MaxK = 131071;   // 128 * 128 * k stays below 2^31
+constexpr int64_t kInt8KAlign = 128;
+inline int64_t int8_kpad(int64_t k) { return (k + kInt8KAlign - 1) / kInt8KAlign * kInt8KAlign; }
+
+}  // namespace ufp4

@@ -48,11 +48,19 @@
 // tile's FP32 sums are added to its outputs (read back by the same lanes),
 // so the error of the FP32 running sum stays that of a 65536-long chain
 // whatever K is; shorter contractions write once and are unchanged.
+//
+// GATED: the product act(x Wg^T) * (x Wu^T) of two projections in one kernel.
+// A wave's two 32x32 tiles are then the gate's and the up projection's of the
+// same 32 columns (the workgroup's 128 rows of B are 64 of either, in runs of
+// 32), so gate and up values meet in the same lane and register and the
+// activation and the product are an epilogue of two operands in registers.  The
+// K loop is the same, and so are g and u bit for bit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
 
+#include "act_device.h"
 #include "ufp4_device.h"
 #include "ufp4_kernels.h"
 
@@ -109,6 +117,7 @@ __device__ __forceinline__ uint2 nib8_to_fp8(uint32_t w) {
 struct TileJob {
   int64_t a_row0, a_rows;   // A rows [a_row0, a_row0 + a_rows)
   int64_t b_row0, b_rows;
+  int64_t b_row1;           // GATED: the up projection's rows begin here (b_rows of them too)
   int64_t kb0, kb1;         // block range [kb0, kb1)
   int64_t c_off;            // element offset of C(0, 0) of the tile
 };
@@ -126,13 +135,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, n, 0x00020000);
 }
 
-template <int GRID>
+template <int GRID, bool GATED>
 struct Gemm {
   const GemmArgs &g;
   TileJob job;
   __amdgpu_buffer_rsrc_t ra_q, ra_s, rb_q, rb_s;
   int nkb;     // blocks in [kb0, kb1)
   int oq, os;  // this thread's (row, block) item at stage 0: code and scale byte offsets
+  int bq, bs;  // and its item of B
 
   __device__ Gemm(const GemmArgs &args, const TileJob &j) : g(args), job(j) {
     const int64_t kblocks = g.kpad / 16;
@@ -140,8 +150,14 @@ struct Gemm {
     // rows past the tile read as zero.
     ra_q = make_rsrc(g.a_codes + job.a_row0 * (g.kpad / 2), job.a_rows * (g.kpad / 2));
     ra_s = make_rsrc(g.a_scales + job.a_row0 * kblocks, job.a_rows * kblocks * 4);
-    rb_q = make_rsrc(g.b_codes + job.b_row0 * (g.kpad / 2), job.b_rows * (g.kpad / 2));
-    rb_s = make_rsrc(g.b_scales + job.b_row0 * kblocks, job.b_rows * kblocks * 4);
+    int64_t b_row0 = job.b_row0;
+    if (GATED) {
+      // 16 rows a wave: the same projection for all of it
+      const int up = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> (kSBLog + 5)) & 1);
+      if (up) b_row0 = job.b_row1;
+    }
+    rb_q = make_rsrc(g.b_codes + b_row0 * (g.kpad / 2), job.b_rows * (g.kpad / 2));
+    rb_s = make_rsrc(g.b_scales + b_row0 * kblocks, job.b_rows * kblocks * 4);
     nkb = (int)(job.kb1 - job.kb0);
     int row = threadIdx.x >> kSBLog;
     const int blk = threadIdx.x & (kSB - 1);
@@ -151,6 +167,14 @@ struct Gemm {
     asm volatile("" : "+v"(row));
     oq = (int)(row * (g.kpad / 2) + (job.kb0 + blk) * 8);
     os = (int)((row * kblocks + job.kb0 + blk) * 4);
+    if (GATED) {
+      const int col = (row >> 6) * 32 + (row & 31);      // of the projection's 64
+      bq = (int)(col * (g.kpad / 2) + blk * 8);
+      bs = (int)((col * kblocks + blk) * 4);
+    } else {
+      bq = oq;
+      bs = os;
+    }
   }
 
   // Global loads of stage st (blocks kb0 + st*kSB ...).  Full stages put the
@@ -158,11 +182,13 @@ struct Gemm {
   // per-lane range test (offsets past the resource read as zero).
   __device__ __forceinline__ void load(Regs &r, int st) const {
     const int kbs = st * kSB;
-    int vq = oq, vs = os, sq = kbs * 8, ss = kbs * 4;
+    int vq = oq, vs = os, wq = bq, ws = bs, sq = kbs * 8, ss = kbs * 4;
     if (kbs + kSB > nkb) {
       const bool ok = kbs + (int)(threadIdx.x & (kSB - 1)) < nkb;
       vq = ok ? oq + sq : 0x7FFFFFF8;
       vs = ok ? os + ss : 0x7FFFFFF8;
+      wq = ok ? bq + sq : 0x7FFFFFF8;
+      ws = ok ? bs + ss : 0x7FFFFFF8;
       sq = 0;
       ss = 0;
     }
@@ -173,9 +199,9 @@ struct Gemm {
     const auto a = __builtin_amdgcn_raw_buffer_load_b64(ra_q, vq, sq, 0);
     r.aq[0] = make_uint2(a[0], a[1]);
     r.as[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra_s, vs, ss, 0));
-    const auto b = __builtin_amdgcn_raw_buffer_load_b64(rb_q, vq, sq, 0);
+    const auto b = __builtin_amdgcn_raw_buffer_load_b64(rb_q, wq, sq, 0);
     r.bq[0] = make_uint2(b[0], b[1]);
-    r.bs[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb_s, vs, ss, 0));
+    r.bs[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb_s, ws, ss, 0));
   }
 
   __device__ __forceinline__ static void store(const Regs &r, Stage &s) {
@@ -267,7 +293,59 @@ struct Gemm {
         flushed = true;
       }
     }
-    put<false>(acc, flushed);
+    if constexpr (GATED) put_gated(acc);
+    else put<false>(acc, flushed);
+  }
+
+  // Writes y = act(g) * u, and g and u themselves where they are wanted, from
+  // the FP32 sums of the two projections: acc[0] and acc[1] of the same column.
+  // There are no chunks of K here (the call takes K up to one chunk).
+  __device__ __forceinline__ void put_gated(floatx16 (&acc)[kNT]) {
+    constexpr float g2 = (GRID == kGridUniform) ? 49.0f : (GRID == kGridE2M1) ? 144.0f : 16.0f;
+    constexpr float inv_g2 = 1.0f / g2;
+    int tid = threadIdx.x;
+    int64_t ldc = g.ldc, ldg = g.ld_gu, row0 = job.a_row0, c_off = job.c_off;
+    int64_t a_rows = job.a_rows, b_rows = job.b_rows;
+    // formed here and not held across the K loop, as in put()
+    asm volatile("" : "+v"(tid), "+s"(ldc), "+s"(ldg), "+s"(row0), "+s"(c_off), "+s"(a_rows),
+                 "+s"(b_rows));
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int wm = wave % kWavesM, wn = wave / kWavesM;
+    const int m0 = wm * 32 + 4 * (lane >> 5);
+    const int n0 = wn * 32 + (lane & 31);
+    const int mrem = (int)a_rows - m0;
+    if (n0 >= (int)b_rows) return;
+    const int64_t off = (row0 + m0) * ldc + c_off + n0;
+    const int64_t goff = (row0 + m0) * ldg + c_off + n0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int dm = 8 * (r >> 2) + (r & 3);
+      if (dm >= mrem) continue;
+      const float gate = acc[0][r] * inv_g2, up = acc[1][r] * inv_g2;
+      const float y = up * (g.act == UFP4_ACT_SILU ? act_value<UFP4_ACT_SILU>(gate)
+                                                   : act_value<UFP4_ACT_GELU>(gate));
+      if (g.out_bf16) {
+        __builtin_nontemporal_store(bf16_bits(y), static_cast<uint16_t *>(g.c) + off + dm * ldc);
+        if (g.gu != nullptr) {
+          uint16_t *p = static_cast<uint16_t *>(g.gu) + goff + dm * ldg;
+          __builtin_nontemporal_store(bf16_bits(gate), p);
+          __builtin_nontemporal_store(bf16_bits(up), p + g.N);
+        }
+      } else {
+        __builtin_nontemporal_store(y, static_cast<float *>(g.c) + off + dm * ldc);
+        if (g.gu != nullptr) {
+          float *p = static_cast<float *>(g.gu) + goff + dm * ldg;
+          __builtin_nontemporal_store(gate, p);
+          __builtin_nontemporal_store(up, p + g.N);
+        }
+      }
+    }
+  }
+
+  // Nearest even, NaN kept.
+  __device__ __forceinline__ static uint16_t bf16_bits(float f) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
   }
 
   // Writes acc / g^2 to the tile's outputs, or adds it to what an earlier
@@ -354,14 +432,14 @@ __device__ __forceinline__ int64_t clampv(int64_t v, int64_t n) {
 // access leaves the operands whatever the device array holds; a decreasing
 // pair is an empty group), s_pre = prefix of per-group tile counts (mode 1) or
 // of padded K lengths (mode 2).
-template <int MODE>
+template <int MODE, int BN>
 __device__ void load_gemm_groups(const GemmArgs &g, int64_t *s_off, int64_t *s_pre,
                                  int64_t *s_scan, int *s_order) {
   const int tid = threadIdx.x;
   const int ng = g.n_groups;
   const int per = (ng + kThreads - 1) / kThreads;
   const int g0 = tid * per;
-  const int64_t tiles_n = (g.N + kBN - 1) / kBN;
+  const int64_t tiles_n = (g.N + BN - 1) / BN;
   const int64_t limit = (MODE == 1) ? g.M : (int64_t)1 << 40;
   int64_t local = 0;
   for (int e = g0; e < g0 + per && e < ng; ++e) {
@@ -425,7 +503,7 @@ __device__ __forceinline__ void band_tile(int64_t local, int64_t tiles_m, int64_
   tm = band * kBand + (r - q * rows);
 }
 
-template <int GRID, int MODE>
+template <int GRID, int MODE, bool GATED = false>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
                           amdgpu_waves_per_eu(4, 4))) void gemm_kernel(GemmArgs g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -435,10 +513,12 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
   int64_t *s_scan = s_pre + (kMaxGemmGroups + 1);
   int *s_order = reinterpret_cast<int *>(s_scan + kThreads);
 
+  static_assert(!GATED || MODE != 2, "gated products are not grouped along K");
+  constexpr int BN = GATED ? kBN / 2 : kBN;      // output columns of a tile
   const int64_t tiles_m = (g.M + kBM - 1) / kBM;
-  const int64_t tiles_n = (g.N + kBN - 1) / kBN;
+  const int64_t tiles_n = (g.N + BN - 1) / BN;
   const int64_t kblocks = g.kpad / 16;
-  if (MODE != 0) load_gemm_groups<MODE>(g, s_off, s_pre, s_scan, s_order);
+  if (MODE != 0) load_gemm_groups<MODE, BN>(g, s_off, s_pre, s_scan, s_order);
 
   int64_t total;
   if (MODE == 0) total = tiles_m * tiles_n * g.n_split;
@@ -481,11 +561,16 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
       band_tile(local, tiles_m, tiles_n_t, tm, tn);
       job.a_row0 = tm * kBM;
       job.a_rows = min((int64_t)kBM, g.M - job.a_row0);
-      job.b_row0 = tn * kBN;
-      job.b_rows = min((int64_t)kBN, g.N - job.b_row0);
+      job.b_row0 = tn * BN;
+      job.b_rows = min((int64_t)BN, g.N - job.b_row0);
       job.kb0 = min(sp * g.split_kb, kblocks_t);
       job.kb1 = min(job.kb0 + g.split_kb, kblocks_t);
-      job.c_off = sp * g.split_stride + job.a_row0 * g.ldc + job.b_row0;
+      if (GATED) {
+        job.b_row1 = g.N + job.b_row0;
+        job.c_off = job.b_row0;                  // the column: y and gu have strides of their own
+      } else {
+        job.c_off = sp * g.split_stride + job.a_row0 * g.ldc + job.b_row0;
+      }
     } else if (MODE == 1) {
       int lo = 0, hi = g.n_groups;   // largest e with s_pre[e] <= t
       while (hi - lo > 1) {
@@ -498,11 +583,16 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
       band_tile(local, (s_pre[e + 1] - s_pre[e]) / tiles_n_t, tiles_n_t, tm, tn);
       job.a_row0 = s_off[e] + tm * kBM;
       job.a_rows = min((int64_t)kBM, s_off[e + 1] - job.a_row0);
-      job.b_row0 = (int64_t)e * g.N + tn * kBN;
-      job.b_rows = min((int64_t)kBN, g.N - tn * kBN);
+      job.b_row0 = (int64_t)e * (GATED ? 2 : 1) * g.N + tn * BN;
+      job.b_rows = min((int64_t)BN, g.N - tn * BN);
       job.kb0 = 0;
       job.kb1 = kblocks;
-      job.c_off = job.a_row0 * g.ldc + tn * kBN;
+      if (GATED) {
+        job.b_row1 = job.b_row0 + g.N;
+        job.c_off = tn * BN;
+      } else {
+        job.c_off = job.a_row0 * g.ldc + tn * BN;
+      }
     } else {
       const int64_t per_group = tiles_m * tiles_n_t;
       const int64_t slot = t / per_group;
@@ -524,11 +614,12 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
       job.a_rows = wave_uniform(job.a_rows);
       job.b_row0 = wave_uniform(job.b_row0);
       job.b_rows = wave_uniform(job.b_rows);
+      if (GATED) job.b_row1 = wave_uniform(job.b_row1);
       job.kb0 = wave_uniform(job.kb0);
       job.kb1 = wave_uniform(job.kb1);
       job.c_off = wave_uniform(job.c_off);
     }
-    Gemm<GRID> gm(g, job);
+    Gemm<GRID, GATED> gm(g, job);
     gm.run(stages);
     __syncthreads();
   }
@@ -541,7 +632,7 @@ static size_t smem_bytes(int mode) {
   return b;
 }
 
-template <int GRID, int MODE>
+template <int GRID, int MODE, bool GATED = false>
 static hipError_t launch_t(const GemmArgs &g, int64_t blocks, hipStream_t st) {
   const size_t sm = smem_bytes(MODE);
   // The dynamic-LDS limit is a per-device function attribute: set it once on
@@ -553,13 +644,29 @@ static hipError_t launch_t(const GemmArgs &g, int64_t blocks, hipStream_t st) {
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
   if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
-    e = hipFuncSetAttribute((const void *)gemm_kernel<GRID, MODE>,
+    e = hipFuncSetAttribute((const void *)gemm_kernel<GRID, MODE, GATED>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != hipSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  hipLaunchKernelGGL((gemm_kernel<GRID, MODE>), dim3((unsigned)blocks), dim3(kThreads), sm, st, g);
+  hipLaunchKernelGGL((gemm_kernel<GRID, MODE, GATED>), dim3((unsigned)blocks), dim3(kThreads), sm,
+                     st, g);
   return hipGetLastError();
+}
+
+template <int GRID>
+static hipError_t launch_gated_t(const GemmArgs &g, int64_t blocks, hipStream_t st) {
+  return g.mode == 0 ? launch_t<GRID, 0, true>(g, blocks, st)
+                     : launch_t<GRID, 1, true>(g, blocks, st);
+}
+static_assert(kGatedMaxK == kFlushStages * kSB * 16, "a gated product has one chunk of K");
+hipError_t launch_gated_gemm(const GemmArgs &g, hipStream_t st) {
+  const int64_t tiles_m = (g.M + kBM - 1) / kBM + (g.mode == 0 ? 0 : g.n_groups);
+  const int64_t total = tiles_m * ((g.N + kBN / 2 - 1) / (kBN / 2));
+  const int64_t blocks = total < 65536 ? total : 65536;
+  if (g.grid == kGridUniform) return launch_gated_t<kGridUniform>(g, blocks, st);
+  if (g.grid == kGridE2M1) return launch_gated_t<kGridE2M1>(g, blocks, st);
+  return launch_gated_t<kGridE2M1Max2>(g, blocks, st);
 }
 
 // Deterministic split-K sum: c[m, n] = sum over s = 0, 1, ... of the

@@ -104,9 +104,16 @@ struct GemmArgs {
   int n_split;
   int64_t split_kb;
   int64_t split_stride;
+  // gated product: B has 2 N rows (per group), c is act(g) * u, and gu (g | u)
+  // with row stride ld_gu, or nullptr
+  int act;
+  void *gu;
+  int64_t ld_gu;
 };
 
 hipError_t launch_gemm(const GemmArgs &g, hipStream_t st);
+constexpr int64_t kGatedMaxK = 65536;
+hipError_t launch_gated_gemm(const GemmArgs &g, hipStream_t st);
 
 // Split-K of a dense GEMM whose output tiles do not fill the GPU: partial
 // outputs of the K splits in the FP32 workspace ws [n_split, M, N], then a
