@@ -114,8 +114,8 @@ ufp4_status ufp4_gated_bwd(const void *dy, int64_t ld_dy, const void *gu, int64_
 
 /* ------------------------------------------------------------------------
  * Rows in 8-bit integers with one scale each.
- *   scale = max|x| / 127 over the row, q = round(x * (127 / max|x|)), to
- *   nearest even, FP32 operations; |q| <= 127.
+ *   scale = max|x| / 127 over the row, q = round(x * (127 * (1 / max|x|))),
+ *   to nearest even, each operation rounded to FP32; |q| <= 127.
  * q is dense [rows, kpad] with kpad = cols rounded up to a multiple of 128,
  * zero past the row's end.  A zero row has scale 0 and q 0.  A row that holds
  * an infinity or a NaN has scale NaN and q 0, so that its products are NaN.

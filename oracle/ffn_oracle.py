@@ -113,9 +113,10 @@ def int8_quantize(x):
     top = np.abs(x).max(1, initial=0)
     bad = ~np.isfinite(top)
     t = np.where(bad, np.float32(0), top).astype(np.float32)
-    lift = np.where(t < np.float32(2.0 ** -64), np.float32(2.0 ** 64), np.float32(1))
+    lift = np.where(t < np.float32(2.0 ** -64), np.float32(2.0 ** 64),
+                    np.where(t > np.float32(2.0 ** 64), np.float32(2.0 ** -64), np.float32(1)))
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
-        inv = np.where(t > 0, np.float32(127) / (t * lift), np.float32(0)).astype(np.float32)
+        inv = np.where(t > 0, np.float32(127) * (np.float32(1) / (t * lift)), np.float32(0)).astype(np.float32)
         codes = np.rint(np.where(bad[:, None], np.float32(0), x * lift[:, None] * inv[:, None]))
     scale = np.where(bad, np.float32(np.nan), t / np.float32(127)).astype(np.float32)
     return np.where(bad[:, None], 0, codes).astype(np.int64), scale

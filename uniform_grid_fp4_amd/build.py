@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libufp4.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "stats.hip",
            "block_api.hip", "rmsnorm.hip", "route.hip", "exchange.hip", "gradnorm.hip",
-           "ffn_api.hip", "layernorm.hip", "dropout.hip", "gated_bwd.hip", "int8_quantize.hip",
-           "int8_gemm.hip"]
+           "ffn_api.hip", "layernorm.hip", "dropout.hip", "gated_small.hip", "gated_bwd.hip",
+           "int8_quantize.hip", "int8_gemm.hip"]
 # The bench's MFMA issue-rate probe: a separate library, not part of the ABI.
 PROBE_LIB = os.path.join(HERE, "libufp4_probe.so")
 PROBE_SOURCES = ["probe.hip"]

@@ -14,24 +14,29 @@ struct ActPair {
   float value, slope;
 };
 
-// 1 / x to nearest but for a last bit: the hardware's reciprocal (within one
-// step) and one Newton step.  x in [1, inf].
-__device__ __forceinline__ float recip(float x) {
-  const float r = __builtin_amdgcn_rcpf(x);
-  const float e = __builtin_fmaf(-x, r, 1.0f);
-  return x < 0x1p126f ? __builtin_fmaf(e, r, r) : r;
+// p = 1 / (1 + exp(-g)) within 4 steps.  exp(-g) = 2^n 2^f with -g log2(e) = n +
+// f, f taken from the product's two halves (log2(e) as two floats), so that no
+// digit is lost in a large g; the exponential and the reciprocal are the
+// hardware's, within a step.  Beyond 104 either way p is 1 or 0 (or NaN).
+__device__ __forceinline__ float sigmoid(float g) {
+  const float c = __builtin_amdgcn_fmed3f(g, -104.0f, 104.0f);
+  const float n = __builtin_rintf(c * -1.4426950216293335f);
+  float f = __builtin_fmaf(c, -1.4426950216293335f, -n);
+  f = __builtin_fmaf(c, -1.925963e-8f, f);
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+  return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float g) {
-  if (ACT == UFP4_ACT_SILU) return g * recip(1.0f + expf(-g));
+  if (ACT == UFP4_ACT_SILU) return g * sigmoid(g);
   return g * (0.5f * erfcf(-0.70710678118654752f * g));
 }
 
 template <int ACT>
 __device__ __forceinline__ ActPair act_pair(float g) {
   if (ACT == UFP4_ACT_SILU) {
-    const float p = recip(1.0f + expf(-g));
+    const float p = sigmoid(g);
     return {g * p, p * (1.0f + g * (1.0f - p))};
   }
   const float c = 0.5f * erfcf(-0.70710678118654752f * g);

@@ -54,7 +54,7 @@
 // same 32 columns (the workgroup's 128 rows of B are 64 of either, in runs of
 // 32), so gate and up values meet in the same lane and register and the
 // activation and the product are an epilogue of two operands in registers.  The
-// K loop is the same, and so are g and u bit for bit.
+// K loop is the same, and so are g and u bit for bit.  Few tiles go to gated_small.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -99,20 +99,6 @@ struct Stage {
   float sa[kSB * (kBM + 16)];
   float sb[kSB * (kBN + 16)];
 };
-
-// 8 nibbles -> 8 FP8 E4M3 bytes.  Output byte order [n0 n2 n4 n6 | n1 n3 n5
-// n7]; A and B use the same order, so products still pair up.
-template <int GRID>
-__device__ __forceinline__ uint2 nib8_to_fp8(uint32_t w) {
-  constexpr uint32_t lut_lo = 0x44403800u;  // 0, 1, 2, 3
-  constexpr uint32_t lut_hi = (GRID == kGridUniform) ? 0x4E4C4A48u   // 4, 5, 6, 7
-                                                     : 0x54504C48u;  // 4, 6, 8, 12
-  const uint32_t me = w & 0x07070707u;
-  const uint32_t mo = (w >> 4) & 0x07070707u;
-  const uint32_t fe = __builtin_amdgcn_perm(lut_hi, lut_lo, me) | ((w << 4) & 0x80808080u);
-  const uint32_t fo = __builtin_amdgcn_perm(lut_hi, lut_lo, mo) | (w & 0x80808080u);
-  return make_uint2(fe, fo);
-}
 
 struct TileJob {
   int64_t a_row0, a_rows;   // A rows [a_row0, a_row0 + a_rows)
@@ -660,7 +646,20 @@ static hipError_t launch_gated_t(const GemmArgs &g, int64_t blocks, hipStream_t 
                      : launch_t<GRID, 1, true>(g, blocks, st);
 }
 static_assert(kGatedMaxK == kFlushStages * kSB * 16, "a gated product has one chunk of K");
+// Tiles of bm rows and bn columns, taking the groups' rows to be even.
+static int64_t gated_tiles(const GemmArgs &g, int bm, int bn) {
+  const int64_t rows = (g.M + g.n_groups - 1) / g.n_groups;
+  return g.n_groups * ((rows + bm - 1) / bm) * ((g.N + bn - 1) / bn);
+}
 hipError_t launch_gated_gemm(const GemmArgs &g, hipStream_t st) {
+  // A 32 x 32 tile of the kernel for few tiles costs 0.043 us of the whole GPU at K
+  // = 2048, a 128 x 64 tile 0.14 us, but no less than 42 us together, the time of
+  // one tile (257 x 333 columns, K = 1000: 7.2 and 45.6 us; 128 x 8192, K = 2048:
+  // 45 and 45 us; 512 x 8192: 168 and 76 us; 128 rows over 32 experts of 2048 columns, K = 6144: 211
+  // and 387 us).
+  const int64_t few = gated_tiles(g, 32, 32), tiles = gated_tiles(g, kBM, kBN / 2);
+  if (10 * few < 32 * (tiles > 300 ? tiles : 300) && few < 1 << 20)
+    return launch_gated_small(g, st);
   const int64_t tiles_m = (g.M + kBM - 1) / kBM + (g.mode == 0 ? 0 : g.n_groups);
   const int64_t total = tiles_m * ((g.N + kBN / 2 - 1) / (kBN / 2));
   const int64_t blocks = total < 65536 ? total : 65536;

@@ -1,0 +1,66 @@
+// Row groups of the grouped products (gfx950): which rows and which tile a
+// workgroup has, from device offsets.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ufp4 {
+
+__device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) {
+  return v < 0 ? 0 : (v > n ? n : v);
+}
+
+// The group and the tile in it of tile t, where group e has ceil(rows of e / bm)
+// * per_row tiles.  Offsets are clamped to [0, M], a decreasing pair is an empty
+// group.  Every wave finds it by itself: a lane sums a run of groups, a scan over
+// the lanes finds the run, and the run is walked.
+struct GroupTile {
+  int e;                                         // -1: past the last tile
+  int64_t row0, rows, local, tiles_m;
+};
+__device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_groups, int64_t M,
+                                                int bm, int64_t per_row, int64_t t) {
+  GroupTile g{0, 0, M, t, (M + bm - 1) / bm};
+  if (goff == nullptr) {
+    if (t >= g.tiles_m * per_row) g.e = -1;
+    return g;
+  }
+  const int lane = threadIdx.x & 63;
+  const int per = (n_groups + 63) / 64;
+  auto tiles_of = [&](int e) -> int64_t {
+    if (e >= n_groups) return 0;
+    const int64_t n = clamped(goff[e + 1], M) - clamped(goff[e], M);
+    return n > 0 ? (n + bm - 1) / bm : 0;
+  };
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i);
+  mine *= per_row;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t v = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += v;
+  }
+  const uint64_t over = __ballot(incl > t);
+  if (over == 0) {
+    g.e = -1;
+    return g;
+  }
+  const int src = __builtin_ctzll(over);
+  int64_t base = __shfl(incl - mine, src, 64);
+  for (int e = src * per;; ++e) {
+    const int64_t n = tiles_of(e);
+    if (t < base + n * per_row) {
+      g.e = e;
+      g.row0 = clamped(goff[e], M);
+      g.rows = clamped(goff[e + 1], M) - g.row0;
+      g.local = t - base;
+      g.tiles_m = n;
+      return g;
+    }
+    base += n * per_row;
+  }
+}
+
+}  // namespace ufp4

@@ -2,9 +2,12 @@
 //   p[m, n] = sa[m] sw[n] sum_k qa[m, k] qw[n, k] (+ bias[n]);  gated: act(p_gate) * p_up
 // on v_mfma_i32_*_i8, whose sums are exact: any order and split of K gives the
 // same bits.
+#include <atomic>
+
 #include "act_device.h"
 #include "block_device.h"
 #include "ffn_kernels.h"
+#include "group_device.h"
 
 namespace ufp4 {
 
@@ -12,83 +15,43 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kXcd = 8;
-constexpr int kStageK = 128;                     // bytes of K per LDS stage, one row's line
+constexpr int kStageK = 128;                     // bytes of K per LDS stage: a row's piece is a line
 
-__device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) {
-  return v < 0 ? 0 : (v > n ? n : v);
+// One value of the result from its exact sums: the same operations in every
+// kernel, so that which one runs shows in no bit.
+template <int ACT>
+__device__ __forceinline__ float finish(int gate, int up, float sa, float sg, float su, float bg,
+                                        float bu, bool bias) {
+  float v = (float)gate * sa * sg;
+  if (bias) v += bg;
+  if constexpr (ACT != UFP4_ACT_NONE) {
+    float u = (float)up * sa * su;
+    if (bias) u += bu;
+    v = u * act_value<ACT>(v);
+  }
+  return v;
 }
-
-// The group and the tile in it of tile t, where group e has ceil(rows of e / bm)
-// * per_row tiles.  Offsets are clamped to [0, M], a decreasing pair is an empty
-// group.  Every wave finds it by itself: a lane sums a run of groups, a scan over
-// the lanes finds the run, and the run is walked.
-struct GroupTile {
-  int e;                                         // -1: past the last tile
-  int64_t row0, rows, local, tiles_m;
-};
-__device__ __forceinline__ GroupTile group_tile(const Int8GemmArgs &a, int bm, int64_t per_row,
-                                                int64_t t) {
-  GroupTile g{0, 0, a.M, t, (a.M + bm - 1) / bm};
-  if (a.goff == nullptr) {
-    if (t >= g.tiles_m * per_row) g.e = -1;
-    return g;
-  }
-  const int lane = threadIdx.x & 63;
-  const int per = (a.n_groups + 63) / 64;
-  auto tiles_of = [&](int e) -> int64_t {
-    if (e >= a.n_groups) return 0;
-    const int64_t n = clamped(a.goff[e + 1], a.M) - clamped(a.goff[e], a.M);
-    return n > 0 ? (n + bm - 1) / bm : 0;
-  };
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i);
-  mine *= per_row;
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t v = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += v;
-  }
-  const uint64_t over = __ballot(incl > t);
-  if (over == 0) {
-    g.e = -1;
-    return g;
-  }
-  const int src = __builtin_ctzll(over);
-  int64_t base = __shfl(incl - mine, src, 64);
-  for (int e = src * per;; ++e) {
-    const int64_t n = tiles_of(e);
-    if (t < base + n * per_row) {
-      g.e = e;
-      g.row0 = clamped(a.goff[e], a.M);
-      g.rows = clamped(a.goff[e + 1], a.M) - g.row0;
-      g.local = t - base;
-      g.tiles_m = n;
-      return g;
-    }
-    base += n * per_row;
-  }
-}
-
 __device__ __forceinline__ void put(const Int8GemmArgs &a, int64_t row, int64_t col, float v) {
   if (a.out_bf16) static_cast<uint16_t *>(a.y)[row * a.ld_y + col] = to_bf16_bits(v);
   else static_cast<float *>(a.y)[row * a.ld_y + col] = v;
 }
-__device__ __forceinline__ float gated(int act, float gate, float up) {
-  return up * (act == UFP4_ACT_SILU ? act_value<UFP4_ACT_SILU>(gate)
-                                    : act_value<UFP4_ACT_GELU>(gate));
-}
 
 // ---------------------------------------------------------------------------
-// Few rows of x per group: w is read once, straight into the matrix
-// instruction's registers, by workgroups of 16 columns (gated: 16 of either
-// projection) whose four waves take every fourth 64 bytes of K; their sums meet
-// in LDS.  MT tiles of 16 rows of x at a time, in a loop over the group's rows.
+// Few rows of x per group: bound by reading w, which goes once, straight into
+// the matrix instruction's registers.  A workgroup has 16 columns (gated: of
+// either projection); its eight waves take every eighth line of 128 bytes of its
+// rows, and their sums meet in LDS.  MT tiles of 16 rows of x at a time, in a loop
+// over the group's rows.  The two loads of a line follow each other, and all
+// loads of a turn go before its products: 128 rows over 32 experts of 6144 to 2 x
+// 2048 columns take 131 us (805 MB, 6.1 TB/s), in the order of the products 155 us, with
+// streaming loads 150-200 us; one row to 2 x 8192 columns 7.6 us.
 // ---------------------------------------------------------------------------
-template <int MT, bool GATED>
-__global__ __launch_bounds__(256) void int8_rows_kernel(const Int8GemmArgs a) {
-  constexpr int P = GATED ? 2 : 1, WAVES = 4, U = 4;
-  __shared__ int s_acc[WAVES][P * MT][256];
+constexpr int kRowWaves = 8;
+template <int MT, int ACT>
+__global__ __launch_bounds__(64 * kRowWaves) void int8_rows_kernel(const Int8GemmArgs a) {
+  constexpr bool GATED = ACT != UFP4_ACT_NONE;
+  constexpr int P = GATED ? 2 : 1;
+  __shared__ int s_acc[kRowWaves][P * MT][256];
   const int64_t out_n = a.N / P;                  // output columns
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, chunk = (lane >> 4) * 16;
@@ -99,7 +62,7 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const Int8GemmArgs a) {
     rows = clamped(a.goff[e + 1], a.M) - row0;
   }
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t units = a.kpad / 64;
+  const int kpad = (int)a.kpad;
   const int8_t *pw[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -116,36 +79,26 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const Int8GemmArgs a) {
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[p][t] = i32x4(0);
-    int64_t k = wave;
-    for (; k + (U - 1) * WAVES < units; k += U * WAVES) {
-      i32x4 w[U][P], x[U][MT];
+    for (int k = wave * kStageK; k < kpad; k += kRowWaves * kStageK) {
+      i32x4 w[P][2], x[MT][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = (k + u * WAVES) * 64;
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int p = 0; p < P; ++p) w[u][p] = *reinterpret_cast<const i32x4 *>(pw[p] + at);
+        for (int u = 0; u < 2; ++u)
+          w[p][u] = *reinterpret_cast<const i32x4 *>(pw[p] + k + u * 64);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[u][t] = *reinterpret_cast<const i32x4 *>(pa[t] + at);
-      }
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < 2; ++u)
+          x[t][u] = *reinterpret_cast<const i32x4 *>(pa[t] + k + u * 64);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
           for (int t = 0; t < MT; ++t)
-            acc[p][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[u][t], w[u][p], acc[p][t], 0, 0, 0);
-    }
-    for (; k < units; k += WAVES) {
-      i32x4 w[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) w[p] = *reinterpret_cast<const i32x4 *>(pw[p] + k * 64);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const i32x4 x = *reinterpret_cast<const i32x4 *>(pa[t] + k * 64);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          acc[p][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, w[p], acc[p][t], 0, 0, 0);
-      }
+            acc[p][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[t][u], w[p][u], acc[p][t], 0, 0, 0);
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -155,73 +108,163 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const Int8GemmArgs a) {
         for (int r = 0; r < 4; ++r)
           s_acc[wave][p * MT + t][(4 * (lane >> 4) + r) * 16 + l16] = acc[p][t][r];
     __syncthreads();
-    const int64_t col = n0 + (threadIdx.x & 15);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int64_t m = m0 + 16 * t + (threadIdx.x >> 4);
+    for (int i = threadIdx.x; i < MT * 256; i += 64 * kRowWaves) {
+      const int tile = i >> 8, at = i & 255;
+      const int64_t m = m0 + 16 * tile + (at >> 4), col = n0 + (at & 15);
       if (m >= rows || col >= out_n) continue;
-      const float sa = a.sa[row0 + m];
-      float v[P];
+      int sum[2] = {0, 0};
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        int sum = 0;
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) sum += s_acc[w][p * MT + t][threadIdx.x];
-        const int64_t n = (int64_t)e * a.N + p * out_n + col;
-        v[p] = (float)sum * sa * a.sw[n];
-        if (a.bias != nullptr) v[p] += a.bias[n];
-      }
-      put(a, row0 + m, col, GATED ? gated(a.act, v[0], v[P - 1]) : v[0]);
+        for (int w = 0; w < kRowWaves; ++w) sum[p] += s_acc[w][p * MT + tile][at];
+      const int64_t n = (int64_t)e * a.N + col, up = GATED ? n + out_n : n;
+      const bool bias = a.bias != nullptr;
+      put(a, row0 + m, col,
+          finish<ACT>(sum[0], sum[1], a.sa[row0 + m], a.sw[n], a.sw[up], bias ? a.bias[n] : 0.0f,
+                      bias ? a.bias[up] : 0.0f, bias));
     }
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: BM x BN tiles of p, staged through LDS.
+// Many rows: BM x BN tiles of p (BM = 32 MT WM, BN = 64 WN), one per workgroup of
+// WM x WN waves, a wave owning 32 MT x 64 of it in 32x32 tiles; gated: its two
+// tiles of a row are the gate's and the up projection's of the same 32 columns.
+//
+// K goes through LDS in stages of 128 bytes per row, double-buffered, brought
+// there by buffer loads that write LDS directly (16 bytes a lane, no registers).
+// The loads of a stage are in flight while the one before is multiplied.  A
+// fragment is read from LDS one step of 32 bytes before its products, across the
+// stages too: the last step of a stage waits for the next stage's loads and the
+// other waves' reads, reads the next stage's first fragments, sends the loads of
+// the stage after it into the buffer that is now free, and only then issues its
+// own products.  Rows are 128 bytes, so a fragment's 32 rows fall on the same
+// banks: the 16-byte pieces of a row are kept in an order of its own (piece c at
+// place c ^ swizzle(row)), which the loads make by the address each lane asks for.
+//
+// w is the matrix instruction's first operand and x its second, so a lane ends
+// with four neighbouring columns of one row: the epilogue packs them, passes them
+// through LDS and writes 16 bytes a lane.  8192 x 2048 to 2 x 8192 columns, silu,
+// bf16: 273 us (2.01 POP/s), 235 without the epilogue; with the fragments read in
+// their own step 300-320 us, with stages of 64 bytes 290-297 us, with 128 x 128 tiles 298 us,
+// with 128 x 128 per wave (4 waves) 300-315 us.  A library product of the same
+// size takes 287 us with its int32 output.  What bounds it: reads of LDS (24 KB
+// per 8.4 MOP of a wave) and the products take about the same time, and under
+// them the clock falls to 1.9 GHz (zeros in place of the data: 225 us).
 // ---------------------------------------------------------------------------
-template <int WM, int WN, int MT, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(const Int8GemmArgs a,
-                                                                 int64_t tiles_n,
-                                                                 int64_t first) {
-  constexpr int NT = 2, THREADS = 64 * WM * WN;
-  constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
+__device__ __forceinline__ int swizzle(int row) {
+  return ((row >> 1) & 3) | ((((row >> 3) ^ (row >> 4)) & 1) << 2);
+}
+// Waits for all of this wave's loads into LDS, and for its LDS accesses.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Between the waves of a workgroup; memory accesses stay on their side.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// 16 bytes per lane from base + voffset + soffset to dst + 16 * lane.
+__device__ __forceinline__ void load_lds(const int8_t *base, int voffset, int soffset,
+                                         uint8_t *dst) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t *>(base), (short)0, 0x7FFFFFF0, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (__attribute__((address_space(3))) void *)dst, 16, voffset, soffset, 0, 0);
+}
+
+// The first n columns of a vector (none for n <= 0).
+template <typename T>
+__device__ __forceinline__ void store_cols(T *p, int n, u32x4 v) {
+  if (n > 0) store_vec(p, n, v);
+}
+
+constexpr int kBandRows = 8;       // tile rows that neighbouring workgroups share w's panels over
+template <int WM, int WN, int MT>
+struct TileShape {
+  static constexpr int kThreads = 64 * WM * WN, kBM = 32 * MT * WM, kBN = 64 * WN;
+  static constexpr int kStage = (kBM + kBN) * kStageK;
+  // two stages; the rows' scales; the columns' scales and biases
+  static constexpr size_t kLds = 2 * kStage + (kBM + 2 * kBN) * sizeof(float);
+};
+
+template <int WM, int WN, int MT, int ACT>
+__global__ __attribute__((amdgpu_flat_work_group_size(64 * WM * WN, 64 * WM * WN),
+                          amdgpu_waves_per_eu(2, 2))) void
+int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
+  using S = TileShape<WM, WN, MT>;
+  constexpr bool GATED = ACT != UFP4_ACT_NONE;
+  constexpr int NT = 2, WAVES = WM * WN, BM = S::kBM, BN = S::kBN;
   constexpr int OUT = GATED ? BN / 2 : BN;        // output columns of a tile
-  constexpr int AL = BM * kStageK / (16 * THREADS), BL = BN * kStageK / (16 * THREADS);
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int kStage = (BM + BN) * kStageK;
+  constexpr int AL = BM / (8 * WAVES), BL = BN / (8 * WAVES);   // loads per lane and stage
+  static_assert(AL * 8 * WAVES == BM && BL * 8 * WAVES == BN, "rows per load");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  float *s_sa = reinterpret_cast<float *>(lds + 2 * S::kStage);
+  float *s_sw = s_sa + BM, *s_bias = s_sw + BN;
   const int64_t out_n = a.N / (GATED ? 2 : 1);
 
-  // The workgroups of an XCD (every eighth) walk a contiguous range of tiles, so
-  // that a panel stays in one L2.
+  // The workgroups of an XCD (every eighth) walk a contiguous range of tiles, in
+  // bands of kBandRows tile rows, column by column: their panels meet in one L2.
   const unsigned per = gridDim.x / kXcd;          // the grid is a multiple of the XCDs
   const int64_t t = first + blockIdx.x % kXcd * per + blockIdx.x / kXcd;
-  const GroupTile g = group_tile(a, BM, tiles_n, t);
+  const GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, t);
   if (g.e < 0) return;
-  const int64_t tm = g.local / tiles_n, tn = g.local - tm * tiles_n;
+  const int64_t band = g.local / (kBandRows * tiles_n);
+  const int64_t in_band = g.local - band * kBandRows * tiles_n;
+  const int64_t deep = min((int64_t)kBandRows, g.tiles_m - band * kBandRows);
+  const int64_t tn = in_band / deep, tm = band * kBandRows + in_band - tn * deep;
   const int64_t row0 = g.row0 + tm * BM;
   const int rows = (int)min((int64_t)BM, g.rows - tm * BM);
   const int64_t col0 = tn * OUT;
   const int cols = (int)min((int64_t)OUT, out_n - col0);
+  const int64_t w_row = (int64_t)g.e * a.N + col0;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  const int8_t *pa[AL], *pb[BL];
+  const int l32 = lane & 31, half = lane >> 5;
+  const int kpad = (int)a.kpad;
+
+  // A load takes eight rows; rows past the tile's repeat its last one (their
+  // products are not stored).  Offsets stay below 256 rows of 2^17 bytes.
+  const int8_t *base_a = a.a + row0 * a.kpad, *base_w = a.w + w_row * a.kpad;
+  const int8_t *base_u = base_w + (GATED ? out_n * a.kpad : 0);
+  int va[AL], vw[BL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
-    const int item = i * THREADS + threadIdx.x;
-    const int r = item >> 3, c = (item & 7) ^ (r & 7);
-    pa[i] = a.a + (row0 + min(r, rows - 1)) * a.kpad + c * 16;
+    const int r = (i * WAVES + wave) * 8 + (lane >> 3);
+    va[i] = min(r, rows - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < BL; ++i) {
-    const int item = i * THREADS + threadIdx.x;
-    const int r = item >> 3, c = (item & 7) ^ (r & 7);
-    int64_t n;
-    if (GATED) n = (int64_t)((r >> 5) & 1) * out_n + col0 + min((r >> 6) * 32 + (r & 31), cols - 1);
-    else n = col0 + min(r, cols - 1);
-    pb[i] = a.w + ((int64_t)g.e * a.N + n) * a.kpad + c * 16;
+    const int r = (i * WAVES + wave) * 8 + (lane >> 3);
+    const int n = GATED ? (r >> 6) * 32 + (r & 31) : r;
+    vw[i] = min(n, cols - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
   }
+  auto issue = [&](int stage) __attribute__((always_inline)) {
+    uint8_t *st = lds + (stage & 1) * S::kStage + wave * 1024;
+    const int k0 = stage * kStageK;
+#pragma unroll
+    for (int i = 0; i < AL; ++i) load_lds(base_a, va[i], k0, st + i * WAVES * 1024);
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      // runs of 32 rows of either projection; a load's eight are of one
+      const bool up = GATED && (((i * WAVES + wave) >> 2) & 1) != 0;
+      load_lds(up ? base_u : base_w, vw[i], k0, st + BM * kStageK + i * WAVES * 1024);
+    }
+  };
+  const int stages = kpad / kStageK;
+  issue(0);
+  if (stages > 1) issue(1);
+  for (int r = threadIdx.x; r < BM; r += S::kThreads) s_sa[r] = a.sa[row0 + min(r, rows - 1)];
+  for (int r = threadIdx.x; r < BN; r += S::kThreads) {
+    const int n = min(GATED ? (r >> 6) * 32 + (r & 31) : r, cols - 1);
+    const int64_t at = w_row + n + (GATED && (r >> 5) & 1 ? out_n : 0);
+    s_sw[r] = a.sw[at];
+    s_bias[r] = a.bias != nullptr ? a.bias[at] : 0.0f;
+  }
+
   i32x16 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -229,119 +272,175 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(const Int8GemmA
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-  const int64_t stages = a.kpad / kStageK;
-  i32x4 ra[AL], rb[BL];
-  auto load = [&](int64_t s) {
+  constexpr int KK = kStageK / 32;
+  i32x4 fa[2][MT], fw[2][NT];
+  const uint8_t *pa = lds + (wm * MT * 32 + l32) * kStageK;
+  const uint8_t *pw = lds + (BM + wn * NT * 32 + l32) * kStageK;
+  const int sw32 = swizzle(l32);
+  auto read = [&](int into, int stage, int kk) __attribute__((always_inline)) {
+    const int at = (stage & 1) * S::kStage + ((2 * kk + half) ^ sw32) * 16;
 #pragma unroll
-    for (int i = 0; i < AL; ++i) ra[i] = *reinterpret_cast<const i32x4 *>(pa[i] + s * kStageK);
+    for (int i = 0; i < MT; ++i)
+      fa[into][i] = *reinterpret_cast<const i32x4 *>(pa + at + i * 32 * kStageK);
 #pragma unroll
-    for (int i = 0; i < BL; ++i) rb[i] = *reinterpret_cast<const i32x4 *>(pb[i] + s * kStageK);
+    for (int j = 0; j < NT; ++j)
+      fw[into][j] = *reinterpret_cast<const i32x4 *>(pw + at + j * 32 * kStageK);
   };
-  auto store = [&](uint8_t *st) {
+  wait_loads();
+  wait_lds();
+  meet();
+  read(0, 0, 0);
+  for (int s = 0; s < stages; ++s) {
 #pragma unroll
-    for (int i = 0; i < AL; ++i)
-      *reinterpret_cast<i32x4 *>(st + (i * THREADS + threadIdx.x) * 16) = ra[i];
-#pragma unroll
-    for (int i = 0; i < BL; ++i)
-      *reinterpret_cast<i32x4 *>(st + BM * kStageK + (i * THREADS + threadIdx.x) * 16) = rb[i];
-  };
-  const int l32 = lane & 31, half = lane >> 5;
-  load(0);
-  store(lds);
-  __syncthreads();
-  for (int64_t s = 0; s < stages; ++s) {
-    const uint8_t *st = lds + (s & 1) * kStage;
-    if (s + 1 < stages) load(s + 1);
-#pragma unroll
-    for (int kk = 0; kk < kStageK / 32; ++kk) {
-      const int slot = ((2 * kk + half) ^ (l32 & 7)) * 16;
-      i32x4 fa[MT], fb[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        fa[i] = *reinterpret_cast<const i32x4 *>(st + ((wm * MT + i) * 32 + l32) * kStageK + slot);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        fb[j] = *reinterpret_cast<const i32x4 *>(st + (BM + (wn * NT + j) * 32 + l32) * kStageK +
-                                                 slot);
+    for (int kk = 0; kk < KK; ++kk) {
+      if (kk + 1 < KK) {
+        read((kk + 1) & 1, s, kk + 1);
+      } else if (s + 1 < stages) {
+        wait_loads();                             // of stage s + 1
+        wait_lds();                               // this wave's last fragments of stage s
+        meet();
+        read((kk + 1) & 1, s + 1, 0);
+        if (s + 2 < stages) issue(s + 2);
+      }
+      // the reads and loads above go out before the products below
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][j], fa[kk & 1][i], acc[i][j],
+                                                            0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (s + 1 < stages) store(lds + ((s + 1) & 1) * kStage);
-    __syncthreads();
   }
+  wait_lds();
+  meet();                                         // the stages' LDS is free
+
+  // Epilogue, 32 rows of the wave at a time through its own piece of LDS: a lane
+  // has columns 8 q + 4 half + 0..3 of row l32.
+  constexpr int W = GATED ? 32 : 64;              // output columns of the wave
+  constexpr int kLine = W * 4 + 16;               // bytes; 16 more to spread the banks
+  static_assert(WAVES * 32 * kLine <= 2 * S::kStage, "epilogue LDS");
+  uint8_t *line = lds + wave * 32 * kLine;
+  const int out_bytes = a.out_bf16 ? 2 : 4;
+  const int wcol = wn * W, left = cols - wcol;    // columns of the wave that exist
 #pragma unroll
-  for (int j = 0; j < (GATED ? 1 : NT); ++j) {
-    const int col = GATED ? wn * 32 + l32 : (wn * NT + j) * 32 + l32;
-    if (col >= cols) continue;
-    const int64_t n = (int64_t)g.e * a.N + col0 + col;
-    const float sw = a.sw[n], su = GATED ? a.sw[n + out_n] : 0.0f;
-    const float bw = a.bias ? a.bias[n] : 0.0f, bu = GATED && a.bias ? a.bias[n + out_n] : 0.0f;
+  for (int i = 0; i < MT; ++i) {
+    const int m0 = (wm * MT + i) * 32;
+    const float sa = s_sa[m0 + l32];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < W / 32; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int m = (wm * MT + i) * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
-        if (m >= rows) continue;
-        const float sa = a.sa[row0 + m];
-        float v = (float)acc[i][j][r] * sa * sw;
-        if (a.bias) v += bw;
-        if (GATED) {
-          float u = (float)acc[i][1][r] * sa * su;
-          if (a.bias) u += bu;
-          v = gated(a.act, v, u);
+      for (int q = 0; q < 4; ++q) {
+        const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half;
+        float v[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int n = n0 + z, r = q * 4 + z;
+          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, s_sw[n], GATED ? s_sw[n + 32] : 0.0f,
+                             s_bias[n], GATED ? s_bias[n + 32] : 0.0f, a.bias != nullptr);
         }
-        put(a, row0 + m, col0 + col, v);
+        uint8_t *p = line + l32 * kLine + (j * 32 + 8 * q + 4 * half) * out_bytes;
+        if (a.out_bf16) {
+          uint2 w;
+          w.x = (uint32_t)to_bf16_bits(v[0]) | (uint32_t)to_bf16_bits(v[1]) << 16;
+          w.y = (uint32_t)to_bf16_bits(v[2]) | (uint32_t)to_bf16_bits(v[3]) << 16;
+          *reinterpret_cast<uint2 *>(p) = w;
+        } else {
+          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        }
       }
+    wait_lds();                                   // the wave's own lines; its lanes run together
+    const int pieces = W * out_bytes / 16;        // 16-byte pieces of a row: 4, 8 or 16
+    for (int x = lane; x < 32 * pieces; x += 64) {
+      const int r = x / pieces, c = x % pieces, m = m0 + r;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(line + r * kLine + c * 16);
+      if (m >= rows) continue;
+      if (a.out_bf16)
+        store_cols(static_cast<uint16_t *>(a.y) + (row0 + m) * a.ld_y + col0 + wcol + c * 8,
+                   left - c * 8, v);
+      else
+        store_cols(static_cast<float *>(a.y) + (row0 + m) * a.ld_y + col0 + wcol + c * 4,
+                   left - c * 4, v);
+    }
+    wait_lds();
   }
 }
 
 // ---------------------------------------------------------------------------
-template <int MT, bool GATED>
+template <int MT, int ACT>
 static hipError_t launch_rows(const Int8GemmArgs &a, hipStream_t st) {
-  const int64_t out_n = a.N / (GATED ? 2 : 1);
-  hipLaunchKernelGGL((int8_rows_kernel<MT, GATED>),
-                     dim3((unsigned)((out_n + 15) / 16), (unsigned)a.n_groups), dim3(256), 0, st, a);
+  const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
+  hipLaunchKernelGGL((int8_rows_kernel<MT, ACT>),
+                     dim3((unsigned)((out_n + 15) / 16), (unsigned)a.n_groups),
+                     dim3(64 * kRowWaves), 0, st, a);
   return hipGetLastError();
 }
 
-template <int WM, int WN, int MT, bool GATED>
+// The dynamic-LDS limit is a per-device function attribute: set once on each
+// device the kernel runs on (a bit per device id; concurrent first calls at worst
+// both set it, which is harmless).
+template <int WM, int WN, int MT, int ACT>
+static hipError_t allow_lds(const void *kernel, size_t bytes) {
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (bit != 0 && (configured.load(std::memory_order_acquire) & bit) != 0) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) configured.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <int WM, int WN, int MT, int ACT>
 static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
-  constexpr int BM = 32 * MT * WM, BN = 64 * WN;
-  constexpr size_t kLds = 2 * (BM + BN) * kStageK;
-  const int64_t out_n = a.N / (GATED ? 2 : 1);
-  const int64_t tiles_n = (out_n + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
-  const int64_t tiles_m = (a.M + BM - 1) / BM + (a.goff ? a.n_groups : 0);
+  using S = TileShape<WM, WN, MT>;
+  const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
+  const int64_t out = ACT != UFP4_ACT_NONE ? S::kBN / 2 : S::kBN;
+  const int64_t tiles_n = (out_n + out - 1) / out;
+  const int64_t tiles_m = (a.M + S::kBM - 1) / S::kBM + (a.goff ? a.n_groups : 0);
   const int64_t total = (tiles_m * tiles_n + kXcd - 1) / kXcd * kXcd;
   constexpr int64_t kMost = 1 << 22;              // tiles of a launch: below 2^32 threads
-  auto *kernel = int8_tile_kernel<WM, WN, MT, GATED>;
-  const hipError_t e = hipFuncSetAttribute((const void *)kernel,
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  auto *kernel = int8_tile_kernel<WM, WN, MT, ACT>;
+  hipError_t e = allow_lds<WM, WN, MT, ACT>((const void *)kernel, S::kLds);
   if (e != hipSuccess) return e;
   for (int64_t first = 0; first < total; first += kMost) {
     const unsigned n = (unsigned)(total - first < kMost ? total - first : kMost);
-    hipLaunchKernelGGL(kernel, dim3(n), dim3(64 * WM * WN), kLds, st, a, tiles_n, first);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(kernel, dim3(n), dim3(S::kThreads), S::kLds, st, a, tiles_n, first);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <bool GATED>
+template <int ACT>
 static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t rows = (a.M + a.n_groups - 1) / a.n_groups;
-  if (rows <= 16) return launch_rows<1, GATED>(a, st);
-  if (rows <= 64) return launch_rows<4, GATED>(a, st);
+  const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
+  const int64_t groups16 = (out_n + 15) / 16 * a.n_groups;      // workgroups of the rows kernel
+  // Up to 16 rows the rows kernel reads w at the memory's rate.  With more rows it
+  // reads them in every workgroup, which pays while there are few (17 rows, 8192
+  // to 2048 columns: 10 us, 64-row tiles 41; 64 rows, 2048 to 4096 columns: 7 and 12 us;
+  // 48 rows, 2048 to 2 x 8192: 14.4 and 14.4 us; 1000 rows over 32 experts, 2048 to 2 x 2048
+  // columns: 89 and 70 us).
+  if (rows <= 16) return launch_rows<1, ACT>(a, st);
+  if (rows <= 32 && groups16 <= 1024) return launch_rows<2, ACT>(a, st);
+  if (rows <= 64 && groups16 <= 512) return launch_rows<4, ACT>(a, st);
+  // The largest tiles that fill the GPU: 4000 x 4096 x 4096: 71 us, with 128-row
+  // tiles 86, with 64-row ones 110; 2000 x 4096 x 4096: 61, 46 and 57 us; 1000 x 4096
+  // x 4096: 58, 33 and 31 us; 500 x 2048 x 2048: 32, 18 and 13 us.
   const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= 256) return launch_tiles<2, 4, 4, GATED>(a, st);
-  return launch_tiles<2, 2, 2, GATED>(a, st);
+  if (big >= 256) return launch_tiles<2, 4, 4, ACT>(a, st);
+  const int64_t middle = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (middle >= 512) return launch_tiles<2, 2, 2, ACT>(a, st);
+  return launch_tiles<2, 2, 1, ACT>(a, st);
 }
 
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
-  return a.act == UFP4_ACT_NONE ? int8_gemm<false>(a, st) : int8_gemm<true>(a, st);
+  if (a.act == UFP4_ACT_NONE) return int8_gemm<UFP4_ACT_NONE>(a, st);
+  return a.act == UFP4_ACT_SILU ? int8_gemm<UFP4_ACT_SILU>(a, st) : int8_gemm<UFP4_ACT_GELU>(a, st);
 }
 
 }  // namespace ufp4

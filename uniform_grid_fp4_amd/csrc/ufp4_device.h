@@ -126,6 +126,21 @@ __device__ __forceinline__ uint32_t e2m1_sr(float m, uint32_t u) {
 }
 
 // ---------------------------------------------------------------------------
+// 8 nibbles -> 8 FP8 E4M3 bytes.  Output byte order [n0 n2 n4 n6 | n1 n3 n5
+// n7]; A and B use the same order, so products still pair up.
+template <int GRID>
+__device__ __forceinline__ uint2 nib8_to_fp8(uint32_t w) {
+  constexpr uint32_t lut_lo = 0x44403800u;  // 0, 1, 2, 3
+  constexpr uint32_t lut_hi = (GRID == kGridUniform) ? 0x4E4C4A48u   // 4, 5, 6, 7
+                                                     : 0x54504C48u;  // 4, 6, 8, 12
+  const uint32_t me = w & 0x07070707u;
+  const uint32_t mo = (w >> 4) & 0x07070707u;
+  const uint32_t fe = __builtin_amdgcn_perm(lut_hi, lut_lo, me) | ((w << 4) & 0x80808080u);
+  const uint32_t fo = __builtin_amdgcn_perm(lut_hi, lut_lo, mo) | (w & 0x80808080u);
+  return make_uint2(fe, fo);
+}
+
+// ---------------------------------------------------------------------------
 // Packing eight results into one word of nibbles (element 2i in the low
 // nibble of byte i), SWAR style.
 // ---------------------------------------------------------------------------

@@ -114,6 +114,8 @@ struct GemmArgs {
 hipError_t launch_gemm(const GemmArgs &g, hipStream_t st);
 constexpr int64_t kGatedMaxK = 65536;
 hipError_t launch_gated_gemm(const GemmArgs &g, hipStream_t st);
+// The same for few output tiles.
+hipError_t launch_gated_small(const GemmArgs &g, hipStream_t st);
 
 // Split-K of a dense GEMM whose output tiles do not fill the GPU: partial
 // outputs of the K splits in the FP32 workspace ws [n_split, M, N], then a
