@@ -110,7 +110,9 @@ def check_backward(dy, r, w, b, dh, eps=EPS):
 SHAPES = [(1, 1), (1, 2048), (3, 7), (2, 8), (5, 63), (4, 64), (3, 65), (7, 511), (2, 1024),
           (33, 1411), (3, 2049), (2, 4104), (2, 6144), (3, 8192), (2, 12289), (2, 16384),
           (1, 40000), (300, 96), (600, 5000), (530, 9000), (3, 11000), (700, 15),
-          (1500, 121), (600, 2047), (520, 6143), (600, 1073), (40, 1536)]
+          (1500, 121), (600, 2047), (520, 6143), (600, 1073), (40, 1536), (1500, 2000),
+          (1300, 1601), (600, 8000), (300, 15001), (270, 16000), (2300, 1300), (4500, 512),
+          (20000, 100)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)

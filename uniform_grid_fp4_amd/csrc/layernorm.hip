@@ -20,9 +20,39 @@ __device__ __forceinline__ bool counts(int c0, int cols, int j) {
   return c0 < cols && !elsewhere<TAIL, V>(c0, cols, j);
 }
 
+// Two sums over the TPR threads that hold a row, through one exchange; s is of
+// another turn than the last exchange's.
+template <int TPR>
+__device__ __forceinline__ void span_sums(float &a, float &b, float (*s)[16]) {
+  if constexpr (TPR == 16) {
+    a = row_sum(a);
+    b = row_sum(b);
+  } else {
+    a = lanes_sum(a);
+    b = lanes_sum(b);
+    if constexpr (TPR > 64) {
+      constexpr int WAVES = TPR / 64;
+      if ((threadIdx.x & 63) == 0) {
+        s[0][threadIdx.x % TPR >> 6] = a;
+        s[1][threadIdx.x % TPR >> 6] = b;
+      }
+      __syncthreads();
+      a = s[0][0];
+      b = s[1][0];
+#pragma unroll
+      for (int i = 1; i < WAVES; ++i) {
+        a += s[0][i];
+        b += s[1][i];
+      }
+    }
+  }
+}
+
 // A row per TPR threads at a time, as NV vectors each.  Two sums per row go
 // through LDS words of their own: between two uses of either lies the other's
-// barrier.
+// barrier.  8192 x 2048 bf16 with residual 24 us (134 MB, 5.6 TB/s, partly from the
+// 256 MB cache), 16384 x 6144 139 us (805 MB, 5.8 TB/s), 4096 x 8192 FP32 100 us (537
+// MB, 5.4 TB/s), one row 3.2 us: bound by memory.
 template <typename T, typename W, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(group_size(TPR)) void layernorm_kernel(const LayerNormArgs a) {
   constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, STEP = TPR * V;
@@ -159,14 +189,22 @@ __global__ __launch_bounds__(256) void layernorm_row_kernel(const LayerNormArgs 
   }
 }
 
+// Threads of a workgroup of the backward pass: it holds 512 / TPR rows at once,
+// whose sums of dw and db it joins, so that fewer partial rows are written.
+constexpr int bwd_threads(int tpr) { return tpr < 512 ? 512 : tpr; }
+
 // Backward with rows held in registers: dx, and the workgroup's share of dw and
 // db, which stay in registers over all its rows (in the order of the rows) and
 // go to partial[workgroup][0 and 1][cols] at the end, the rows of a workgroup
-// that holds several added in their order.
+// that holds several added in their order.  8192 x 2048 bf16 29 us and 4 us for the
+// second half of dw and db (134 MB and 17 MB of partial sums; with one row of 256
+// threads per workgroup 33 and 4); 16384 x 6144 156 us together (805 MB, 5.2 TB/s).
+// Loading the next row ahead cost registers and gained nothing.
 template <typename T, typename W, int TPR, int NV, bool TAIL>
-__global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const LayerNormBwdArgs a) {
-  constexpr int V = Elem<T>::V, ROWS = group_size(TPR) / TPR, STEP = TPR * V;
-  __shared__ float s_g[16], s_gx[16];
+__global__ __launch_bounds__(bwd_threads(TPR)) void layernorm_bwd_kernel(const LayerNormBwdArgs a) {
+  constexpr int THREADS = bwd_threads(TPR);
+  constexpr int V = Elem<T>::V, ROWS = THREADS / TPR, STEP = TPR * V;
+  __shared__ float s_sums[2][ROWS][2][16];
   const int cols = (int)a.cols;
   const int first = (threadIdx.x % TPR) * V;
   WeightVec<T, W, TAIL> w[NV];
@@ -181,7 +219,15 @@ __global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const La
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   const T *dy = static_cast<const T *>(a.dy), *h = static_cast<const T *>(a.h);
   const T *dh = static_cast<const T *>(a.dh);
-  for (; row < a.rows; row += step) {
+  // 16 lanes or a wave leave the loop on their own.  The rows of a workgroup with
+  // barriers leave it together: one past the end repeats the last one and counts
+  // nowhere.
+  constexpr bool TOGETHER = TPR > 64 && ROWS > 1;
+  for (int turn = 0; TOGETHER ? row - threadIdx.x / TPR < a.rows : row < a.rows;
+       row += step, turn ^= 1) {
+    const int64_t mine = row;
+    const bool live = !TOGETHER || row < a.rows;
+    if (TOGETHER && !live) row = a.rows - 1;
     RowVecs<NV, T, TAIL> vd, vy, vh;
     vy.load(dy + row * a.ld_dy, first, STEP, cols);
     vh.load(h + row * a.ld_h, first, STEP, cols);
@@ -198,7 +244,7 @@ __global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const La
       for (int j = 0; j < V; ++j) {
         // what is not of the row, or another lane's, counts nowhere
         f[j] = (f[j] - mean) * rstd;
-        if (!counts<TAIL, V>(first + i * STEP, cols, j)) g[j] = f[j] = 0.0f;
+        if (!live || !counts<TAIL, V>(first + i * STEP, cols, j)) g[j] = f[j] = 0.0f;
         acc[i][j] = __builtin_fmaf(g[j], f[j], acc[i][j]);
         acb[i][j] += g[j];
         g[j] *= wf[j];
@@ -212,8 +258,8 @@ __global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const La
 #pragma unroll
       for (int i = 0; i < NV; ++i) asm volatile("" ::"v"(vd.v[i]));
     }
-    const float mg = span_sum<TPR>(sg, s_g) / (float)cols;
-    const float mgx = span_sum<TPR>(sgx, s_gx) / (float)cols;
+    span_sums<TPR>(sg, sgx, s_sums[turn][threadIdx.x / TPR]);
+    const float mg = sg / (float)cols, mgx = sgx / (float)cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[V], g[V], wf[V];
@@ -229,9 +275,11 @@ __global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const La
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] += g[j];
       }
-      row_store<T, TAIL>(static_cast<T *>(a.dx) + row * a.cols, first + i * STEP, cols,
-                         Elem<T>::pack(f), a.stream);
+      if (live)
+        row_store<T, TAIL>(static_cast<T *>(a.dx) + row * a.cols, first + i * STEP, cols,
+                           Elem<T>::pack(f), a.stream);
     }
+    if (TOGETHER) row = mine;
   }
   float *partial = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
   if (ROWS == 1) {
@@ -263,7 +311,7 @@ __global__ __launch_bounds__(group_size(TPR)) void layernorm_bwd_kernel(const La
               which ? acb[i][j] : acc[i][j];
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < STEP && i * STEP + c < cols; c += 256) {
+      for (int c = threadIdx.x; c < STEP && i * STEP + c < cols; c += THREADS) {
         float t = s_acc[0][c];
 #pragma unroll
         for (int r = 1; r < ROWS; ++r) t += s_acc[r][c];
@@ -363,16 +411,25 @@ __global__ __launch_bounds__(1024) void layernorm_dw_final_kernel(const LayerNor
     static_cast<W *>(blockIdx.y ? a.db : a.dw)[c] = Elem<W>::put(s_sum[0][col]);
 }
 
-// The backward pass keeps the sums of dw and db next to three rows: beyond 128
-// vectors a workgroup holds a row (a wave would with three per lane, and spill).
+// The backward pass keeps the sums of dw and db next to three rows: with four
+// vectors per lane of a wave it would spill, so 193 to 256 vectors take 256 threads
+// with one each.  With fewer, too many of them would idle (30000 x 1280 bf16: 71 us,
+// a wave per row 63).  In the same way twice the threads take two vectors each where
+// half would take four.
 static RowShape bwd_shape(int64_t cols, int v) {
   const int64_t n = (cols + v - 1) / v;
-  return n > 128 && n <= 256 ? RowShape{256, 1} : row_shape(cols, v);
+  const RowShape s = row_shape(cols, v);
+  if (s.nv != 4) return s;
+  return n <= 256 ? RowShape{256, 1} : RowShape{s.tpr * 2, 2};
 }
-// Workgroups of the backward pass, each of which writes its partial sums.
-constexpr int kLayerNormBwdGrid = 512;
+// Workgroups of the backward pass, each of which writes its partial sums: two per
+// CU where a thread holds one vector and two fit (8192 x 2048 bf16: 33 us, one per
+// CU 38; 60000 x 256: 33 and 41), else one (30000 x 1280: 68 and 63 us, 2000 x 12000: 86
+// and 65; 16384 x 6144: 168 and 156).
+static int bwd_grid(RowShape s) { return s.nv == 1 ? 512 : 256; }
 
-#define UFP4_BWD_SHAPES(F) F(16, 1) F(64, 1) F(64, 2) F(256, 1) UFP4_LONG_SHAPES(F)
+#define UFP4_BWD_SHAPES(F)                                                                   \
+  F(16, 1) F(64, 1) F(64, 2) F(64, 3) F(256, 1) F(256, 2) F(256, 3) F(512, 2) F(512, 3) F(1024, 2)
 
 template <typename T, typename W, bool TAIL>
 static hipError_t fwd_rows(const LayerNormArgs &a, RowShape s, hipStream_t st) {
@@ -412,8 +469,9 @@ hipError_t launch_layernorm(const LayerNormArgs &a, hipStream_t st) {
 // not known to the caller, so this is the larger of the two types' needs.
 static int bwd_slices(int64_t rows, int64_t cols, int v) {
   const RowShape s = bwd_shape(cols, v);
-  int64_t n = s.tpr != 0 ? row_groups(rows, s.tpr) : (rows + 63) / 64;
-  const int64_t most = s.tpr != 0 ? kLayerNormBwdGrid : 256;
+  const int per = s.tpr != 0 ? bwd_threads(s.tpr) / s.tpr : 64;
+  int64_t n = (rows + per - 1) / per;
+  const int64_t most = s.tpr != 0 ? bwd_grid(s) : 256;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
@@ -427,7 +485,7 @@ static hipError_t bwd_rows(const LayerNormBwdArgs &a, RowShape s, int slices, hi
 #define UFP4_NORM(TPR, NV)                                                                   \
   if (s.tpr == TPR && s.nv == NV) {                                                          \
     hipLaunchKernelGGL((layernorm_bwd_kernel<T, W, TPR, NV, TAIL>), dim3(slices),            \
-                       dim3(group_size(TPR)), 0, st, a);                                     \
+                       dim3(bwd_threads(TPR)), 0, st, a);                                    \
     return hipGetLastError();                                                                \
   }
   UFP4_BWD_SHAPES(UFP4_NORM)
