@@ -148,16 +148,25 @@ class MoEOut(NamedTuple):
 
 class UFP4MoEBlock(torch.nn.Module):
     """A pre-norm MoE block: RMS norm of x + residual, router, dispatch, two
-    `UFP4ExpertLinear` layers with a SiLU between them, combine.  x and residual
-    are bf16 [..., hidden]; `valid` (bool, one per token) leaves padding tokens
-    out.  The next block's norm adds y to the returned residual."""
+    `UFP4ExpertLinear` layers with a SiLU between them, combine.  `gated` ("silu" or
+    "gelu") makes the first a `UFP4GatedExpertLinear`, whose kernel applies that
+    activation to its gate.  x and residual are bf16 [..., hidden]; `valid` (bool,
+    one per token) leaves padding tokens out.  The next block's norm adds y to the
+    returned residual."""
 
     def __init__(self, hidden: int, ffn: int, n_experts: int, k: int, seed: int = 0, device=None,
-                 grid: int = U.GRID_UNIFORM):
+                 grid: int = U.GRID_UNIFORM, gated: Optional[str] = None):
         super().__init__()
         self.norm = RMSNorm(hidden, device=device)
         self.router = MoERouter(hidden, n_experts, k, device=device)
-        self.up = UFP4ExpertLinear(n_experts, hidden, ffn, seed=seed, grid=grid, device=device)
+        self.gated = gated is not None
+        if self.gated:
+            from .feedforward import UFP4GatedExpertLinear   # which imports this module
+            self.up = UFP4GatedExpertLinear(n_experts, hidden, ffn, act=gated, seed=seed,
+                                            grid=grid, device=device)
+        else:
+            self.up = UFP4ExpertLinear(n_experts, hidden, ffn, seed=seed, grid=grid,
+                                       device=device)
         self.down = UFP4ExpertLinear(n_experts, ffn, hidden, seed=seed + 1, grid=grid,
                                      device=device)
 
@@ -169,7 +178,8 @@ class UFP4MoEBlock(torch.nn.Module):
             y, h = self.norm(x, residual)
         r = self.router(y, None if valid is None else valid.reshape(-1))
         xs = dispatch(y, r.slots)
-        ys = self.down(torch.nn.functional.silu(self.up(xs, r.offsets)), r.offsets)
+        up = self.up(xs, r.offsets)
+        ys = self.down(up if self.gated else torch.nn.functional.silu(up), r.offsets)
         out = combine(ys, r.slots, r.gates)
         return MoEOut(out.reshape(x.shape), h, r.losses, r.counts)
 
