@@ -143,14 +143,16 @@ typedef struct {
  * n_groups; results are the same bit for bit.
  * ufp4_int8_linear: the same with a = ufp4_int8_quantize(x), x [M, k] of type
  * dtype; workspace: device, 16-byte aligned, at least
- * ufp4_int8_linear_workspace_size(M, k) bytes, overwritten.
+ * ufp4_int8_linear_workspace_size(M, k, grouped) bytes, overwritten, grouped 0
+ * where d_group_offsets is NULL (0 bytes for a few rows, which every workgroup
+ * quantizes itself: then it may be NULL).  y may not be x.
  * Returns OK, INVALID_ARG, SHAPE (k of a and w differ, rows not a multiple of
  * the groups, n_groups outside 1..1024), UNSUPPORTED (k beyond 131071: a sum
  * could pass 31 bits), HIP. */
 ufp4_status ufp4_int8_gemm(const ufp4_int8_rows *a, const ufp4_int8_rows *w, const float *bias,
                            int32_t act, int32_t n_groups, const int64_t *d_group_offsets,
                            int32_t out_dtype, void *y, int64_t ld_y, hipStream_t stream);
-size_t ufp4_int8_linear_workspace_size(int64_t rows, int64_t cols);
+size_t ufp4_int8_linear_workspace_size(int64_t rows, int64_t cols, int32_t grouped);
 ufp4_status ufp4_int8_linear(const void *x, int64_t ld_x, int32_t dtype, int64_t rows,
                              int64_t cols, const ufp4_int8_rows *w, const float *bias, int32_t act,
                              int32_t n_groups, const int64_t *d_group_offsets, int32_t out_dtype,

@@ -201,9 +201,11 @@ def test_int8_left_operand_and_workspace():
     assert L.ufp4_int8_gemm(None, *tail, None) == -1
     good = rows(rows=8)
     assert L.ufp4_int8_gemm(ctypes.addressof(good), None, *tail[1:], None) == -1
-    need = F.ufp4_int8_linear_workspace_size(8, 64)
-    assert need >= 8 * 128 + 8 * 4 and F.ufp4_int8_linear_workspace_size(-1, 64) == 0
-    lin = lambda x, ld, ws, n: L.ufp4_int8_linear(x, ld, BF16, 8, 64, *tail, ws, n, None)
+    need = F.ufp4_int8_linear_workspace_size(80, 64)
+    assert need >= 80 * 128 + 80 * 4 and F.ufp4_int8_linear_workspace_size(-1, 64) == 0
+    assert F.ufp4_int8_linear_workspace_size(8, 64) == 0
+    assert F.ufp4_int8_linear_workspace_size(8, 64, grouped=True) >= 8 * 128 + 8 * 4
+    lin = lambda x, ld, ws, n: L.ufp4_int8_linear(x, ld, BF16, 80, 64, *tail, ws, n, None)
     assert lin(A, 64, A, need - 1) == -1 and lin(A, 64, None, need) == -1
     assert lin(A, 64, A + 8, need) == -1 and lin(None, 64, A, need) == -1
     assert lin(A + 1, 64, A, need) == -1 and lin(A, 63, A, need) == -2
@@ -237,7 +239,7 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 
 
 def test_the_tensors_device_is_current(monkeypatch):
-    """As of the block operators: every call of a stream goes through block._call."""
+    """As of the block operators."""
     at, seen = [0], []
 
     @contextlib.contextmanager
@@ -251,7 +253,7 @@ def test_the_tensors_device_is_current(monkeypatch):
     monkeypatch.setattr(B, "_current_device", lambda: at[0])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(B, "_raw_stream", lambda index: ("stream of", index))
-    monkeypatch.setattr(B, "lib", lambda: types.SimpleNamespace(
+    monkeypatch.setattr(F, "lib", lambda: types.SimpleNamespace(
         some_call=lambda *a: seen.append((at[0], a)) or 0))
     F._call("some_call", torch.device("cuda", 2), 7)
     assert seen == [(2, (7, ("stream of", 2)))] and at == [0]

@@ -234,8 +234,34 @@ def test_linear_is_quantize_then_product(m, dtype):
         assert torch.equal(y, want)
         flat = torch.full((m, 150), float("nan"), dtype=dtype, device=DEV)
         flat[:, 3:133].copy_(x)
-        ws = torch.empty(F.ufp4_int8_linear_workspace_size(m, 130), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(F.ufp4_int8_linear_workspace_size(m, 130, True), dtype=torch.uint8, device=DEV)
         assert torch.equal(F.ufp4_int8_linear(flat[:, 3:133], w, workspace=ws, **kw), y)
+
+
+@pytest.mark.parametrize("m,k", [(1, 1), (1, 7), (1, 130), (1, 2048), (1, 32768), (1, 32641),
+                                 (2, 5000), (3, 10000), (4, 8192), (5, 100), (7, 4000), (8, 4096),
+                                 (9, 3500), (15, 2000), (16, 2048), (16, 130), (16, 3)])
+@pytest.mark.parametrize("dtype", BOTH)
+def test_few_rows_quantized_by_the_product(m, k, dtype):
+    """Bit for bit what the two calls give, at the rows' ends, zero rows and rows
+    that are not finite among them."""
+    assert F.ufp4_int8_linear_workspace_size(m, k) == 0
+    x, w = normal(m, k, dtype), F.ufp4_int8_quantize(normal(38, k, seed=2, std=0.05))
+    bias = normal(1, 38, seed=3)[0].contiguous()
+    for i in range(3):
+        for kw in (dict(), dict(bias=bias), dict(act=F.ACT_SILU), dict(act=F.ACT_GELU, bias=bias)):
+            want = F.ufp4_int8_gemm(F.ufp4_int8_quantize(x), w, out_dtype=dtype, **kw)
+            y = F.ufp4_int8_linear(x, w, **kw)
+            assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0)), (i, kw)
+        x = x.clone()
+        if i == 0:
+            x[m // 2] = 0
+        else:
+            x[m - 1, k - 1] = float("nan")
+    flat = torch.full((m, k + 5), float("nan"), dtype=dtype, device=DEV)
+    x = normal(m, k, dtype)
+    flat[:, 3:3 + k].copy_(x)
+    assert torch.equal(F.ufp4_int8_linear(flat[:, 3:3 + k], w), F.ufp4_int8_linear(x, w))
 
 
 def test_output_rows_of_any_stride():
@@ -282,4 +308,4 @@ def test_no_rows_and_refusals():
     with pytest.raises(UFP4Error):
         F.ufp4_int8_gemm(a, w, act=7)
     with pytest.raises(UFP4Error):
-        F.ufp4_int8_linear(x, w, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+        F.ufp4_int8_linear(normal(40, 64), w, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))

@@ -252,8 +252,8 @@ ufp4_status ufp4_int8_gemm(const ufp4_int8_rows *a, const ufp4_int8_rows *w, con
 }
 
 // The codes, then the scales.
-size_t ufp4_int8_linear_workspace_size(int64_t rows, int64_t cols) {
-  if (bad_shape(rows, cols)) return 0;
+size_t ufp4_int8_linear_workspace_size(int64_t rows, int64_t cols, int32_t grouped) {
+  if (bad_shape(rows, cols) || (grouped == 0 && int8_fuses(rows, int8_kpad(cols)))) return 0;
   return (size_t)rows * ((size_t)int8_kpad(cols) + sizeof(float));
 }
 
@@ -268,16 +268,18 @@ ufp4_status ufp4_int8_linear(const void *x, int64_t ld_x, int32_t dtype, int64_t
   s = int8_product(rows, cols, w, bias, act, n_groups, d_group_offsets, out_dtype, y, ld_y, g);
   if (s != UFP4_OK) return s;
   if (rows == 0) return UFP4_OK;
-  if (!good(workspace, 16) || workspace_bytes < ufp4_int8_linear_workspace_size(rows, cols))
-    return UFP4_ERR_INVALID_ARG;
-  int8_t *q = static_cast<int8_t *>(workspace);
-  float *scale = reinterpret_cast<float *>(q + rows * g.kpad);
-  const hipError_t e =
-      launch_int8_quantize(quantize_args(x, ld_x, dtype, rows, cols, q, scale), stream);
-  if (e != hipSuccess) return of(e);
+  const size_t need =
+      ufp4_int8_linear_workspace_size(rows, cols, d_group_offsets != nullptr ? 1 : 0);
+  int8_t *q = nullptr;
+  float *scale = nullptr;
+  if (need > 0) {
+    if (!good(workspace, 16) || workspace_bytes < need) return UFP4_ERR_INVALID_ARG;
+    q = static_cast<int8_t *>(workspace);
+    scale = reinterpret_cast<float *>(q + rows * g.kpad);
+  }
   g.a = q;
   g.sa = scale;
-  return of(launch_int8_gemm(g, stream));
+  return of(launch_int8_linear(g, quantize_args(x, ld_x, dtype, rows, cols, q, scale), stream));
 }
 
 }  // extern "C"

@@ -95,6 +95,15 @@ struct Int8GemmArgs {
   int64_t ld_y;
 };
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st);
+// Whether that many rows of one group are quantized by the product's workgroups
+// themselves.
+constexpr int64_t kFusedBytes = 32768;
+inline bool int8_fuses(int64_t rows, int64_t kpad) {
+  return rows <= 16 && rows * kpad <= kFusedBytes;
+}
+// Quantizes q.x into q.q and q.scale, which are a.a and a.sa, and multiplies; where
+// it fuses and there is one group without offsets, q.q and q.scale are not used.
+hipError_t launch_int8_linear(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st);
 
 constexpr int kMaxFfnGroups = 1024;
 constexpr int64_t kInt8MaxK = 131071;   // 128 * 128 * k stays below 2^31

@@ -8,6 +8,7 @@
 #include "block_device.h"
 #include "ffn_kernels.h"
 #include "group_device.h"
+#include "int8_device.h"
 
 namespace ufp4 {
 
@@ -125,6 +126,119 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_rows_kernel(const Int8Gem
     }
     __syncthreads();
   }
+}
+
+// ---------------------------------------------------------------------------
+// The same for so few rows of x, in one group, that every workgroup quantizes them
+// by itself: one launch instead of two, and no workspace.  The waves share out the
+// rows (or parts of one), their largest elements meet in LDS, the codes go to LDS,
+// and the products read them there.  The first loads of w are on their way
+// meanwhile.
+// ---------------------------------------------------------------------------
+template <typename T, int ACT>
+__global__ __launch_bounds__(64 * kRowWaves) void int8_fused_kernel(const Int8GemmArgs a,
+                                                                    const Int8QuantArgs q) {
+  constexpr bool GATED = ACT != UFP4_ACT_NONE;
+  constexpr int P = GATED ? 2 : 1, V = Elem<T>::V;
+  __shared__ int s_acc[kRowWaves][P][256];
+  __shared__ uint32_t s_top[16][kRowWaves];
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
+  const int64_t out_n = a.N / P;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, chunk = (lane >> 4) * 16;
+  const int rows = (int)a.M, kpad = (int)a.kpad, cols = (int)q.cols;
+  const int line = kpad + 16;                     // 16 more to spread the rows over the banks
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int8_t *pw[P];
+  i32x4 w[P][2];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    pw[p] = a.w + (p * out_n + min(n0 + l16, out_n - 1)) * a.kpad + chunk;
+    // a wave beyond K loads the first line and does not use it
+    const int k = wave * kStageK < kpad ? wave * kStageK : 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) w[p][u] = *reinterpret_cast<const i32x4 *>(pw[p] + k + u * 64);
+  }
+
+  // waves per row: 8 for one row, down to 1; beyond 8 rows a wave has two
+  const int parts = rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1;
+  const int part = wave % parts, row_step = kRowWaves / parts;
+  const int step = parts * 64 * V, c_first = (part * 64 + lane) * V;
+  const T *x = static_cast<const T *>(q.x);
+  for (int r = wave / parts; r < rows; r += row_step) {
+    uint32_t top = 0;
+    for (int c = c_first; c < cols; c += step) {
+      float f[V];
+      Elem<T>::unpack(load_vec(x + r * q.ld_x + c, cols - c), f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(fabsf(f[j])));
+    }
+    top = lanes_max(top);
+    if (lane == 0) s_top[r][part] = top;
+  }
+  __syncthreads();
+  for (int r = wave / parts; r < rows; r += row_step) {
+    uint32_t top = s_top[r][0];
+    for (int i = 1; i < parts; ++i) top = max(top, s_top[r][i]);
+    const Int8Scale s = int8_scale(top);
+    for (int c = c_first; c < kpad; c += step) {
+      float f[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = 0.0f;
+      if (c < cols) Elem<T>::unpack(load_vec(x + r * q.ld_x + c, cols - c), f);
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j)
+        *reinterpret_cast<uint32_t *>(s_x + r * line + c + 4 * j) = int8x4(f + 4 * j, s);
+    }
+  }
+  __syncthreads();
+
+  i32x4 acc[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) acc[p] = i32x4(0);
+  const uint8_t *px = s_x + min(l16, rows - 1) * line + chunk;
+  for (int k = wave * kStageK; k < kpad; k += kRowWaves * kStageK) {
+    i32x4 f[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) f[u] = *reinterpret_cast<const i32x4 *>(px + k + u * 64);
+    i32x4 next[P][2];
+    const int k1 = k + kRowWaves * kStageK < kpad ? k + kRowWaves * kStageK : k;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        next[p][u] = *reinterpret_cast<const i32x4 *>(pw[p] + k1 + u * 64);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        acc[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[u], w[p][u], acc[p], 0, 0, 0);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) w[p][u] = next[p][u];
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s_acc[wave][p][(4 * (lane >> 4) + r) * 16 + l16] = acc[p][r];
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  const int m = threadIdx.x >> 4;
+  const int64_t n = n0 + l16, up = GATED ? n + out_n : n;
+  if (m >= rows || n >= out_n) return;
+  int sum[2] = {0, 0};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < kRowWaves; ++i) sum[p] += s_acc[i][p][threadIdx.x];
+  uint32_t top = s_top[m][0];
+  for (int i = 1; i < parts; ++i) top = max(top, s_top[m][i]);
+  const bool bias = a.bias != nullptr;
+  put(a, m, n,
+      finish<ACT>(sum[0], sum[1], int8_scale(top).scale, a.sw[n], a.sw[up], bias ? a.bias[n] : 0.0f,
+                  bias ? a.bias[up] : 0.0f, bias));
 }
 
 // ---------------------------------------------------------------------------
@@ -435,6 +549,27 @@ static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t middle = ((a.M + 127) / 128) * ((a.N + 127) / 128);
   if (middle >= 512) return launch_tiles<2, 2, 2, ACT>(a, st);
   return launch_tiles<2, 2, 1, ACT>(a, st);
+}
+
+template <typename T, int ACT>
+static hipError_t launch_fused(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st) {
+  const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
+  hipLaunchKernelGGL((int8_fused_kernel<T, ACT>), dim3((unsigned)((out_n + 15) / 16)),
+                     dim3(64 * kRowWaves), (size_t)(a.M * (a.kpad + 16)), st, a, q);
+  return hipGetLastError();
+}
+template <typename T>
+static hipError_t fused(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st) {
+  if (a.act == UFP4_ACT_NONE) return launch_fused<T, UFP4_ACT_NONE>(a, q, st);
+  return a.act == UFP4_ACT_SILU ? launch_fused<T, UFP4_ACT_SILU>(a, q, st)
+                                : launch_fused<T, UFP4_ACT_GELU>(a, q, st);
+}
+hipError_t launch_int8_linear(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st) {
+  if (a.M == 0) return hipSuccess;
+  if (a.goff == nullptr && int8_fuses(a.M, a.kpad))
+    return q.bf16 ? fused<uint16_t>(a, q, st) : fused<float>(a, q, st);
+  const hipError_t e = launch_int8_quantize(q, st);
+  return e == hipSuccess ? launch_int8_gemm(a, st) : e;
 }
 
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st) {

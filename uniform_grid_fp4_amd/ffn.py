@@ -52,7 +52,7 @@ def lib() -> ctypes.CDLL:
     L.ufp4_int8_quantize.argtypes = [P, I64, I32, I64, I64, P, P, P]
     L.ufp4_int8_gemm.argtypes = [R, R, P, I32, I32, P, I32, P, I64, P]
     L.ufp4_int8_linear.argtypes = [P, I64, I32, I64, I64, R, P, I32, I32, P, I32, P, I64, P, S, P]
-    L.ufp4_int8_linear_workspace_size.argtypes = [I64, I64]
+    L.ufp4_int8_linear_workspace_size.argtypes = [I64, I64, I32]
     for f in EXPORTS:
         getattr(L, f).restype = S if f.endswith("_size") else I32
     _lib = L
@@ -60,8 +60,31 @@ def lib() -> ctypes.CDLL:
 
 
 def _call(name: str, device: torch.device, *args):
-    lib()
-    B._call(name, device, *args)
+    """As block._call."""
+    index = device.index
+    if index == B._current_device():
+        st = getattr(lib(), name)(*args, B._raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, B._raw_stream(index))
+    if st:
+        U._check(st, name)
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor) -> int:
+    """block._rows2d of a tensor like another; dense ones, as most are, take one
+    look (these checks are a third of a small call's time)."""
+    if t.dtype == like.dtype and t.shape == like.shape and t.device == like.device \
+            and t.is_contiguous():
+        return t.shape[1]
+    return _rows2d(t, name, like)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int, device) -> torch.Tensor:
+    """block._exact of n numbers."""
+    if t.dtype == dtype and t.shape == (n,) and t.device == device and t.is_contiguous():
+        return t
+    return _exact(t, name, dtype, (n,), device)
 
 
 # ---------------------------------------------------------------------------
@@ -83,22 +106,26 @@ def ufp4_layernorm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     weight and bias are of x's type or both float32.  `out_h` receives the sum
     and may be x or residual itself (in place)."""
     ld = _rows2d(x, "x")
-    wd = _weight(weight, x)
     rows, cols = x.shape
-    dev = x.device
+    dev, dtype = x.device, x.dtype
+    wtype = weight.dtype
+    if wtype != dtype and wtype != torch.float32:
+        raise TypeError(f"weight is {dtype} or float32, got {wtype}")
+    _vector(weight, "weight", wtype, cols, dev)
+    pb = pr = ph = None
     if bias is not None:
-        _exact(bias, "bias", weight.dtype, (cols,), dev)
+        pb = _vector(bias, "bias", wtype, cols, dev).data_ptr()
     ldr, h = 0, x
     if residual is not None:
-        ldr = _rows2d(residual, "residual", x)
-        h = _new(x) if out_h is None else _exact(out_h, "out_h", x.dtype, (rows, cols), dev)
+        ldr = _rows(residual, "residual", x)
+        h = _new(x) if out_h is None else _exact(out_h, "out_h", dtype, (rows, cols), dev)
+        pr, ph = residual.data_ptr(), h.data_ptr()
     elif out_h is not None:
         raise ValueError("out_h is given without a residual")
     y = _new(x)
     mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
-    _call("ufp4_layernorm", dev, _p(x), ld, _p(residual), ldr, _p(weight), _p(bias),
-          _CODE[x.dtype], wd, rows, cols, eps, _p(h) if residual is not None else None, _p(y),
-          _p(mean), _p(rstd))
+    _call("ufp4_layernorm", dev, x.data_ptr(), ld, pr, ldr, weight.data_ptr(), pb, _CODE[dtype],
+          _CODE[wtype], rows, cols, eps, ph, y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     if out_h is not None:
         _written(out_h)
     return LayerNormOut(y, h, mean, rstd)
@@ -116,13 +143,13 @@ def ufp4_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, 
     reaches h from elsewhere (None: nothing).  dx is the gradient of x and of
     the residual; dw and db have the weight's type; db is None without `bias`."""
     ldh = _rows2d(h, "h")
-    ldy = _rows2d(dy, "dy", h)
-    ldd = _rows2d(dh, "dh", h) if dh is not None else 0
+    ldy = _rows(dy, "dy", h)
+    ldd = _rows(dh, "dh", h) if dh is not None else 0
     wd = _weight(weight, h)
     rows, cols = h.shape
     dev = h.device
-    _exact(mean, "mean", torch.float32, (rows,), dev)
-    _exact(rstd, "rstd", torch.float32, (rows,), dev)
+    _vector(mean, "mean", torch.float32, rows, dev)
+    _vector(rstd, "rstd", torch.float32, rows, dev)
     dx, dw = _new(h), torch.empty_like(weight)
     db = torch.empty_like(weight) if bias else None
     ws, nbytes = _workspace(workspace, lib().ufp4_layernorm_bwd_workspace_size(rows, cols), dev)
@@ -154,7 +181,7 @@ def ufp4_dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.
         raise ValueError(f"p = {p}: a probability")
     ldr = 0
     if residual is not None:
-        ldr = _rows2d(residual, "residual", x)
+        ldr = _rows(residual, "residual", x)
     y = _new(x) if out is None else _exact(out, "out", x.dtype, (rows, cols), dev)
     there = None
     if isinstance(offset, torch.Tensor):
@@ -178,11 +205,16 @@ class GatedOut(NamedTuple):
 
 
 def _operand(q: U.Quantized, name: str, device=None) -> U.QTensorDesc:
-    dev = q.codes.device if device is None else device
-    if not q.codes.is_cuda:
-        raise ValueError(f"{name} is not on a GPU")
-    _exact(q.codes, f"{name}.codes", torch.uint8, (q.rows, q.kpad // 2), dev)
-    _exact(q.scales, f"{name}.scales", torch.float32, (q.rows, q.kpad // 16), dev)
+    codes, scales, rows, kpad = q.codes, q.scales, q.rows, q.kpad
+    dev = codes.device if device is None else device
+    if not (codes.is_cuda and codes.device == dev and scales.device == dev
+            and codes.dtype == torch.uint8 and scales.dtype == torch.float32
+            and codes.shape == (rows, kpad // 2) and scales.shape == (rows, kpad // 16)
+            and codes.is_contiguous() and scales.is_contiguous()):
+        if not codes.is_cuda:
+            raise ValueError(f"{name} is not on a GPU")
+        _exact(codes, f"{name}.codes", torch.uint8, (rows, kpad // 2), dev)
+        _exact(scales, f"{name}.scales", torch.float32, (rows, kpad // 16), dev)
     return q.desc()
 
 
@@ -234,7 +266,7 @@ def ufp4_gated_bwd(dy: torch.Tensor, gu: torch.Tensor, act: int = ACT_SILU,
     if cols % 2:
         raise ValueError(f"gu is [rows, 2 ffn], got {tuple(gu.shape)}")
     _like(dy, "dy", gu.dtype, (rows, cols // 2), gu.device)
-    ldy = _rows2d(dy, "dy")
+    ldy = cols // 2 if dy.is_contiguous() else _rows2d(dy, "dy")
     dgu = _new(gu) if out is None else _exact(out, "out", gu.dtype, (rows, cols), gu.device)
     _call("ufp4_gated_bwd", gu.device, _p(dy), ldy, _p(gu), ldg, act, _CODE[gu.dtype], rows,
           cols // 2, _p(dgu))
@@ -277,9 +309,11 @@ def _int8_operand(r: Int8Rows, name: str, device) -> array:
     if q.dim() != 2 or not 1 <= k or q.shape[1] != int8_kpad(k):
         raise ValueError(f"{name}.q is [rows, {int8_kpad(max(1, k))}] for k = {k}, got "
                          f"{tuple(q.shape)}")
-    _exact(q, f"{name}.q", torch.int8, q.shape, device)
-    _exact(scale, f"{name}.scale", torch.float32, (q.shape[0],), device)
-    return array("Q", (q.data_ptr(), scale.data_ptr(), q.shape[0], k))
+    if not (q.dtype == torch.int8 and q.device == device and q.is_contiguous()):
+        _exact(q, f"{name}.q", torch.int8, q.shape, device)
+    n = q.shape[0]
+    _vector(scale, f"{name}.scale", torch.float32, n, device)
+    return array("Q", (q.data_ptr(), scale.data_ptr(), n, k))
 
 
 def _int8_out(rows: int, w: Int8Rows, bias, act: int, offsets, out_dtype, device):
@@ -291,7 +325,7 @@ def _int8_out(rows: int, w: Int8Rows, bias, act: int, offsets, out_dtype, device
     n = w.q.shape[0]
     cols = _rows_per_group(n, groups, 1 if act == ACT_NONE else 2)
     if bias is not None:
-        _exact(bias, "bias", torch.float32, (n,), device)
+        _vector(bias, "bias", torch.float32, n, device)
     return words, groups, torch.empty((rows, cols), dtype=out_dtype, device=device)
 
 
@@ -312,8 +346,8 @@ def ufp4_int8_gemm(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None
     return y
 
 
-def ufp4_int8_linear_workspace_size(rows: int, cols: int) -> int:
-    return int(lib().ufp4_int8_linear_workspace_size(rows, cols))
+def ufp4_int8_linear_workspace_size(rows: int, cols: int, grouped: bool = False) -> int:
+    return int(lib().ufp4_int8_linear_workspace_size(rows, cols, int(grouped)))
 
 
 def ufp4_int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] = None,
@@ -329,7 +363,8 @@ def ufp4_int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] 
         raise ValueError(f"x has rows of {cols}, w of {w.k}")
     out_dtype = x.dtype if out_dtype is None else out_dtype
     dw, groups, y = _int8_out(rows, w, bias, act, offsets, out_dtype, dev)
-    ws, nbytes = _workspace(workspace, lib().ufp4_int8_linear_workspace_size(rows, cols), dev)
+    need = lib().ufp4_int8_linear_workspace_size(rows, cols, offsets is not None)
+    ws, nbytes = (None, 0) if need == 0 else _workspace(workspace, need, dev)
     _call("ufp4_int8_linear", dev, _p(x), ld, _CODE[x.dtype], rows, cols, dw.buffer_info()[0],
           _p(bias), act, groups, _p(offsets), _CODE[out_dtype], _p(y), y.shape[1], _p(ws), nbytes)
     return y
