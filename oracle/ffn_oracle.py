@@ -84,25 +84,30 @@ def act(g, kind):
 
 def act_error(g, kind, u):
     """Bounds of what FP32 makes of (value, slope), u half a step.  silu: p is
-    within 7 u of itself (the exponential two steps, the sum, the reciprocal with
-    its Newton step), 1 - p within that and u, and three more roundings follow.
-    gelu: the argument of erfc is off by 2 u of itself (the constant and the
-    product), which moves c = erfc / 2 by 2 u |g| phi(g); erfc itself is granted 16
-    steps; exp(-g^2 / 2) is off by (1.5 g^2 + 2) u of itself, and each product
-    and sum adds u.  What is below the normal numbers may be zero."""
+    within 6 u of itself (the exponential and the reciprocal two each, the sum) and
+    1.3 |g| u where g < 0, 1 u where g >= 0, for the rounded exponent; 1 - p is off by
+    as much of p and u, and three more roundings follow.  gelu: the argument of erfc is off by 2 u of itself (the constant and the
+    product), which moves c = erfc / 2 by 2 u |g| phi(g); erfc itself is granted
+    6 (1 + g^2 / 2) u for its fit and exponent, 12 u for its reciprocal and
+    exponential (two each, at a slope of up to 2) and 4 u for its products, of the
+    half h = min(c, 1 - c) that is computed; exp(-g^2 / 2) is off by (1.5 g^2 + 4) u
+    of itself, and each product and sum adds u.  What is below the normal numbers may
+    be zero."""
     g = np.asarray(g, np.float64)
     value, slope = act(g, kind)
     tiny = 1e-36 * (1.0 + np.abs(g))
     if kind == SILU:
         e = np.exp(-np.abs(g))
         p = np.where(g >= 0, 1.0, e) / (1.0 + e)
-        return (10 * u * np.abs(value) + tiny,
-                12 * u * p * (1.0 + np.abs(g) * (1.0 - p)) + 9 * u * p * p * np.abs(g) + tiny)
+        rel = (6 + np.where(g < 0, 1.3 * np.abs(g), 1.0)) * u
+        return ((rel + 2 * u) * np.abs(value) + tiny,
+                (rel + 4 * u) * p * (1.0 + np.abs(g) * (1.0 - p)) + (rel + u) * p * p * np.abs(g)
+                + u * p * np.abs(g) + tiny)
     c = 0.5 * _erfc(-g / math.sqrt(2.0)) if g.size else g
     phi = np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
-    c_err = 2 * u * np.abs(g) * phi + 33 * u * c
+    c_err = 2 * u * np.abs(g) * phi + (22 + 3 * g * g) * u * np.minimum(c, 1 - c) + u * (g > 0)
     return (np.abs(g) * c_err + 2 * u * np.abs(value) + tiny,
-            c_err + (1.5 * g * g + 6) * u * np.abs(g) * phi + 2 * u * np.abs(slope) + tiny)
+            c_err + (1.5 * g * g + 8) * u * np.abs(g) * phi + 2 * u * np.abs(slope) + tiny)
 
 
 # -- int8 -------------------------------------------------------------------------
