@@ -6,12 +6,15 @@
 //
 // A workgroup has 32 rows and 32 columns of either projection, and its eight
 // waves split K: each takes every eighth run of four blocks, straight from
-// memory into registers (32 bytes of codes and 16 of scales per row and run), and
-// expands its own nibbles.  Per block the arithmetic is gemm.hip's: two FP8
-// products, one FP32 outer product of the scales, one FMA per output.  The eight
-// partial sums meet in LDS and are added in the order of the waves.  Nothing is
-// shared between waves before that, so there are no barriers along K and all
-// loads of a run are in flight together, for 4 to 8 times the reads of the L2.
+// memory into registers, and expands its own nibbles.  Per block the arithmetic is
+// gemm.hip's: two FP8 products, one FP32 outer product of the scales, one FMA per
+// output.  The eight partial sums meet in LDS and are added in the order of the
+// waves.  Nothing is shared between waves before that, so there are no barriers
+// along K, for 4 to 8 times the reads of the L2.  Bound by the cache lines that its
+// loads touch (192 per wave and run, every row another line): reading each row's
+// run once per wave and exchanging words between the halves of the wave, instead of
+// in both halves, took 512 x 2048 columns, K = 2048, from 42 to 34 us; loading a run
+// ahead gained nothing.
 #include "act_device.h"
 #include "block_device.h"
 #include "group_device.h"
@@ -22,7 +25,6 @@ namespace ufp4 {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx32 __attribute__((ext_vector_type(32)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x4_dword __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kSmallWaves = 8;
@@ -52,6 +54,24 @@ __device__ __forceinline__ void block_product(uint32_t x, uint32_t g, uint32_t u
   for (int r = 0; r < 16; ++r) acc[1][r] = fmaf(S[16 + r], p1[r], acc[1][r]);
 }
 
+// Four blocks of a row.  A lane of the wave's lower half loads the first two, its
+// counterpart in the upper half the other two: 32 rows and 32 bytes of each, in
+// one access.  Exchanging the upper half of a block's first word with the lower half
+// of its second gives both halves their own four bytes of the first pair's block
+// and of the second's.
+struct FourBlocks {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    const u32x4_dword v = *reinterpret_cast<const u32x4_dword *>(p);
+    const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[1], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v[2], v[3], false, false);
+    w[0] = a[0];
+    w[1] = b[0];
+    w[2] = a[1];
+    w[3] = b[1];
+  }
+};
+
 template <int GRID>
 __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const GemmArgs a,
                                                                        int64_t tiles_n) {
@@ -78,33 +98,25 @@ __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const Gem
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
-  for (int kb = wave * 4; kb < nkb; kb += kSmallWaves * 4) {
-    if (kb + 4 <= nkb) {
-      // both halves of the wave read whole blocks and keep their own four bytes
-      u32x4_dword x[2], g[2], u[2];
+  const int runs = nkb / 4;                       // of four blocks
+  for (int i = wave; i < runs; i += kSmallWaves) {
+    FourBlocks x, g, u;
+    x.load(qx + i * 32 + half * 16);
+    g.load(qg + i * 32 + half * 16);
+    u.load(qu + i * 32 + half * 16);
+    const u32x4_dword fx = *reinterpret_cast<const u32x4_dword *>(sx + i * 4);
+    const u32x4_dword fw = *reinterpret_cast<const u32x4_dword *>(sw + i * 4);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[i] = *reinterpret_cast<const u32x4_dword *>(qx + kb * 8 + i * 16);
-        g[i] = *reinterpret_cast<const u32x4_dword *>(qg + kb * 8 + i * 16);
-        u[i] = *reinterpret_cast<const u32x4_dword *>(qu + kb * 8 + i * 16);
-      }
-      const u32x4_dword fx = *reinterpret_cast<const u32x4_dword *>(sx + kb);
-      const u32x4_dword fw = *reinterpret_cast<const u32x4_dword *>(sw + kb);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int i = b >> 1, lo = (b & 1) * 2;
-        block_product<GRID>(half ? x[i][lo + 1] : x[i][lo], half ? g[i][lo + 1] : g[i][lo],
-                            half ? u[i][lo + 1] : u[i][lo], __uint_as_float(fx[b]),
-                            __uint_as_float(fw[b]), acc);
-      }
-    } else {
-      for (int k = kb; k < nkb; ++k)
-        block_product<GRID>(*reinterpret_cast<const uint32_t *>(qx + k * 8 + half * 4),
-                            *reinterpret_cast<const uint32_t *>(qg + k * 8 + half * 4),
-                            *reinterpret_cast<const uint32_t *>(qu + k * 8 + half * 4), sx[k],
-                            sw[k], acc);
-    }
+    for (int b = 0; b < 4; ++b)
+      block_product<GRID>(x.w[b], g.w[b], u.w[b], __uint_as_float(fx[b]), __uint_as_float(fw[b]),
+                          acc);
   }
+  // the last blocks, one to a wave
+  if (const int k = runs * 4 + wave; k < nkb)
+    block_product<GRID>(*reinterpret_cast<const uint32_t *>(qx + k * 8 + half * 4),
+                        *reinterpret_cast<const uint32_t *>(qg + k * 8 + half * 4),
+                        *reinterpret_cast<const uint32_t *>(qu + k * 8 + half * 4), sx[k], sw[k],
+                        acc);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
