@@ -3,6 +3,7 @@
 // on v_mfma_i32_*_i8, whose sums are exact: any order and split of K gives the
 // same bits.
 #include <atomic>
+#include <cmath>
 
 #include "act_device.h"
 #include "block_device.h"
@@ -14,6 +15,7 @@ namespace ufp4 {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr int kXcd = 8;
 constexpr int kStageK = 128;                     // bytes of K per LDS stage: a row's piece is a line
@@ -446,13 +448,20 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
     for (int j = 0; j < W / 32; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half;
+        const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half, n1 = GATED ? n0 + 32 : n0;
+        const floatx4 sg = *reinterpret_cast<const floatx4 *>(s_sw + n0);
+        const floatx4 su = *reinterpret_cast<const floatx4 *>(s_sw + n1);
+        floatx4 bg = 0.0f, bu = 0.0f;
+        if (a.bias != nullptr) {
+          bg = *reinterpret_cast<const floatx4 *>(s_bias + n0);
+          bu = *reinterpret_cast<const floatx4 *>(s_bias + n1);
+        }
         float v[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          const int n = n0 + z, r = q * 4 + z;
-          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, s_sw[n], GATED ? s_sw[n + 32] : 0.0f,
-                             s_bias[n], GATED ? s_bias[n + 32] : 0.0f, a.bias != nullptr);
+          const int r = q * 4 + z;
+          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, sg[z], su[z], bg[z], bu[z],
+                             a.bias != nullptr);
         }
         uint8_t *p = line + l32 * kLine + (j * 32 + 8 * q + 4 * half) * out_bytes;
         if (a.out_bf16) {
@@ -528,6 +537,39 @@ static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
   return hipSuccess;
 }
 
+// Which tiles: those whose time, estimated from their number per CU at even groups,
+// is least.  A CU holds one workgroup of 256 x 256, two of 128 x 128 or three of 64 x
+// 128; the last one to start costs as much as a full set.  The unit is 1.0 us per
+// stage of K, and a workgroup's start and end cost as much as 5 stages where nothing
+// hides them and 3.5 where another one runs beside it.  Measured, us (256 x 256, 128
+// x 128, 64 x 128):
+//   8192 x 2048 to 2 x 8192, gated                314   366   489
+//   10000 x 2048 to 2 x 1408, gated, 32 groups    148   125   165
+//   24000 x 64 to 2 x 3648, gated, 32 groups      164   155   216
+//   3808 x 6065 to 2172, 8 groups                  97   112   137
+//   4000, 2000, 1000 x 4096 to 4096                71    86   110;   61  46  57;   58  33  31
+//   500 x 2048 to 2048                             32    18    13
+template <int ACT>
+static hipError_t launch_best_tiles(const Int8GemmArgs &a, hipStream_t st) {
+  const int64_t per = (a.M + a.n_groups - 1) / a.n_groups;      // rows of an even group
+  const double stages = (double)(a.kpad / kStageK);
+  auto per_cu = [&](int64_t bm, int64_t bn) {
+    return (double)((per + bm - 1) / bm * ((a.N + bn - 1) / bn) * a.n_groups) / 256.0;
+  };
+  const double big = per_cu(256, 256), middle = per_cu(128, 128), small = per_cu(64, 128);
+  const double pairs = std::floor(middle / 2.0), left = middle - 2.0 * pairs;
+  const double t_big = std::ceil(big) * 1.96 * (stages + 5.0);
+  const double t_middle =
+      (pairs * 1.3 + (left <= 0.0 ? 0.0 : left <= 1.0 ? 0.95 : 1.2)) * (stages + 3.5);
+  const double whole = std::floor(small);
+  const double t_small = (small <= 1.0   ? 0.75
+                          : small <= 2.0 ? 0.9
+                                         : whole * 0.41 + (small > whole ? 0.9 : 0.0)) *
+                         (stages + 3.5);
+  if (t_big <= t_middle && t_big <= t_small) return launch_tiles<2, 4, 4, ACT>(a, st);
+  return t_middle <= t_small ? launch_tiles<2, 2, 2, ACT>(a, st) : launch_tiles<2, 2, 1, ACT>(a, st);
+}
+
 template <int ACT>
 static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t rows = (a.M + a.n_groups - 1) / a.n_groups;
@@ -541,14 +583,7 @@ static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   if (rows <= 16) return launch_rows<1, ACT>(a, st);
   if (rows <= 32 && groups16 <= 1024) return launch_rows<2, ACT>(a, st);
   if (rows <= 64 && groups16 <= 512) return launch_rows<4, ACT>(a, st);
-  // The largest tiles that fill the GPU: 4000 x 4096 x 4096: 71 us, with 128-row
-  // tiles 86, with 64-row ones 110; 2000 x 4096 x 4096: 61, 46 and 57 us; 1000 x 4096
-  // x 4096: 58, 33 and 31 us; 500 x 2048 x 2048: 32, 18 and 13 us.
-  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= 256) return launch_tiles<2, 4, 4, ACT>(a, st);
-  const int64_t middle = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (middle >= 512) return launch_tiles<2, 2, 2, ACT>(a, st);
-  return launch_tiles<2, 2, 1, ACT>(a, st);
+  return launch_best_tiles<ACT>(a, st);
 }
 
 template <typename T, int ACT>
