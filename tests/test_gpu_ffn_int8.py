@@ -141,6 +141,22 @@ def test_large_tiles(m, n):
     assert torch.equal(F.ufp4_int8_gemm(few, w, act=F.ACT_SILU, out_dtype=torch.float32), g[pick])
 
 
+@pytest.mark.parametrize("m,n,k", [(65, 66, 513), (129, 300, 900), (1000, 70, 6080), (70, 34, 131),
+                                   (905, 1536, 1411), (460, 2050, 1300)])
+def test_few_tiles_of_a_long_contraction(m, n, k):
+    """Tiles that split K over their waves, with a number of stages that the parts
+    share and with one that they do not."""
+    check(*operands(m, n, k))
+
+
+@pytest.mark.parametrize("counts", [[65, 0, 66, 64, 1, 70], [300, 20, 140]])
+def test_grouped_few_tiles(counts):
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    for n, k in ((34, 1411), (258, 640)):
+        a, w = operands(int(off[-1]), n * len(counts), k)
+        check(a, w, torch.from_numpy(off).to(DEV), off)
+
+
 COUNTS = [[5, 0, 130, 1, 0, 64], [0, 0, 7], [40], [1] * 70, [0, 129], [300, 0, 280, 3],
           [0, 0], [0, 33, 0, 0, 0, 0, 0, 0]]
 

@@ -76,7 +76,8 @@ template <int GRID>
 __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const GemmArgs a,
                                                                        int64_t tiles_n) {
   __shared__ float s_acc[kSmallWaves][2][kSmallRows * kSmallCols];
-  const GroupTile t = group_tile(a.goff, a.n_groups, a.M, kSmallRows, tiles_n, blockIdx.x);
+  const GroupTile t = group_tile(a.goff, a.n_groups, a.M, kSmallRows, tiles_n,
+                                 [](int64_t) { return (int64_t)blockIdx.x; });
   if (t.e < 0) return;
   // row tiles next to each other share w's rows
   const int64_t tn = t.local / t.tiles_m, tm = t.local - tn * t.tiles_m;

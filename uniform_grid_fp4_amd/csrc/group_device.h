@@ -11,7 +11,7 @@ __device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) {
   return v < 0 ? 0 : (v > n ? n : v);
 }
 
-// The group and the tile in it of tile t, where group e has ceil(rows of e / bm)
+// The group and the tile in it of tile t = pick(number of tiles), where group e has ceil(rows of e / bm)
 // * per_row tiles.  Offsets are clamped to [0, M], a decreasing pair is an empty
 // group.  Every wave finds it by itself: a lane sums a run of groups, a scan over
 // the lanes finds the run, and the run is walked.
@@ -19,11 +19,13 @@ struct GroupTile {
   int e;                                         // -1: past the last tile
   int64_t row0, rows, local, tiles_m;
 };
+template <typename P>
 __device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_groups, int64_t M,
-                                                int bm, int64_t per_row, int64_t t) {
-  GroupTile g{0, 0, M, t, (M + bm - 1) / bm};
+                                                int bm, int64_t per_row, P pick) {
+  GroupTile g{0, 0, M, 0, (M + bm - 1) / bm};
   if (goff == nullptr) {
-    if (t >= g.tiles_m * per_row) g.e = -1;
+    g.local = pick(g.tiles_m * per_row);
+    if (g.local >= g.tiles_m * per_row) g.e = -1;
     return g;
   }
   const int lane = threadIdx.x & 63;
@@ -42,6 +44,7 @@ __device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_group
     const int64_t v = __shfl_up(incl, o, 64);
     if (lane >= o) incl += v;
   }
+  const int64_t t = pick((int64_t)__shfl(incl, 63, 64));
   const uint64_t over = __ballot(incl > t);
   if (over == 0) {
     g.e = -1;

@@ -247,6 +247,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_fused_kernel(const Int8Ge
 // Many rows: BM x BN tiles of p (BM = 32 MT WM, BN = 64 WN), one per workgroup of
 // WM x WN waves, a wave owning 32 MT x 64 of it in 32x32 tiles; gated: its two
 // tiles of a row are the gate's and the up projection's of the same 32 columns.
+// Where the tiles are fewer than the CUs, a workgroup has KS such sets of waves,
+// each with its own stages of K (every KS-th) and its own LDS, so that one set's
+// products cover another's waits; their integer sums meet in LDS.
 //
 // K goes through LDS in stages of 128 bytes per row, double-buffered, brought
 // there by buffer loads that write LDS directly (16 bytes a lane, no registers).
@@ -297,34 +300,37 @@ __device__ __forceinline__ void store_cols(T *p, int n, u32x4 v) {
 }
 
 constexpr int kBandRows = 8;       // tile rows that neighbouring workgroups share w's panels over
-template <int WM, int WN, int MT>
+template <int WM, int WN, int MT, int KS>
 struct TileShape {
-  static constexpr int kThreads = 64 * WM * WN, kBM = 32 * MT * WM, kBN = 64 * WN;
+  static constexpr int kThreads = 64 * WM * WN * KS, kBM = 32 * MT * WM, kBN = 64 * WN;
   static constexpr int kStage = (kBM + kBN) * kStageK;
-  // two stages; the rows' scales; the columns' scales and biases
-  static constexpr size_t kLds = 2 * kStage + (kBM + 2 * kBN) * sizeof(float);
+  // the stages; the rows' scales; the columns' scales and biases
+  static constexpr size_t kLds = KS * 2 * kStage + (kBM + 2 * kBN) * sizeof(float);
 };
 
-template <int WM, int WN, int MT, int ACT>
-__global__ __attribute__((amdgpu_flat_work_group_size(64 * WM * WN, 64 * WM * WN),
+template <int WM, int WN, int MT, int KS, int ACT>
+__global__ __attribute__((amdgpu_flat_work_group_size(64 * WM * WN * KS, 64 * WM * WN * KS),
                           amdgpu_waves_per_eu(2, 2))) void
 int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
-  using S = TileShape<WM, WN, MT>;
+  using S = TileShape<WM, WN, MT, KS>;
   constexpr bool GATED = ACT != UFP4_ACT_NONE;
   constexpr int NT = 2, WAVES = WM * WN, BM = S::kBM, BN = S::kBN;
   constexpr int OUT = GATED ? BN / 2 : BN;        // output columns of a tile
   constexpr int AL = BM / (8 * WAVES), BL = BN / (8 * WAVES);   // loads per lane and stage
   static_assert(AL * 8 * WAVES == BM && BL * 8 * WAVES == BN, "rows per load");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  float *s_sa = reinterpret_cast<float *>(lds + 2 * S::kStage);
+  float *s_sa = reinterpret_cast<float *>(lds + KS * 2 * S::kStage);
   float *s_sw = s_sa + BM, *s_bias = s_sw + BN;
   const int64_t out_n = a.N / (GATED ? 2 : 1);
 
-  // The workgroups of an XCD (every eighth) walk a contiguous range of tiles, in
-  // bands of kBandRows tile rows, column by column: their panels meet in one L2.
-  const unsigned per = gridDim.x / kXcd;          // the grid is a multiple of the XCDs
-  const int64_t t = first + blockIdx.x % kXcd * per + blockIdx.x / kXcd;
-  const GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, t);
+  // The workgroups of an XCD (every eighth) walk a contiguous eighth of the tiles, in
+  // bands of kBandRows tile rows, column by column: their panels meet in one L2.  Of
+  // the tiles that there are: eighths of the grid, which is cut for the most tiles that
+  // the groups can have, would leave the last XCDs idle.
+  const GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, [=](int64_t tiles) {
+    const int64_t id = first + blockIdx.x, per = (tiles + kXcd - 1) / kXcd;
+    return id / kXcd < per ? id % kXcd * per + id / kXcd : tiles;
+  });
   if (g.e < 0) return;
   const int64_t band = g.local / (kBandRows * tiles_n);
   const int64_t in_band = g.local - band * kBandRows * tiles_n;
@@ -337,7 +343,8 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
   const int64_t w_row = (int64_t)g.e * a.N + col0;
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = id / WAVES, wave = id % WAVES; // of K, of the part
   const int wm = wave % WM, wn = wave / WM;
   const int l32 = lane & 31, half = lane >> 5;
   const int kpad = (int)a.kpad;
@@ -358,9 +365,10 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
     const int n = GATED ? (r >> 6) * 32 + (r & 31) : r;
     vw[i] = min(n, cols - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
   }
+  uint8_t *const mine = lds + part * 2 * S::kStage;
   auto issue = [&](int stage) __attribute__((always_inline)) {
-    uint8_t *st = lds + (stage & 1) * S::kStage + wave * 1024;
-    const int k0 = stage * kStageK;
+    uint8_t *st = mine + (stage & 1) * S::kStage + wave * 1024;
+    const int k0 = (stage * KS + part) * kStageK;
 #pragma unroll
     for (int i = 0; i < AL; ++i) load_lds(base_a, va[i], k0, st + i * WAVES * 1024);
 #pragma unroll
@@ -370,16 +378,25 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
       load_lds(up ? base_u : base_w, vw[i], k0, st + BM * kStageK + i * WAVES * 1024);
     }
   };
-  const int stages = kpad / kStageK;
-  issue(0);
-  if (stages > 1) issue(1);
-  for (int r = threadIdx.x; r < BM; r += S::kThreads) s_sa[r] = a.sa[row0 + min(r, rows - 1)];
-  for (int r = threadIdx.x; r < BN; r += S::kThreads) {
+  const int total = kpad / kStageK;
+  const int stages = (total - part + KS - 1) / KS, turns = (total + KS - 1) / KS;
+  // The scales wait in registers for the epilogue: a write to LDS would wait for all
+  // loads into it.
+  float scale_a[(BM + S::kThreads - 1) / S::kThreads];
+  float scale_w[(BN + S::kThreads - 1) / S::kThreads], bias[(BN + S::kThreads - 1) / S::kThreads];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < BM; ++i)
+    scale_a[i] = a.sa[row0 + min((int)threadIdx.x + i * S::kThreads, rows - 1)];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < BN; ++i) {
+    const int r = min((int)threadIdx.x + i * S::kThreads, BN - 1);
     const int n = min(GATED ? (r >> 6) * 32 + (r & 31) : r, cols - 1);
     const int64_t at = w_row + n + (GATED && (r >> 5) & 1 ? out_n : 0);
-    s_sw[r] = a.sw[at];
-    s_bias[r] = a.bias != nullptr ? a.bias[at] : 0.0f;
+    scale_w[i] = a.sw[at];
+    bias[i] = a.bias != nullptr ? a.bias[at] : 0.0f;
   }
+  if (stages > 0) issue(0);
+  if (stages > 1) issue(1);
 
   i32x16 acc[MT][NT];
 #pragma unroll
@@ -390,8 +407,8 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
   constexpr int KK = kStageK / 32;
   i32x4 fa[2][MT], fw[2][NT];
-  const uint8_t *pa = lds + (wm * MT * 32 + l32) * kStageK;
-  const uint8_t *pw = lds + (BM + wn * NT * 32 + l32) * kStageK;
+  const uint8_t *pa = mine + (wm * MT * 32 + l32) * kStageK;
+  const uint8_t *pw = mine + (BM + wn * NT * 32 + l32) * kStageK;
   const int sw32 = swizzle(l32);
   auto read = [&](int into, int stage, int kk) __attribute__((always_inline)) {
     const int at = (stage & 1) * S::kStage + ((2 * kk + half) ^ sw32) * 16;
@@ -406,12 +423,12 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
   wait_lds();
   meet();
   read(0, 0, 0);
-  for (int s = 0; s < stages; ++s) {
+  for (int s = 0; s < turns; ++s) {
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       if (kk + 1 < KK) {
         read((kk + 1) & 1, s, kk + 1);
-      } else if (s + 1 < stages) {
+      } else if (s + 1 < turns) {
         wait_loads();                             // of stage s + 1
         wait_lds();                               // this wave's last fragments of stage s
         meet();
@@ -420,23 +437,68 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
       }
       // the reads and loads above go out before the products below
       __builtin_amdgcn_sched_barrier(0);
+      if (KS == 1 || s < stages) {                // a part may have one stage less
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][j], fa[kk & 1][i],
+                                                              acc[i][j], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i * S::kThreads < BM; ++i)
+    if (const int r = threadIdx.x + i * S::kThreads; r < BM) s_sa[r] = scale_a[i];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < BN; ++i)
+    if (const int r = threadIdx.x + i * S::kThreads; r < BN) {
+      s_sw[r] = scale_w[i];
+      s_bias[r] = bias[i];
+    }
+  wait_lds();
+  meet();                                         // the stages' LDS is free
+  if (KS > 1) {
+    // the parts' sums meet in the first one's waves
+    i32x4 *sums = reinterpret_cast<i32x4 *>(lds) + wave * (MT * NT * 4 * 64) + lane;
+    constexpr int PART = WAVES * MT * NT * 4 * 64;
+    static_assert((KS - 1) * PART * 16 <= KS * 2 * S::kStage, "sums in LDS");
+    if (part > 0) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][j], fa[kk & 1][i], acc[i][j],
-                                                            0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const i32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                             acc[i][j][4 * q + 3]};
+            sums[(part - 1) * PART + ((i * NT + j) * 4 + q) * 64] = v;
+          }
     }
+    wait_lds();
+    meet();
+    if (part > 0) return;
+#pragma unroll
+    for (int from = 0; from < KS - 1; ++from)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const i32x4 v = sums[from * PART + ((i * NT + j) * 4 + q) * 64];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) acc[i][j][4 * q + z] += v[z];
+          }
+    wait_lds();
   }
-  wait_lds();
-  meet();                                         // the stages' LDS is free
 
   // Epilogue, 32 rows of the wave at a time through its own piece of LDS: a lane
   // has columns 8 q + 4 half + 0..3 of row l32.
   constexpr int W = GATED ? 32 : 64;              // output columns of the wave
   constexpr int kLine = W * 4 + 16;               // bytes; 16 more to spread the banks
-  static_assert(WAVES * 32 * kLine <= 2 * S::kStage, "epilogue LDS");
+  static_assert(WAVES * 32 * kLine <= KS * 2 * S::kStage, "epilogue LDS");
   uint8_t *line = lds + wave * 32 * kLine;
   const int out_bytes = a.out_bf16 ? 2 : 4;
   const int wcol = wn * W, left = cols - wcol;    // columns of the wave that exist
@@ -503,7 +565,7 @@ static hipError_t launch_rows(const Int8GemmArgs &a, hipStream_t st) {
 // The dynamic-LDS limit is a per-device function attribute: set once on each
 // device the kernel runs on (a bit per device id; concurrent first calls at worst
 // both set it, which is harmless).
-template <int WM, int WN, int MT, int ACT>
+template <int WM, int WN, int MT, int KS, int ACT>
 static hipError_t allow_lds(const void *kernel, size_t bytes) {
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -516,17 +578,17 @@ static hipError_t allow_lds(const void *kernel, size_t bytes) {
   return e;
 }
 
-template <int WM, int WN, int MT, int ACT>
+template <int WM, int WN, int MT, int KS, int ACT>
 static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
-  using S = TileShape<WM, WN, MT>;
+  using S = TileShape<WM, WN, MT, KS>;
   const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
   const int64_t out = ACT != UFP4_ACT_NONE ? S::kBN / 2 : S::kBN;
   const int64_t tiles_n = (out_n + out - 1) / out;
   const int64_t tiles_m = (a.M + S::kBM - 1) / S::kBM + (a.goff ? a.n_groups : 0);
   const int64_t total = (tiles_m * tiles_n + kXcd - 1) / kXcd * kXcd;
   constexpr int64_t kMost = 1 << 22;              // tiles of a launch: below 2^32 threads
-  auto *kernel = int8_tile_kernel<WM, WN, MT, ACT>;
-  hipError_t e = allow_lds<WM, WN, MT, ACT>((const void *)kernel, S::kLds);
+  auto *kernel = int8_tile_kernel<WM, WN, MT, KS, ACT>;
+  hipError_t e = allow_lds<WM, WN, MT, KS, ACT>((const void *)kernel, S::kLds);
   if (e != hipSuccess) return e;
   for (int64_t first = 0; first < total; first += kMost) {
     const unsigned n = (unsigned)(total - first < kMost ? total - first : kMost);
@@ -538,17 +600,24 @@ static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
 }
 
 // Which tiles: those whose time, estimated from their number per CU at even groups,
-// is least.  A CU holds one workgroup of 256 x 256, two of 128 x 128 or three of 64 x
-// 128; the last one to start costs as much as a full set.  The unit is 1.0 us per
-// stage of K, and a workgroup's start and end cost as much as 5 stages where nothing
-// hides them and 3.5 where another one runs beside it.  Measured, us (256 x 256, 128
-// x 128, 64 x 128):
-//   8192 x 2048 to 2 x 8192, gated                314   366   489
-//   10000 x 2048 to 2 x 1408, gated, 32 groups    148   125   165
-//   24000 x 64 to 2 x 3648, gated, 32 groups      164   155   216
-//   3808 x 6065 to 2172, 8 groups                  97   112   137
-//   4000, 2000, 1000 x 4096 to 4096                71    86   110;   61  46  57;   58  33  31
-//   500 x 2048 to 2048                             32    18    13
+// is least.  A CU holds one workgroup of 256 x 256, two of 128 x 128, three of 64 x
+// 128, or one of those that split K; the last one to start costs as much as a full
+// set.  A workgroup's start and end cost as much as the added stages of K.  Measured,
+// us:
+//                                  256x256 128x128 64x128 64x128/2 64x64/4
+//   8192 x 2048 to 2 x 8192, gated     300     350    488      572     815
+//   10000 x 2048 to 2 x 1408, gated,
+//     32 groups                        124     124    151      185     247
+//   24000 x 64 to 2 x 3648, gated,
+//     32 groups                        140     142    197      395     805
+//   3808 x 6065 to 2172, 8 groups       96     108    131      140     164
+//   24000 x 512 to 2048                 53      56     71
+//   2000 x 4096 to 4096                 56      43     53
+//   1000 x 4096 to 4096                 58      32     29       35      46
+//   905 x 2560 to 2 x 768, gated        40      20     16       13      17
+//   500 x 2048 to 2048                  32      17     13       10     8.3
+//   200 x 4096 to 4096                  54      28     23       17      13
+//   1000 x 6080 to 128                  78      38     27       20      15
 template <int ACT>
 static hipError_t launch_best_tiles(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t per = (a.M + a.n_groups - 1) / a.n_groups;      // rows of an even group
@@ -556,18 +625,27 @@ static hipError_t launch_best_tiles(const Int8GemmArgs &a, hipStream_t st) {
   auto per_cu = [&](int64_t bm, int64_t bn) {
     return (double)((per + bm - 1) / bm * ((a.N + bn - 1) / bn) * a.n_groups) / 256.0;
   };
-  const double big = per_cu(256, 256), middle = per_cu(128, 128), small = per_cu(64, 128);
+  const double middle = per_cu(128, 128), small = per_cu(64, 128);
   const double pairs = std::floor(middle / 2.0), left = middle - 2.0 * pairs;
-  const double t_big = std::ceil(big) * 1.96 * (stages + 5.0);
-  const double t_middle =
-      (pairs * 1.3 + (left <= 0.0 ? 0.0 : left <= 1.0 ? 0.95 : 1.2)) * (stages + 3.5);
   const double whole = std::floor(small);
-  const double t_small = (small <= 1.0   ? 0.75
-                          : small <= 2.0 ? 0.9
-                                         : whole * 0.41 + (small > whole ? 0.9 : 0.0)) *
-                         (stages + 3.5);
-  if (t_big <= t_middle && t_big <= t_small) return launch_tiles<2, 4, 4, ACT>(a, st);
-  return t_middle <= t_small ? launch_tiles<2, 2, 2, ACT>(a, st) : launch_tiles<2, 2, 1, ACT>(a, st);
+  const double t[5] = {
+      std::ceil(per_cu(256, 256)) * 1.96 * (stages + 5.0),
+      (pairs * 1.3 + (left <= 0.0 ? 0.0 : left <= 1.0 ? 0.95 : 1.2)) * (stages + 3.5),
+      (small <= 1.0   ? 0.65
+       : small <= 2.0 ? 0.83
+                      : whole * 0.41 + (small > whole ? 0.9 : 0.0)) * (stages + 3.5),
+      std::ceil(small) * 0.42 * (stages + 9.0),
+      std::ceil(per_cu(64, 64)) * 0.29 * (stages + 12.5)};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (t[i] < t[best]) best = i;
+  switch (best) {
+    case 0: return launch_tiles<2, 4, 4, 1, ACT>(a, st);
+    case 1: return launch_tiles<2, 2, 2, 1, ACT>(a, st);
+    case 2: return launch_tiles<2, 2, 1, 1, ACT>(a, st);
+    case 3: return launch_tiles<2, 2, 1, 2, ACT>(a, st);
+    default: return launch_tiles<2, 1, 1, 4, ACT>(a, st);
+  }
 }
 
 template <int ACT>
@@ -576,13 +654,13 @@ static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t out_n = a.N / (ACT != UFP4_ACT_NONE ? 2 : 1);
   const int64_t groups16 = (out_n + 15) / 16 * a.n_groups;      // workgroups of the rows kernel
   // Up to 16 rows the rows kernel reads w at the memory's rate.  With more rows it
-  // reads them in every workgroup, which pays while there are few (17 rows, 8192
-  // to 2048 columns: 10 us, 64-row tiles 41; 64 rows, 2048 to 4096 columns: 7 and 12 us;
-  // 48 rows, 2048 to 2 x 8192: 14.4 and 14.4 us; 1000 rows over 32 experts, 2048 to 2 x 2048
-  // columns: 89 and 70 us).
+  // reads them in every workgroup, which pays while there are few (32 rows, 8192 to
+  // 2048 columns: 13 us, tiles 22; 48 rows, 1024 to 2 x 2048: 5.0 and 6.0; 32 rows, 2048
+  // to 2 x 8192: 10.1 and 10.1; 64 rows, 2048 to 2 x 4096: 8.6 and 8.1; 300 rows over 8
+  // experts, 2048 to 2 x 1024: 14.5 and 12.3).
   if (rows <= 16) return launch_rows<1, ACT>(a, st);
-  if (rows <= 32 && groups16 <= 1024) return launch_rows<2, ACT>(a, st);
-  if (rows <= 64 && groups16 <= 512) return launch_rows<4, ACT>(a, st);
+  if (rows <= 32 && groups16 <= 512) return launch_rows<2, ACT>(a, st);
+  if (rows <= 64 && groups16 <= 256) return launch_rows<4, ACT>(a, st);
   return launch_best_tiles<ACT>(a, st);
 }
 
