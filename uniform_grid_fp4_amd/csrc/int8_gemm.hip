@@ -22,18 +22,15 @@ constexpr int kStageK = 128;                     // bytes of K per LDS stage: a 
 
 // One value of the result from its exact sums: the same operations in every
 // kernel, so that which one runs shows in no bit.
+// No bias is one of -0, which changes no sum, and costs less than the choice.
 template <int ACT>
 __device__ __forceinline__ float finish(int gate, int up, float sa, float sg, float su, float bg,
-                                        float bu, bool bias) {
-  float v = (float)gate * sa * sg;
-  if (bias) v += bg;
-  if constexpr (ACT != UFP4_ACT_NONE) {
-    float u = (float)up * sa * su;
-    if (bias) u += bu;
-    v = u * act_value<ACT>(v);
-  }
+                                        float bu) {
+  const float v = (float)gate * sa * sg + bg;
+  if constexpr (ACT != UFP4_ACT_NONE) return ((float)up * sa * su + bu) * act_value<ACT>(v);
   return v;
 }
+constexpr float kNoBias = -0.0f;
 __device__ __forceinline__ void put(const Int8GemmArgs &a, int64_t row, int64_t col, float v) {
   if (a.out_bf16) static_cast<uint16_t *>(a.y)[row * a.ld_y + col] = to_bf16_bits(v);
   else static_cast<float *>(a.y)[row * a.ld_y + col] = v;
@@ -123,8 +120,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_rows_kernel(const Int8Gem
       const int64_t n = (int64_t)e * a.N + col, up = GATED ? n + out_n : n;
       const bool bias = a.bias != nullptr;
       put(a, row0 + m, col,
-          finish<ACT>(sum[0], sum[1], a.sa[row0 + m], a.sw[n], a.sw[up], bias ? a.bias[n] : 0.0f,
-                      bias ? a.bias[up] : 0.0f, bias));
+          finish<ACT>(sum[0], sum[1], a.sa[row0 + m], a.sw[n], a.sw[up],
+                      bias ? a.bias[n] : kNoBias, bias ? a.bias[up] : kNoBias));
     }
     __syncthreads();
   }
@@ -239,8 +236,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_fused_kernel(const Int8Ge
   for (int i = 1; i < parts; ++i) top = max(top, s_top[m][i]);
   const bool bias = a.bias != nullptr;
   put(a, m, n,
-      finish<ACT>(sum[0], sum[1], int8_scale(top).scale, a.sw[n], a.sw[up], bias ? a.bias[n] : 0.0f,
-                  bias ? a.bias[up] : 0.0f, bias));
+      finish<ACT>(sum[0], sum[1], int8_scale(top).scale, a.sw[n], a.sw[up],
+                  bias ? a.bias[n] : kNoBias, bias ? a.bias[up] : kNoBias));
 }
 
 // ---------------------------------------------------------------------------
@@ -393,7 +390,7 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
     const int n = min(GATED ? (r >> 6) * 32 + (r & 31) : r, cols - 1);
     const int64_t at = w_row + n + (GATED && (r >> 5) & 1 ? out_n : 0);
     scale_w[i] = a.sw[at];
-    bias[i] = a.bias != nullptr ? a.bias[at] : 0.0f;
+    bias[i] = a.bias != nullptr ? a.bias[at] : kNoBias;
   }
   if (stages > 0) issue(0);
   if (stages > 1) issue(1);
@@ -513,17 +510,13 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
         const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half, n1 = GATED ? n0 + 32 : n0;
         const floatx4 sg = *reinterpret_cast<const floatx4 *>(s_sw + n0);
         const floatx4 su = *reinterpret_cast<const floatx4 *>(s_sw + n1);
-        floatx4 bg = 0.0f, bu = 0.0f;
-        if (a.bias != nullptr) {
-          bg = *reinterpret_cast<const floatx4 *>(s_bias + n0);
-          bu = *reinterpret_cast<const floatx4 *>(s_bias + n1);
-        }
+        const floatx4 bg = *reinterpret_cast<const floatx4 *>(s_bias + n0);
+        const floatx4 bu = *reinterpret_cast<const floatx4 *>(s_bias + n1);
         float v[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int r = q * 4 + z;
-          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, sg[z], su[z], bg[z], bu[z],
-                             a.bias != nullptr);
+          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, sg[z], su[z], bg[z], bu[z]);
         }
         uint8_t *p = line + l32 * kLine + (j * 32 + 8 * q + 4 * half) * out_bytes;
         if (a.out_bf16) {
