@@ -475,20 +475,23 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
     }
     wait_lds();
     meet();
-    if (part > 0) return;
+    if (part == 0) {
 #pragma unroll
-    for (int from = 0; from < KS - 1; ++from)
+      for (int from = 0; from < KS - 1; ++from)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const i32x4 v = sums[from * PART + ((i * NT + j) * 4 + q) * 64];
+            for (int q = 0; q < 4; ++q) {
+              const i32x4 v = sums[from * PART + ((i * NT + j) * 4 + q) * 64];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) acc[i][j][4 * q + z] += v[z];
-          }
+              for (int z = 0; z < 4; ++z) acc[i][j][4 * q + z] += v[z];
+            }
+    }
     wait_lds();
+    meet();                                       // a wave's lines lie over others' sums
+    if (part > 0) return;
   }
 
   // Epilogue, 32 rows of the wave at a time through its own piece of LDS: a lane
