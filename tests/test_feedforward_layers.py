@@ -115,6 +115,14 @@ def test_layer_arguments():
     assert isinstance(M.UFP4MoEBlock(8, 4, 2, 1).up, Y.UFP4ExpertLinear)
 
 
+def test_a_residual_of_another_shape_is_refused():
+    """As rows they would fit, each meeting another's."""
+    x, r = torch.zeros(2, 3, 8), torch.zeros(3, 2, 8)
+    for call in (W.LayerNorm(8), W.Dropout(0.5), W.Dropout(0.0)):
+        with pytest.raises(ValueError, match="shape"):
+            call(x, r)
+
+
 def test_layer_norm_gradients(plain):
     norm = W.LayerNorm(4, dtype=torch.float32)
     x, r = torch.randn(2, 3, 4, requires_grad=True), torch.randn(2, 3, 4, requires_grad=True)

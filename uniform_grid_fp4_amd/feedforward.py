@@ -24,6 +24,12 @@ from .layers import UFP4Linear, _bf16_rows, _expert_grads, _linear_grads, _recip
 ACTS = {"silu": F.ACT_SILU, "gelu": F.ACT_GELU}
 
 
+def _same_shape(x: torch.Tensor, residual: torch.Tensor) -> None:
+    """As rows, tensors of other shapes could pass for one another."""
+    if residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+
+
 def _act_code(act: str) -> int:
     if act not in ACTS:
         raise ValueError(f"act = {act!r}: one of {sorted(ACTS)}")
@@ -70,6 +76,7 @@ class LayerNorm(torch.nn.Module):
         if residual is None:
             return _LayerNormFn.apply(_rows(x), None, self.weight, self.bias,
                                       self.eps).reshape(x.shape)
+        _same_shape(x, residual)
         y, h = _LayerNormFn.apply(_rows(x), _rows(residual), self.weight, self.bias, self.eps)
         return y.reshape(x.shape), h.reshape(x.shape)
 
@@ -101,6 +108,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
     """`ufp4_dropout` with its gradients: rows [..., hidden] dropped with
     probability p, onto a residual or alone.  (seed, offset) names the mask.  An
     `offset` on the GPU must hold its value until the backward pass has run."""
+    if residual is not None:
+        _same_shape(x, residual)
     y = _DropoutFn.apply(_rows(x), None if residual is None else _rows(residual), p, seed, offset)
     return y.reshape(x.shape)
 
@@ -109,7 +118,9 @@ class Dropout(torch.nn.Module):
     """forward(x, residual=None) = residual + dropout(x); in eval mode nothing is
     dropped.  Every training call draws another mask: the k-th has offset k, or
     what `offset` holds, an int64 tensor of one element on the GPU that the caller
-    advances (between the replays of a captured step, for instance)."""
+    advances (between the replays of a captured step, for instance).  A call that
+    is run again to recompute its activations counts as another: give such calls
+    `dropout` with the same offset both times."""
 
     def __init__(self, p: float, seed: int = 0, offset: Optional[torch.Tensor] = None):
         super().__init__()
@@ -181,7 +192,8 @@ class UFP4GatedLinear(torch.nn.Module):
     """y = act(x Wg^T) * (x Wu^T), weight [2 * ffn, in_features] in bf16 (Wg's rows,
     then Wu's); x is bf16 [..., in_features]; the output and both gradients are
     bf16.  `act` is "silu" or "gelu"; `rht` and `sr_dy` as for UFP4Linear, of the two
-    projections as one product."""
+    projections as one product.  The gradient of the gate and up values takes their
+    place, so a graph is good for one backward pass; a second one raises."""
 
     def __init__(self, in_features: int, ffn: int, act: str = "silu", seed: int = 0,
                  grid: int = U.GRID_UNIFORM, device=None, rht=(True, True, True),
