@@ -19,7 +19,7 @@ import torch
 
 from . import block as B
 from . import ufp4 as U
-from .block import _CODE, _exact, _like, _new, _p, _rows2d, _weight, _workspace, _written
+from .block import _CODE, _exact, _like, _new, _p, _rows2d, _workspace, _written
 
 # Every symbol include/ufp4_ffn.h declares.
 EXPORTS = ("ufp4_layernorm", "ufp4_layernorm_bwd", "ufp4_layernorm_bwd_workspace_size",
@@ -123,7 +123,7 @@ def ufp4_layernorm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     elif out_h is not None:
         raise ValueError("out_h is given without a residual")
     y = _new(x)
-    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
+    mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind(0)
     _call("ufp4_layernorm", dev, x.data_ptr(), ld, pr, ldr, weight.data_ptr(), pb, _CODE[dtype],
           _CODE[wtype], rows, cols, eps, ph, y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     if out_h is not None:
@@ -145,16 +145,20 @@ def ufp4_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, 
     ldh = _rows2d(h, "h")
     ldy = _rows(dy, "dy", h)
     ldd = _rows(dh, "dh", h) if dh is not None else 0
-    wd = _weight(weight, h)
     rows, cols = h.shape
     dev = h.device
+    wtype = weight.dtype
+    if wtype != h.dtype and wtype != torch.float32:
+        raise TypeError(f"weight is {h.dtype} or float32, got {wtype}")
+    wd = _CODE[_vector(weight, "weight", wtype, cols, dev).dtype]
     _vector(mean, "mean", torch.float32, rows, dev)
     _vector(rstd, "rstd", torch.float32, rows, dev)
     dx, dw = _new(h), torch.empty_like(weight)
     db = torch.empty_like(weight) if bias else None
     ws, nbytes = _workspace(workspace, lib().ufp4_layernorm_bwd_workspace_size(rows, cols), dev)
-    _call("ufp4_layernorm_bwd", dev, _p(dy), ldy, _p(h), ldh, _p(weight), _p(mean), _p(rstd),
-          _p(dh), ldd, _CODE[h.dtype], wd, rows, cols, _p(dx), _p(dw), _p(db), _p(ws), nbytes)
+    _call("ufp4_layernorm_bwd", dev, dy.data_ptr(), ldy, h.data_ptr(), ldh, weight.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr(), _p(dh), ldd, _CODE[h.dtype], wd, rows, cols,
+          dx.data_ptr(), dw.data_ptr(), _p(db), ws.data_ptr(), nbytes)
     return dx, dw, db
 
 
@@ -186,9 +190,9 @@ def ufp4_dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.
     there = None
     if isinstance(offset, torch.Tensor):
         _like(offset.reshape(-1), "offset", torch.int64, (1,), dev)
-        there, offset = offset, 0
-    _call("ufp4_dropout", dev, _p(x), ld, _p(residual), ldr, _CODE[x.dtype], rows, cols, p,
-          seed & _WORD, offset & _WORD, _p(there), _p(y))
+        there, offset = offset.data_ptr(), 0
+    _call("ufp4_dropout", dev, x.data_ptr(), ld, None if residual is None else residual.data_ptr(),
+          ldr, _CODE[x.dtype], rows, cols, p, seed & _WORD, offset & _WORD, there, y.data_ptr())
     if out is not None:
         _written(out)
     return y
@@ -250,10 +254,11 @@ def ufp4_gated_gemm(xq: U.Quantized, wq: U.Quantized, act: int = ACT_SILU, keep:
     dw = _operand(wq, "wq", dev)
     groups = _groups(offsets, dev)
     f = _rows_per_group(wq.rows, groups, 2)
-    y = torch.empty((xq.rows, f), dtype=out_dtype, device=dev)
-    gu = torch.empty((xq.rows, 2 * f), dtype=out_dtype, device=dev) if keep else None
+    new = xq.scales.new_empty
+    y = new((xq.rows, f), dtype=out_dtype)
+    gu = new((xq.rows, 2 * f), dtype=out_dtype) if keep else None
     _call("ufp4_gated_gemm", dev, ctypes.byref(dx), ctypes.byref(dw), act, groups, _p(offsets),
-          _CODE[out_dtype], _p(y), f, _p(gu), 2 * f)
+          _CODE[out_dtype], y.data_ptr(), f, None if gu is None else gu.data_ptr(), 2 * f)
     return GatedOut(y, gu)
 
 
@@ -268,8 +273,8 @@ def ufp4_gated_bwd(dy: torch.Tensor, gu: torch.Tensor, act: int = ACT_SILU,
     _like(dy, "dy", gu.dtype, (rows, cols // 2), gu.device)
     ldy = cols // 2 if dy.is_contiguous() else _rows2d(dy, "dy")
     dgu = _new(gu) if out is None else _exact(out, "out", gu.dtype, (rows, cols), gu.device)
-    _call("ufp4_gated_bwd", gu.device, _p(dy), ldy, _p(gu), ldg, act, _CODE[gu.dtype], rows,
-          cols // 2, _p(dgu))
+    _call("ufp4_gated_bwd", gu.device, dy.data_ptr(), ldy, gu.data_ptr(), ldg, act,
+          _CODE[gu.dtype], rows, cols // 2, dgu.data_ptr())
     if out is not None:
         _written(out)
     return dgu
@@ -326,7 +331,7 @@ def _int8_out(rows: int, w: Int8Rows, bias, act: int, offsets, out_dtype, device
     cols = _rows_per_group(n, groups, 1 if act == ACT_NONE else 2)
     if bias is not None:
         _vector(bias, "bias", torch.float32, n, device)
-    return words, groups, torch.empty((rows, cols), dtype=out_dtype, device=device)
+    return words, groups, w.scale.new_empty((rows, cols), dtype=out_dtype)
 
 
 def ufp4_int8_gemm(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
@@ -364,7 +369,11 @@ def ufp4_int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] 
     out_dtype = x.dtype if out_dtype is None else out_dtype
     dw, groups, y = _int8_out(rows, w, bias, act, offsets, out_dtype, dev)
     need = lib().ufp4_int8_linear_workspace_size(rows, cols, offsets is not None)
-    ws, nbytes = (None, 0) if need == 0 else _workspace(workspace, need, dev)
-    _call("ufp4_int8_linear", dev, _p(x), ld, _CODE[x.dtype], rows, cols, dw.buffer_info()[0],
-          _p(bias), act, groups, _p(offsets), _CODE[out_dtype], _p(y), y.shape[1], _p(ws), nbytes)
+    ws = None
+    if need:
+        ws, need = _workspace(workspace, need, dev)
+        ws = ws.data_ptr()
+    _call("ufp4_int8_linear", dev, x.data_ptr(), ld, _CODE[x.dtype], rows, cols,
+          dw.buffer_info()[0], _p(bias), act, groups, _p(offsets), _CODE[out_dtype], y.data_ptr(),
+          y.shape[1], ws, need)
     return y
