@@ -155,7 +155,7 @@ MANY = [("norm_bwd", dict(t=300, c=2048, dt=BF16)), ("norm_bwd", dict(t=300, c=4
         ("norm_bwd", dict(t=0, c=64, dt=F32)), ("dropout", dict(t=1 << 22, c=8192, dt=BF16)),
         ("linear", dict(t=40, c=64, k=64, e=1, dt=BF16, act=0)),
         ("linear", dict(t=4000, c=640, k=64, e=1, dt=BF16, act=1)),
-        ("gemm", dict(t=1 << 32, c=512, k=64, e=1, dt=BF16, act=0))]
+        ("gemm", dict(t=1 << 32, c=64, k=64, e=1, dt=BF16, act=0))]
 
 
 @pytest.mark.parametrize("op,sizes", MANY)

@@ -17,7 +17,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kXcd = 8;
+constexpr int kXcd = 8, kCus = 256;
 constexpr int kStageK = 128;                     // bytes of K per LDS stage: a row's piece is a line
 
 // One value of the result from its exact sums: the same operations in every
@@ -261,13 +261,17 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_fused_kernel(const Int8Ge
 //
 // w is the matrix instruction's first operand and x its second, so a lane ends
 // with four neighbouring columns of one row: the epilogue packs them, passes them
-// through LDS and writes 16 bytes a lane.  8192 x 2048 to 2 x 8192 columns, silu,
-// bf16: 273 us (2.01 POP/s), 235 without the epilogue; with the fragments read in
-// their own step 300-320 us, with stages of 64 bytes 290-297 us, with 128 x 128 tiles 298 us,
-// with 128 x 128 per wave (4 waves) 300-315 us.  A library product of the same
-// size takes 287 us with its int32 output.  What bounds it: reads of LDS (24 KB
-// per 8.4 MOP of a wave) and the products take about the same time, and under
-// them the clock falls to 1.9 GHz (zeros in place of the data: 225 us).
+// through LDS and writes 16 bytes a lane.  The largest tiles have a CU to
+// themselves, with nothing beside them to hide their start: their workgroups go
+// on to other tiles, whose first two stages are under way during the epilogue.
+// 8192 x 2048 to 2 x 8192 columns, silu, bf16: 280 us (1.96 POP/s; a workgroup per tile
+// 296; a library product of the same size 287 with its int32 output); 8192 x 8192 to
+// 8192: 474 us (2.32 POP/s; 500).  Earlier steps of the first: fragments read in their
+// own step 300-320 us instead of 273 on that day's card, stages of 64 bytes 290-297,
+// 128 x 128 tiles 298, 128 x 128 per wave (4 waves) 300-315.  What bounds it: reads of LDS
+// (24 KB per 8.4 MOP of a wave) and the products take about the same time, under
+// them the clock falls to 1.9 GHz (zeros in place of the data: 225 us), and the
+// epilogue's vector work, 4 to 5 us a tile, runs beside neither.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int swizzle(int row) {
   return ((row >> 1) & 3) | ((((row >> 3) ^ (row >> 4)) & 1) << 2);
@@ -275,6 +279,17 @@ __device__ __forceinline__ int swizzle(int row) {
 // Waits for all of this wave's loads into LDS, and for its LDS accesses.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Writes to LDS that do not wait for the loads into it (elsewhere), as the compiler's
+// own would; wait_lds() before they are read.
+__device__ __forceinline__ uint32_t lds_address(uint8_t *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)p;
+}
+__device__ __forceinline__ void write_lds(uint8_t *p, uint2 v) {
+  asm volatile("ds_write_b64 %0, %1" ::"v"(lds_address(p)), "v"(v) : "memory");
+}
+__device__ __forceinline__ void write_lds(uint8_t *p, floatx4 v) {
+  asm volatile("ds_write_b128 %0, %1" ::"v"(lds_address(p)), "v"(v) : "memory");
+}
 // Between the waves of a workgroup; memory accesses stay on their side.
 __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
@@ -297,13 +312,30 @@ __device__ __forceinline__ void store_cols(T *p, int n, u32x4 v) {
 }
 
 constexpr int kBandRows = 8;       // tile rows that neighbouring workgroups share w's panels over
+constexpr int kLine = 64 + 16;     // bytes of a row's piece in the epilogue; 16 more spread the banks
 template <int WM, int WN, int MT, int KS>
 struct TileShape {
   static constexpr int kThreads = 64 * WM * WN * KS, kBM = 32 * MT * WM, kBN = 64 * WN;
   static constexpr int kStage = (kBM + kBN) * kStageK;
-  // the stages; the rows' scales; the columns' scales and biases
-  static constexpr size_t kLds = KS * 2 * kStage + (kBM + 2 * kBN) * sizeof(float);
+  // the workgroup goes on to other tiles: it has the CU to itself
+  static constexpr bool kStays = 2 * kStage > 80 * 1024 && KS == 1;
+  static constexpr int kLines = WM * WN * 32 * kLine;
+  // the stages; the rows' scales; the columns' scales and biases; the epilogue's lines,
+  // where the next tile's stages come in under it
+  static constexpr size_t kLds =
+      KS * 2 * kStage + (kBM + 2 * kBN) * sizeof(float) + (kStays ? kLines : 0);
 };
+
+// A wave-uniform number in scalar registers.
+__device__ __forceinline__ int64_t wave_uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+// a / b; both are small where it counts.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 template <int WM, int WN, int MT, int KS, int ACT>
 __global__ __attribute__((amdgpu_flat_work_group_size(64 * WM * WN * KS, 64 * WM * WN * KS),
@@ -318,26 +350,8 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   float *s_sa = reinterpret_cast<float *>(lds + KS * 2 * S::kStage);
   float *s_sw = s_sa + BM, *s_bias = s_sw + BN;
+  uint8_t *lines = S::kStays ? reinterpret_cast<uint8_t *>(s_bias + BN) : lds;
   const int64_t out_n = a.N / (GATED ? 2 : 1);
-
-  // The workgroups of an XCD (every eighth) walk a contiguous eighth of the tiles, in
-  // bands of kBandRows tile rows, column by column: their panels meet in one L2.  Of
-  // the tiles that there are: eighths of the grid, which is cut for the most tiles that
-  // the groups can have, would leave the last XCDs idle.
-  const GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, [=](int64_t tiles) {
-    const int64_t id = first + blockIdx.x, per = (tiles + kXcd - 1) / kXcd;
-    return id / kXcd < per ? id % kXcd * per + id / kXcd : tiles;
-  });
-  if (g.e < 0) return;
-  const int64_t band = g.local / (kBandRows * tiles_n);
-  const int64_t in_band = g.local - band * kBandRows * tiles_n;
-  const int64_t deep = min((int64_t)kBandRows, g.tiles_m - band * kBandRows);
-  const int64_t tn = in_band / deep, tm = band * kBandRows + in_band - tn * deep;
-  const int64_t row0 = g.row0 + tm * BM;
-  const int rows = (int)min((int64_t)BM, g.rows - tm * BM);
-  const int64_t col0 = tn * OUT;
-  const int cols = (int)min((int64_t)OUT, out_n - col0);
-  const int64_t w_row = (int64_t)g.e * a.N + col0;
 
   const int lane = threadIdx.x & 63;
   const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -345,24 +359,71 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
   const int wm = wave % WM, wn = wave / WM;
   const int l32 = lane & 31, half = lane >> 5;
   const int kpad = (int)a.kpad;
-
-  // A load takes eight rows; rows past the tile's repeat its last one (their
-  // products are not stored).  Offsets stay below 256 rows of 2^17 bytes.
-  const int8_t *base_a = a.a + row0 * a.kpad, *base_w = a.w + w_row * a.kpad;
-  const int8_t *base_u = base_w + (GATED ? out_n * a.kpad : 0);
-  int va[AL], vw[BL];
-#pragma unroll
-  for (int i = 0; i < AL; ++i) {
-    const int r = (i * WAVES + wave) * 8 + (lane >> 3);
-    va[i] = min(r, rows - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < BL; ++i) {
-    const int r = (i * WAVES + wave) * 8 + (lane >> 3);
-    const int n = GATED ? (r >> 6) * 32 + (r & 31) : r;
-    vw[i] = min(n, cols - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
-  }
+  const int total = kpad / kStageK;
+  const int stages = (total - part + KS - 1) / KS, turns = (total + KS - 1) / KS;
   uint8_t *const mine = lds + part * 2 * S::kStage;
+
+  // A tile: its place, its loads and its scales.  The scales wait in registers for
+  // the epilogue: a write to LDS would wait for all loads into it.
+  int64_t row0 = 0, col0 = 0;
+  int rows = 0, cols = 0;
+  const int8_t *base_a = nullptr, *base_w = nullptr, *base_u = nullptr;
+  int va[AL], vw[BL];
+  float scale_a[(BM + S::kThreads - 1) / S::kThreads];
+  float scale_w[(BN + S::kThreads - 1) / S::kThreads], bias[(BN + S::kThreads - 1) / S::kThreads];
+  // The workgroups of an XCD (every eighth) walk a contiguous eighth of the tiles, in
+  // bands of kBandRows tile rows, column by column: their panels meet in one L2.  Of
+  // the tiles that there are: eighths of the grid, which is cut for the most tiles that
+  // the groups can have, would leave the last XCDs idle.
+  auto place = [&](int64_t at) __attribute__((always_inline)) -> bool {
+    GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, [=](int64_t tiles) {
+      const int64_t per = (tiles + kXcd - 1) / kXcd;
+      return at / kXcd < per ? at % kXcd * per + at / kXcd : tiles;
+    });
+    g.e = __builtin_amdgcn_readfirstlane(g.e);    // into scalar registers
+    if (g.e < 0) return false;
+    g.row0 = wave_uniform(g.row0);
+    g.rows = wave_uniform(g.rows);
+    g.local = wave_uniform(g.local);
+    g.tiles_m = wave_uniform(g.tiles_m);
+    const int64_t band = quotient(g.local, kBandRows * tiles_n);
+    const int64_t in_band = g.local - band * kBandRows * tiles_n;
+    const int64_t deep = min((int64_t)kBandRows, g.tiles_m - band * kBandRows);
+    const int64_t tn = quotient(in_band, deep), tm = band * kBandRows + in_band - tn * deep;
+    row0 = g.row0 + tm * BM;
+    rows = (int)min((int64_t)BM, g.rows - tm * BM);
+    col0 = tn * OUT;
+    cols = (int)min((int64_t)OUT, out_n - col0);
+    const int64_t w_row = (int64_t)g.e * a.N + col0;
+    // A load takes eight rows; rows past the tile's repeat its last one (their
+    // products are not stored).  Offsets stay below 256 rows of 2^17 bytes.
+    base_a = a.a + row0 * a.kpad;
+    base_w = a.w + w_row * a.kpad;
+    base_u = base_w + (GATED ? out_n * a.kpad : 0);
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int r = (i * WAVES + wave) * 8 + (lane >> 3);
+      va[i] = min(r, rows - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int r = (i * WAVES + wave) * 8 + (lane >> 3);
+      const int n = GATED ? (r >> 6) * 32 + (r & 31) : r;
+      vw[i] = min(n, cols - 1) * kpad + ((lane & 7) ^ swizzle(r)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i * S::kThreads < BM; ++i)
+      scale_a[i] = a.sa[row0 + min((int)threadIdx.x + i * S::kThreads, rows - 1)];
+#pragma unroll
+    for (int i = 0; i * S::kThreads < BN; ++i) {
+      const int r = min((int)threadIdx.x + i * S::kThreads, BN - 1);
+      const int n = min(GATED ? (r >> 6) * 32 + (r & 31) : r, cols - 1);
+      const int64_t w = w_row + n + (GATED && (r >> 5) & 1 ? out_n : 0);
+      scale_w[i] = a.sw[w];
+      bias[i] = a.bias != nullptr ? a.bias[w] : kNoBias;
+    }
+    return true;
+  };
   auto issue = [&](int stage) __attribute__((always_inline)) {
     uint8_t *st = mine + (stage & 1) * S::kStage + wave * 1024;
     const int k0 = (stage * KS + part) * kStageK;
@@ -375,176 +436,186 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
       load_lds(up ? base_u : base_w, vw[i], k0, st + BM * kStageK + i * WAVES * 1024);
     }
   };
-  const int total = kpad / kStageK;
-  const int stages = (total - part + KS - 1) / KS, turns = (total + KS - 1) / KS;
-  // The scales wait in registers for the epilogue: a write to LDS would wait for all
-  // loads into it.
-  float scale_a[(BM + S::kThreads - 1) / S::kThreads];
-  float scale_w[(BN + S::kThreads - 1) / S::kThreads], bias[(BN + S::kThreads - 1) / S::kThreads];
-#pragma unroll
-  for (int i = 0; i * S::kThreads < BM; ++i)
-    scale_a[i] = a.sa[row0 + min((int)threadIdx.x + i * S::kThreads, rows - 1)];
-#pragma unroll
-  for (int i = 0; i * S::kThreads < BN; ++i) {
-    const int r = min((int)threadIdx.x + i * S::kThreads, BN - 1);
-    const int n = min(GATED ? (r >> 6) * 32 + (r & 31) : r, cols - 1);
-    const int64_t at = w_row + n + (GATED && (r >> 5) & 1 ? out_n : 0);
-    scale_w[i] = a.sw[at];
-    bias[i] = a.bias != nullptr ? a.bias[at] : kNoBias;
-  }
+
+  int64_t at = first + blockIdx.x;
+  if (!place(at)) return;
   if (stages > 0) issue(0);
   if (stages > 1) issue(1);
-
-  i32x16 acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-  constexpr int KK = kStageK / 32;
-  i32x4 fa[2][MT], fw[2][NT];
-  const uint8_t *pa = mine + (wm * MT * 32 + l32) * kStageK;
-  const uint8_t *pw = mine + (BM + wn * NT * 32 + l32) * kStageK;
-  const int sw32 = swizzle(l32);
-  auto read = [&](int into, int stage, int kk) __attribute__((always_inline)) {
-    const int at = (stage & 1) * S::kStage + ((2 * kk + half) ^ sw32) * 16;
+  for (;;) {
+    i32x16 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      fa[into][i] = *reinterpret_cast<const i32x4 *>(pa + at + i * 32 * kStageK);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      fw[into][j] = *reinterpret_cast<const i32x4 *>(pw + at + j * 32 * kStageK);
-  };
-  wait_loads();
-  wait_lds();
-  meet();
-  read(0, 0, 0);
-  for (int s = 0; s < turns; ++s) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      if (kk + 1 < KK) {
-        read((kk + 1) & 1, s, kk + 1);
-      } else if (s + 1 < turns) {
-        wait_loads();                             // of stage s + 1
-        wait_lds();                               // this wave's last fragments of stage s
-        meet();
-        read((kk + 1) & 1, s + 1, 0);
-        if (s + 2 < stages) issue(s + 2);
-      }
-      // the reads and loads above go out before the products below
-      __builtin_amdgcn_sched_barrier(0);
-      if (KS == 1 || s < stages) {                // a part may have one stage less
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][j], fa[kk & 1][i],
-                                                              acc[i][j], 0, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i * S::kThreads < BM; ++i)
-    if (const int r = threadIdx.x + i * S::kThreads; r < BM) s_sa[r] = scale_a[i];
-#pragma unroll
-  for (int i = 0; i * S::kThreads < BN; ++i)
-    if (const int r = threadIdx.x + i * S::kThreads; r < BN) {
-      s_sw[r] = scale_w[i];
-      s_bias[r] = bias[i];
-    }
-  wait_lds();
-  meet();                                         // the stages' LDS is free
-  if (KS > 1) {
-    // the parts' sums meet in the first one's waves
-    i32x4 *sums = reinterpret_cast<i32x4 *>(lds) + wave * (MT * NT * 4 * 64) + lane;
-    constexpr int PART = WAVES * MT * NT * 4 * 64;
-    static_assert((KS - 1) * PART * 16 <= KS * 2 * S::kStage, "sums in LDS");
-    if (part > 0) {
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    constexpr int KK = kStageK / 32;
+    i32x4 fa[2][MT], fw[2][NT];
+    const uint8_t *pa = mine + (wm * MT * 32 + l32) * kStageK;
+    const uint8_t *pw = mine + (BM + wn * NT * 32 + l32) * kStageK;
+    const int sw32 = swizzle(l32);
+    auto read = [&](int into, int stage, int kk) __attribute__((always_inline)) {
+      const int from = (stage & 1) * S::kStage + ((2 * kk + half) ^ sw32) * 16;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
+        fa[into][i] = *reinterpret_cast<const i32x4 *>(pa + from + i * 32 * kStageK);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const i32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                             acc[i][j][4 * q + 3]};
-            sums[(part - 1) * PART + ((i * NT + j) * 4 + q) * 64] = v;
-          }
-    }
+      for (int j = 0; j < NT; ++j)
+        fw[into][j] = *reinterpret_cast<const i32x4 *>(pw + from + j * 32 * kStageK);
+    };
+    wait_loads();
     wait_lds();
     meet();
-    if (part == 0) {
+    read(0, 0, 0);
+    for (int s = 0; s < turns; ++s) {
 #pragma unroll
-      for (int from = 0; from < KS - 1; ++from)
+      for (int kk = 0; kk < KK; ++kk) {
+        if (kk + 1 < KK) {
+          read((kk + 1) & 1, s, kk + 1);
+        } else if (s + 1 < turns) {
+          wait_loads();                           // of stage s + 1
+          wait_lds();                             // this wave's last fragments of stage s
+          meet();
+          read((kk + 1) & 1, s + 1, 0);
+          if (s + 2 < stages) issue(s + 2);
+        }
+        // the reads and loads above go out before the products below
+        __builtin_amdgcn_sched_barrier(0);
+        if (KS == 1 || s < stages) {              // a part may have one stage less
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[kk & 1][j], fa[kk & 1][i],
+                                                                acc[i][j], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i * S::kThreads < BM; ++i)
+      if (const int r = threadIdx.x + i * S::kThreads; r < BM) s_sa[r] = scale_a[i];
+#pragma unroll
+    for (int i = 0; i * S::kThreads < BN; ++i)
+      if (const int r = threadIdx.x + i * S::kThreads; r < BN) {
+        s_sw[r] = scale_w[i];
+        s_bias[r] = bias[i];
+      }
+    wait_lds();
+    meet();                                       // the scales are there, the stages' LDS is free
+    const int64_t e_row0 = row0, e_col0 = col0;
+    const int e_rows = rows, e_cols = cols;
+    bool more = false;
+    if (S::kStays) {
+      at += gridDim.x;
+      more = place(at);
+      if (more) {
+        issue(0);
+        if (stages > 1) issue(1);
+      }
+    }
+    if (KS > 1) {
+      // the parts' sums meet in the first one's waves
+      i32x4 *sums = reinterpret_cast<i32x4 *>(lds) + wave * (MT * NT * 4 * 64) + lane;
+      constexpr int PART = WAVES * MT * NT * 4 * 64;
+      static_assert((KS - 1) * PART * 16 <= KS * 2 * S::kStage, "sums in LDS");
+      if (part > 0) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const i32x4 v = sums[from * PART + ((i * NT + j) * 4 + q) * 64];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) acc[i][j][4 * q + z] += v[z];
+              const i32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                               acc[i][j][4 * q + 3]};
+              sums[(part - 1) * PART + ((i * NT + j) * 4 + q) * 64] = v;
             }
+      }
+      wait_lds();
+      meet();
+      if (part == 0) {
+#pragma unroll
+        for (int from = 0; from < KS - 1; ++from)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const i32x4 v = sums[from * PART + ((i * NT + j) * 4 + q) * 64];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) acc[i][j][4 * q + z] += v[z];
+              }
+      }
+      wait_lds();
+      meet();                                     // a wave's lines lie over others' sums
+      if (part > 0) return;
     }
-    wait_lds();
-    meet();                                       // a wave's lines lie over others' sums
-    if (part > 0) return;
-  }
 
-  // Epilogue, 32 rows of the wave at a time through its own piece of LDS: a lane
-  // has columns 8 q + 4 half + 0..3 of row l32.
-  constexpr int W = GATED ? 32 : 64;              // output columns of the wave
-  constexpr int kLine = W * 4 + 16;               // bytes; 16 more to spread the banks
-  static_assert(WAVES * 32 * kLine <= KS * 2 * S::kStage, "epilogue LDS");
-  uint8_t *line = lds + wave * 32 * kLine;
-  const int out_bytes = a.out_bf16 ? 2 : 4;
-  const int wcol = wn * W, left = cols - wcol;    // columns of the wave that exist
+    // Epilogue, 64 bytes of 32 rows of the wave at a time through its own piece of
+    // LDS: a lane has columns 8 q + 4 half + 0..3 of row l32.
+    static_assert(S::kStays || S::kLines <= KS * 2 * S::kStage, "epilogue LDS");
+    uint8_t *line = lines + wave * 32 * kLine;
+    constexpr int W = GATED ? 32 : 64;            // output columns of the wave
+    const int wcol = wn * W, left = e_cols - wcol;   // columns of the wave that exist
+    auto value = [&](int i, int j, int q, float sa, float (&v)[4]) __attribute__((always_inline)) {
+      const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half, n1 = GATED ? n0 + 32 : n0;
+      const floatx4 sg = *reinterpret_cast<const floatx4 *>(s_sw + n0);
+      const floatx4 su = *reinterpret_cast<const floatx4 *>(s_sw + n1);
+      const floatx4 bg = *reinterpret_cast<const floatx4 *>(s_bias + n0);
+      const floatx4 bu = *reinterpret_cast<const floatx4 *>(s_bias + n1);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m0 = (wm * MT + i) * 32;
-    const float sa = s_sa[m0 + l32];
+      for (int z = 0; z < 4; ++z) {
+        const int r = q * 4 + z;
+        v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, sg[z], su[z], bg[z], bu[z]);
+      }
+    };
+    // the 32 rows' pieces of columns c.. from LDS, 16 bytes a lane: four lanes a row
+    auto flush = [&](int m0, int c, auto *y) __attribute__((always_inline)) {
+      constexpr int V = 16 / (int)sizeof(*y);
+      wait_lds();                                 // the wave's own lines; its lanes run together
 #pragma unroll
-    for (int j = 0; j < W / 32; ++j)
+      for (int x = 0; x < 2; ++x) {
+        const int r = x * 16 + (lane >> 2), p = lane & 3, m = m0 + r;
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(line + r * kLine + p * 16);
+        if (m < e_rows)
+          store_cols(y + (e_row0 + m) * a.ld_y + e_col0 + wcol + c + p * V, left - c - p * V, v);
+      }
+      wait_lds();
+    };
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n0 = wn * 64 + j * 32 + 8 * q + 4 * half, n1 = GATED ? n0 + 32 : n0;
-        const floatx4 sg = *reinterpret_cast<const floatx4 *>(s_sw + n0);
-        const floatx4 su = *reinterpret_cast<const floatx4 *>(s_sw + n1);
-        const floatx4 bg = *reinterpret_cast<const floatx4 *>(s_bias + n0);
-        const floatx4 bu = *reinterpret_cast<const floatx4 *>(s_bias + n1);
-        float v[4];
+    for (int i = 0; i < MT; ++i) {
+      const int m0 = (wm * MT + i) * 32;
+      const float sa = s_sa[m0 + l32];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int r = q * 4 + z;
-          v[z] = finish<ACT>(acc[i][j][r], acc[i][1][r], sa, sg[z], su[z], bg[z], bu[z]);
-        }
-        uint8_t *p = line + l32 * kLine + (j * 32 + 8 * q + 4 * half) * out_bytes;
+      for (int j = 0; j < W / 32; ++j) {
         if (a.out_bf16) {
-          uint2 w;
-          w.x = (uint32_t)to_bf16_bits(v[0]) | (uint32_t)to_bf16_bits(v[1]) << 16;
-          w.y = (uint32_t)to_bf16_bits(v[2]) | (uint32_t)to_bf16_bits(v[3]) << 16;
-          *reinterpret_cast<uint2 *>(p) = w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v[4];
+            value(i, j, q, sa, v);
+            uint2 w;
+            w.x = (uint32_t)to_bf16_bits(v[0]) | (uint32_t)to_bf16_bits(v[1]) << 16;
+            w.y = (uint32_t)to_bf16_bits(v[2]) | (uint32_t)to_bf16_bits(v[3]) << 16;
+            write_lds(line + l32 * kLine + (8 * q + 4 * half) * 2, w);
+          }
+          flush(m0, j * 32, static_cast<uint16_t *>(a.y));
         } else {
-          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float v[4];
+              value(i, j, 2 * h + q, sa, v);
+              write_lds(line + l32 * kLine + (8 * q + 4 * half) * 4,
+                        floatx4{v[0], v[1], v[2], v[3]});
+            }
+            flush(m0, j * 32 + h * 16, static_cast<float *>(a.y));
+          }
         }
       }
-    wait_lds();                                   // the wave's own lines; its lanes run together
-    const int pieces = W * out_bytes / 16;        // 16-byte pieces of a row: 4, 8 or 16
-    for (int x = lane; x < 32 * pieces; x += 64) {
-      const int r = x / pieces, c = x % pieces, m = m0 + r;
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(line + r * kLine + c * 16);
-      if (m >= rows) continue;
-      if (a.out_bf16)
-        store_cols(static_cast<uint16_t *>(a.y) + (row0 + m) * a.ld_y + col0 + wcol + c * 8,
-                   left - c * 8, v);
-      else
-        store_cols(static_cast<float *>(a.y) + (row0 + m) * a.ld_y + col0 + wcol + c * 4,
-                   left - c * 4, v);
     }
-    wait_lds();
+    if (!more) return;
   }
 }
 
@@ -586,11 +657,12 @@ static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
   auto *kernel = int8_tile_kernel<WM, WN, MT, KS, ACT>;
   hipError_t e = allow_lds<WM, WN, MT, KS, ACT>((const void *)kernel, S::kLds);
   if (e != hipSuccess) return e;
+  const int64_t most = S::kStays ? kCus : kMost;
   for (int64_t first = 0; first < total; first += kMost) {
-    const unsigned n = (unsigned)(total - first < kMost ? total - first : kMost);
+    const unsigned n = (unsigned)(total - first < most ? total - first : most);
     hipLaunchKernelGGL(kernel, dim3(n), dim3(S::kThreads), S::kLds, st, a, tiles_n, first);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || S::kStays) return e;
   }
   return hipSuccess;
 }
@@ -601,35 +673,36 @@ static hipError_t launch_tiles(const Int8GemmArgs &a, hipStream_t st) {
 // set.  A workgroup's start and end cost as much as the added stages of K.  Measured,
 // us:
 //                                  256x256 128x128 64x128 64x128/2 64x64/4
-//   8192 x 2048 to 2 x 8192, gated     300     350    488      572     815
+//   8192 x 2048 to 2 x 8192, gated     290     324    466      571     826
 //   10000 x 2048 to 2 x 1408, gated,
-//     32 groups                        124     124    151      185     247
+//     32 groups                        115     116    137      187     258
 //   24000 x 64 to 2 x 3648, gated,
-//     32 groups                        140     142    197      395     805
-//   3808 x 6065 to 2172, 8 groups       96     108    131      140     164
-//   24000 x 512 to 2048                 53      56     71
-//   2000 x 4096 to 4096                 56      43     53
-//   1000 x 4096 to 4096                 58      32     29       35      46
-//   905 x 2560 to 2 x 768, gated        40      20     16       13      17
-//   500 x 2048 to 2048                  32      17     13       10     8.3
-//   200 x 4096 to 4096                  54      28     23       17      13
-//   1000 x 6080 to 128                  78      38     27       20      15
+//     32 groups                        120     130    186      373     775
+//   3808 x 6065 to 2172, 8 groups       82      98    118      142     168
+//   4000 x 4096 to 4096                 68      83     94      131     169
+//   2000 x 4096 to 4096                 55      41     48       65      86
+//   1500 x 4096 to 4096                 54      39     45       50      66
+//   1000 x 4096 to 4096                 49      27     25       34      43
+//   905 x 2560 to 2 x 768, gated        34      17     15       13      17
+//   500 x 2048 to 2048                  28      13     10        9       8
+//   200 x 4096 to 4096                  47      24     20       16      13
+//   1000 x 6080 to 128                  65      28     20       18      14
 template <int ACT>
 static hipError_t launch_best_tiles(const Int8GemmArgs &a, hipStream_t st) {
   const int64_t per = (a.M + a.n_groups - 1) / a.n_groups;      // rows of an even group
   const double stages = (double)(a.kpad / kStageK);
   auto per_cu = [&](int64_t bm, int64_t bn) {
-    return (double)((per + bm - 1) / bm * ((a.N + bn - 1) / bn) * a.n_groups) / 256.0;
+    return (double)((per + bm - 1) / bm * ((a.N + bn - 1) / bn) * a.n_groups) / kCus;
   };
   const double middle = per_cu(128, 128), small = per_cu(64, 128);
   const double pairs = std::floor(middle / 2.0), left = middle - 2.0 * pairs;
   const double whole = std::floor(small);
   const double t[5] = {
-      std::ceil(per_cu(256, 256)) * 1.96 * (stages + 5.0),
-      (pairs * 1.3 + (left <= 0.0 ? 0.0 : left <= 1.0 ? 0.95 : 1.2)) * (stages + 3.5),
-      (small <= 1.0   ? 0.65
-       : small <= 2.0 ? 0.83
-                      : whole * 0.41 + (small > whole ? 0.9 : 0.0)) * (stages + 3.5),
+      std::ceil(per_cu(256, 256)) * 1.74 * (stages + 4.5) + 4.0,
+      (pairs * 1.15 + (left <= 0.0 ? 0.0 : left <= 1.0 ? 0.95 : 1.1)) * (stages + 3.5),
+      (small <= 1.0   ? 0.63
+       : small <= 2.0 ? 0.81
+                      : whole * 0.4 + (small > whole ? 0.85 : 0.0)) * (stages + 3.5),
       std::ceil(small) * 0.42 * (stages + 9.0),
       std::ceil(per_cu(64, 64)) * 0.29 * (stages + 12.5)};
   int best = 0;
