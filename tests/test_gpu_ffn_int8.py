@@ -141,6 +141,31 @@ def test_large_tiles(m, n):
     assert torch.equal(F.ufp4_int8_gemm(few, w, act=F.ACT_SILU, out_dtype=torch.float32), g[pick])
 
 
+@pytest.mark.parametrize("counts", [[8100], [3000, 0, 1, 5000, 700]])
+def test_large_tiles_of_several_rounds(counts):
+    """Workgroups that go on to other tiles: every row against the same rows in calls
+    of their own, which take other tiles, and some against the oracle."""
+    m, e, n, k = sum(counts), len(counts), 8192, 1411
+    off = [0, *torch.tensor(counts).cumsum(0).tolist()]
+    a, w = operands(m, e * n, k, seed=7)
+    offsets = torch.tensor(off, device=DEV) if e > 1 else None
+    for act, dtype in ((F.ACT_NONE, torch.float32), (F.ACT_NONE, torch.bfloat16),
+                       (F.ACT_SILU, torch.float32), (F.ACT_GELU, torch.bfloat16)):
+        y = F.ufp4_int8_gemm(a, w, act=act, offsets=offsets, out_dtype=dtype)
+        for g in range(e):
+            mine = F.Int8Rows(w.q[g * n:(g + 1) * n], w.scale[g * n:(g + 1) * n], k)
+            for r in range(off[g], off[g + 1], 400):
+                to = min(r + 400, off[g + 1])
+                few = F.ufp4_int8_gemm(F.Int8Rows(a.q[r:to], a.scale[r:to], k), mine, act=act,
+                                       out_dtype=dtype)
+                assert torch.equal(y[r:to], few), (act, dtype, g, r)
+        if act == F.ACT_NONE and dtype == torch.float32:
+            at = off[1] - 1
+            p = plain(F.Int8Rows(a.q[at:at + 1], a.scale[at:at + 1], k),
+                      F.Int8Rows(w.q[:n], w.scale[:n], k))
+            assert np.array_equal(values(y[at:at + 1]), p)
+
+
 @pytest.mark.parametrize("m,n,k", [(65, 66, 513), (129, 300, 900), (1000, 70, 6080), (70, 34, 131),
                                    (905, 1536, 1411), (460, 2050, 1300)])
 def test_few_tiles_of_a_long_contraction(m, n, k):
