@@ -13,8 +13,10 @@
 // along K, for 4 to 8 times the reads of the L2.  Bound by the cache lines that its
 // loads touch (192 per wave and run, every row another line): reading each row's
 // run once per wave and exchanging words between the halves of the wave, instead of
-// in both halves, took 512 x 2048 columns, K = 2048, from 42 to 34 us; loading a run
-// ahead gained nothing.
+// in both halves, took 512 x 2048 columns, K = 2048, from 42 to 35 us.  Two workgroups
+// fit a CU, with at most 128 registers: 29 us; 8 rows over 32 experts of 5120 columns, K
+// = 64, 27 -> 16; 1266 x 1143, K = 384, 21 -> 14.5; 14 rows over 8 experts of 2355 columns, K
+// = 5793, 53 us either way (164 MB, 3.1 TB/s).  Loading a run ahead would spill.
 #include "act_device.h"
 #include "block_device.h"
 #include "group_device.h"
@@ -61,8 +63,7 @@ __device__ __forceinline__ void block_product(uint32_t x, uint32_t g, uint32_t u
 // and of the second's.
 struct FourBlocks {
   uint32_t w[4];
-  __device__ __forceinline__ void load(const uint8_t *p) {
-    const u32x4_dword v = *reinterpret_cast<const u32x4_dword *>(p);
+  __device__ __forceinline__ explicit FourBlocks(u32x4_dword v) {
     const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[1], false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(v[2], v[3], false, false);
     w[0] = a[0];
@@ -73,8 +74,8 @@ struct FourBlocks {
 };
 
 template <int GRID>
-__global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const GemmArgs a,
-                                                                       int64_t tiles_n) {
+__global__ __launch_bounds__(64 * kSmallWaves) __attribute__((amdgpu_waves_per_eu(4, 4))) void
+gated_small_kernel(const GemmArgs a, int64_t tiles_n) {
   __shared__ float s_acc[kSmallWaves][2][kSmallRows * kSmallCols];
   const GroupTile t = group_tile(a.goff, a.n_groups, a.M, kSmallRows, tiles_n,
                                  [](int64_t) { return (int64_t)blockIdx.x; });
@@ -84,15 +85,19 @@ __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const Gem
   const int64_t row0 = t.row0 + tm * kSmallRows, col0 = tn * kSmallCols;
   const int rows = (int)min((int64_t)kSmallRows, t.rows - tm * kSmallRows);
   const int cols = (int)min((int64_t)kSmallCols, a.N - col0);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const int nkb = (int)(a.kpad / 16);
-  // rows and columns past the end repeat the last one; they are not stored
-  const int64_t x_row = row0 + min(l32, rows - 1);
-  const int64_t w_row = (int64_t)t.e * 2 * a.N + col0 + min(l32, cols - 1);
-  const uint8_t *qx = a.a_codes + x_row * (a.kpad / 2), *qg = a.b_codes + w_row * (a.kpad / 2);
-  const uint8_t *qu = qg + a.N * (a.kpad / 2);
-  const float *sx = a.a_scales + x_row * nkb, *sw = a.b_scales + (w_row + half * a.N) * nkb;
+  // Rows and columns past the end repeat the last one; they are not stored.  Lanes
+  // differ by 32-bit offsets from bases in scalar registers, but for the scales of w:
+  // a half has the gate's and a half the up projection's.
+  const int64_t w_row = (int64_t)t.e * 2 * a.N + col0;
+  const uint8_t *qx = a.a_codes + row0 * (nkb * 8), *qg = a.b_codes + w_row * (nkb * 8);
+  const uint8_t *qu = qg + a.N * (nkb * 8);
+  const uint32_t rx = min(l32, rows - 1) * nkb, rw = min(l32, cols - 1) * nkb;
+  const float *sx = a.a_scales + row0 * nkb;
+  const float *sw = a.b_scales + (w_row + half * a.N) * nkb + rw;
 
   floatx16 acc[2];
 #pragma unroll
@@ -101,12 +106,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const Gem
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
   const int runs = nkb / 4;                       // of four blocks
   for (int i = wave; i < runs; i += kSmallWaves) {
-    FourBlocks x, g, u;
-    x.load(qx + i * 32 + half * 16);
-    g.load(qg + i * 32 + half * 16);
-    u.load(qu + i * 32 + half * 16);
-    const u32x4_dword fx = *reinterpret_cast<const u32x4_dword *>(sx + i * 4);
+    const u32x4_dword vx = *reinterpret_cast<const u32x4_dword *>(qx + i * 32 + (rx * 8 + half * 16));
+    const u32x4_dword vg = *reinterpret_cast<const u32x4_dword *>(qg + i * 32 + (rw * 8 + half * 16));
+    const u32x4_dword vu = *reinterpret_cast<const u32x4_dword *>(qu + i * 32 + (rw * 8 + half * 16));
+    const u32x4_dword fx = *reinterpret_cast<const u32x4_dword *>(sx + i * 4 + rx);
     const u32x4_dword fw = *reinterpret_cast<const u32x4_dword *>(sw + i * 4);
+    __builtin_amdgcn_sched_barrier(0);            // all loads go out before the products
+    const FourBlocks x(vx), g(vg), u(vu);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
       block_product<GRID>(x.w[b], g.w[b], u.w[b], __uint_as_float(fx[b]), __uint_as_float(fw[b]),
@@ -114,10 +120,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(const Gem
   }
   // the last blocks, one to a wave
   if (const int k = runs * 4 + wave; k < nkb)
-    block_product<GRID>(*reinterpret_cast<const uint32_t *>(qx + k * 8 + half * 4),
-                        *reinterpret_cast<const uint32_t *>(qg + k * 8 + half * 4),
-                        *reinterpret_cast<const uint32_t *>(qu + k * 8 + half * 4), sx[k], sw[k],
-                        acc);
+    block_product<GRID>(*reinterpret_cast<const uint32_t *>(qx + k * 8 + (rx * 8 + half * 4)),
+                        *reinterpret_cast<const uint32_t *>(qg + k * 8 + (rw * 8 + half * 4)),
+                        *reinterpret_cast<const uint32_t *>(qu + k * 8 + (rw * 8 + half * 4)),
+                        sx[k + rx], sw[k], acc);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll

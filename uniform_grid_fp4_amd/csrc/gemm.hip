@@ -655,13 +655,14 @@ static int64_t gated_tiles(const GemmArgs &g, int bm, int bn) {
   return g.n_groups * ((rows + bm - 1) / bm) * ((g.N + bn - 1) / bn);
 }
 hipError_t launch_gated_gemm(const GemmArgs &g, hipStream_t st) {
-  // A 32 x 32 tile of the kernel for few tiles costs 0.033 us of the whole GPU at K
+  // A 32 x 32 tile of the kernel for few tiles costs 0.029 us of the whole GPU at K
   // = 2048, a 128 x 64 tile 0.14 us, but no less than 42 us together, the time of
-  // one tile (257 x 333 columns, K = 1000: 6.8 and 44 us; 512 x 2048, K = 2048: 34 and
-  // 43 us; 256 x 8192: 68 and 46 us; 128 rows over 32 experts of 2048 columns, K =
-  // 6144: 176 and 365 us).
+  // one tile (257 x 333 columns, K = 1000: 6.4 and 44 us; 512 x 2048, K = 2048: 29 and
+  // 43 us; 1266 x 1143, K = 384: 14.5 and 24.5; 256 x 8192, K = 2048: 55 and 47 us; 128 rows
+  // over 32 experts of 2048 columns, K = 6144: 177 and 365 us; 730 over 8 of 2412, K =
+  // 6720: 215 and 210).
   const int64_t few = gated_tiles(g, 32, 32), tiles = gated_tiles(g, kBM, kBN / 2);
-  if (10 * few < 42 * (tiles > 300 ? tiles : 300) && few < 1 << 20)
+  if (10 * few < 49 * (tiles > 300 ? tiles : 300) && few < 1 << 20)
     return launch_gated_small(g, st);
   const int64_t tiles_m = (g.M + kBM - 1) / kBM + (g.mode == 0 ? 0 : g.n_groups);
   const int64_t total = tiles_m * ((g.N + kBN / 2 - 1) / (kBN / 2));

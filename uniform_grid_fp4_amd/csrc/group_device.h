@@ -11,6 +11,13 @@ __device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) {
   return v < 0 ? 0 : (v > n ? n : v);
 }
 
+// A wave-uniform number in scalar registers.
+__device__ __forceinline__ int64_t wave_uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // The group and the tile in it of tile t = pick(number of tiles), where group e has ceil(rows of e / bm)
 // * per_row tiles.  Offsets are clamped to [0, M], a decreasing pair is an empty
 // group.  Every wave finds it by itself: a lane sums a run of groups, a scan over
@@ -20,8 +27,8 @@ struct GroupTile {
   int64_t row0, rows, local, tiles_m;
 };
 template <typename P>
-__device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_groups, int64_t M,
-                                                int bm, int64_t per_row, P pick) {
+__device__ __forceinline__ GroupTile find_tile(const int64_t *goff, int n_groups, int64_t M,
+                                               int bm, int64_t per_row, P pick) {
   GroupTile g{0, 0, M, 0, (M + bm - 1) / bm};
   if (goff == nullptr) {
     g.local = pick(g.tiles_m * per_row);
@@ -64,6 +71,14 @@ __device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_group
     }
     base += n * per_row;
   }
+}
+// The same in scalar registers (every lane has found it, which the compiler cannot see).
+template <typename P>
+__device__ __forceinline__ GroupTile group_tile(const int64_t *goff, int n_groups, int64_t M,
+                                                int bm, int64_t per_row, P pick) {
+  const GroupTile g = find_tile(goff, n_groups, M, bm, per_row, pick);
+  return {__builtin_amdgcn_readfirstlane(g.e), wave_uniform(g.row0), wave_uniform(g.rows),
+          wave_uniform(g.local), wave_uniform(g.tiles_m)};
 }
 
 }  // namespace ufp4

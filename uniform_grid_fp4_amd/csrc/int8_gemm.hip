@@ -326,12 +326,6 @@ struct TileShape {
       KS * 2 * kStage + (kBM + 2 * kBN) * sizeof(float) + (kStays ? kLines : 0);
 };
 
-// A wave-uniform number in scalar registers.
-__device__ __forceinline__ int64_t wave_uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
-}
 // a / b; both are small where it counts.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((uint64_t)(a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
@@ -376,16 +370,11 @@ int8_tile_kernel(const Int8GemmArgs a, int64_t tiles_n, int64_t first) {
   // the tiles that there are: eighths of the grid, which is cut for the most tiles that
   // the groups can have, would leave the last XCDs idle.
   auto place = [&](int64_t at) __attribute__((always_inline)) -> bool {
-    GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, [=](int64_t tiles) {
+    const GroupTile g = group_tile(a.goff, a.n_groups, a.M, BM, tiles_n, [=](int64_t tiles) {
       const int64_t per = (tiles + kXcd - 1) / kXcd;
       return at / kXcd < per ? at % kXcd * per + at / kXcd : tiles;
     });
-    g.e = __builtin_amdgcn_readfirstlane(g.e);    // into scalar registers
     if (g.e < 0) return false;
-    g.row0 = wave_uniform(g.row0);
-    g.rows = wave_uniform(g.rows);
-    g.local = wave_uniform(g.local);
-    g.tiles_m = wave_uniform(g.tiles_m);
     const int64_t band = quotient(g.local, kBandRows * tiles_n);
     const int64_t in_band = g.local - band * kBandRows * tiles_n;
     const int64_t deep = min((int64_t)kBandRows, g.tiles_m - band * kBandRows);
