@@ -415,10 +415,13 @@ __global__ __launch_bounds__(1024) void layernorm_dw_final_kernel(const LayerNor
 // vectors per lane of a wave it would spill, so 193 to 256 vectors take 256 threads
 // with one each.  With fewer, too many of them would idle (30000 x 1280 bf16: 71 us,
 // a wave per row 63).  In the same way twice the threads take two vectors each where
-// half would take four.
+// half would take four, and in FP32, whose partial rows of that length are few beside
+// the rows, 512 threads one each where 256 would take two (16000 x 1536: 80 and 77 us, 4099 x
+// 1411: 24 and 23; bf16 8192 x 4096: 59 and 62).
 static RowShape bwd_shape(int64_t cols, int v) {
   const int64_t n = (cols + v - 1) / v;
   const RowShape s = row_shape(cols, v);
+  if (v == Elem<float>::V && n > 256 && n <= 512) return {512, 1};
   if (s.nv != 4) return s;
   return n <= 256 ? RowShape{256, 1} : RowShape{s.tpr * 2, 2};
 }
@@ -490,6 +493,7 @@ static hipError_t bwd_rows(const LayerNormBwdArgs &a, RowShape s, int slices, hi
   }
   UFP4_BWD_SHAPES(UFP4_NORM)
   if constexpr (sizeof(T) == 4) {
+    UFP4_NORM(512, 1)
     UFP4_NORM(1024, 3)
   }
 #undef UFP4_NORM
