@@ -280,13 +280,16 @@ def test_linear_is_quantize_then_product(m, dtype):
 
 
 @pytest.mark.parametrize("m,k", [(1, 1), (1, 7), (1, 130), (1, 2048), (1, 32768), (1, 32641),
-                                 (2, 5000), (3, 10000), (4, 8192), (5, 100), (7, 4000), (8, 4096),
-                                 (9, 3500), (15, 2000), (16, 2048), (16, 130), (16, 3)])
+                                 (2, 5000), (2, 8192), (3, 5000), (3, 10000), (4, 4096), (4, 8192),
+                                 (5, 100), (7, 2200), (7, 4000), (8, 2048), (8, 4096), (9, 1700),
+                                 (9, 3500), (15, 1000), (15, 2000), (16, 1024), (16, 2048),
+                                 (16, 130), (16, 3)])
 @pytest.mark.parametrize("dtype", BOTH)
 def test_few_rows_quantized_by_the_product(m, k, dtype):
     """Bit for bit what the two calls give, at the rows' ends, zero rows and rows
     that are not finite among them."""
-    assert F.ufp4_int8_linear_workspace_size(m, k) == 0
+    fuses = F.ufp4_int8_linear_workspace_size(m, k) == 0
+    assert fuses == (m == 1 or m * F.int8_kpad(k) <= 16384)
     x, w = normal(m, k, dtype), F.ufp4_int8_quantize(normal(38, k, seed=2, std=0.05))
     bias = normal(1, 38, seed=3)[0].contiguous()
     for i in range(3):

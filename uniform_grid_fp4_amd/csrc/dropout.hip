@@ -5,7 +5,8 @@
 // elements of 16 bits each.  Per element a call's 20 wide multiplies and 20
 // three-input xors come to 5 instructions, next to some 6 for the element
 // itself and 4 to 12 bytes: bound by memory, with the vector unit about half
-// busy at bf16.
+// busy at bf16.  32768 x 6144 bf16: onto a residual 187 us (1208 MB, 6.5 TB/s), alone (as
+// in the backward pass) 138 us (805 MB, 5.8 TB/s); 257 x 1411 FP32 3.4 us.
 #include "block_device.h"
 #include "ffn_kernels.h"
 #include "ufp4_device.h"

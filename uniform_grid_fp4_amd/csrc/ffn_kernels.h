@@ -96,10 +96,13 @@ struct Int8GemmArgs {
 };
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st);
 // Whether that many rows of one group are quantized by the product's workgroups
-// themselves.
-constexpr int64_t kFusedBytes = 32768;
+// themselves.  It saves a launch, an allocation and, for one row, time on the GPU (us,
+// gated, one launch and two: 1 x 2048 to 2 x 8192 10.1 and 10.2, 1 x 32768 to 2 x 1024 36.7 and
+// 45.5); more rows take longer than in a kernel of their own, which pays while the
+// launch costs more (16 x 1024 to 2 x 2048 6.8 and 5.7, 4 x 2048 to 2 x 8192 11.4 and 10.4, but 16 x
+// 2048 to 2 x 8192 17.5 and 11.7, 8 x 4096 to 2 x 2048 12.6 and 9.5).
 inline bool int8_fuses(int64_t rows, int64_t kpad) {
-  return rows <= 16 && rows * kpad <= kFusedBytes;
+  return rows == 1 ? kpad <= 32768 : rows <= 16 && rows * kpad <= 16384;
 }
 // Quantizes q.x into q.q and q.scale, which are a.a and a.sa, and multiplies; where
 // it fuses and there is one group without offsets, q.q and q.scale are not used.

@@ -1,7 +1,8 @@
 // Rows in 8-bit integers with one scale each (gfx950):
 //   scale = max|x| / 127,  q = round(x * (127 * (1 / max|x|))), nearest even
 // One pass: the row stays in registers between its maximum and its codes.  About
-// 5 operations per element against 3 bytes (bf16): bound by memory.
+// 5 operations per element against 3 bytes (bf16): bound by memory.  30000 x 4096 bf16
+// 67 us (369 MB, 5.5 TB/s), FP32 111 us (5.5 TB/s), x 4099 bf16 73 us; 8192 x 2048 11 us.
 #include "ffn_kernels.h"
 #include "int8_device.h"
 #include "row_device.h"
