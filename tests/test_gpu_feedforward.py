@@ -262,6 +262,47 @@ def test_captured_calls_replay():
             assert torch.equal(p, q), (i, j)
 
 
+def test_captured_products_of_every_kind_of_tile():
+    """int8 products from one row to the largest tiles, dense and by experts, and the
+    gated product of few tiles and of many, in one graph; two graphs of them that
+    share nothing replay in turn."""
+    shapes = [(1, 256, 4096), (20, 300, 2000), (60, 130, 1000), (200, 512, 1500), (905, 1536, 1411),
+              (1000, 2048, 700), (2000, 2050, 900), (2900, 5000, 1411)]
+    ws = [F.ufp4_int8_quantize(bf(n, k, seed=i, std=0.05)) for i, (m, n, k) in enumerate(shapes)]
+    experts = F.ufp4_int8_quantize(bf(4 * 256, 640, seed=30, std=0.05))
+    offsets = torch.tensor([0, 70, 70, 300, 500], device=DEV)
+    wq = U.ufp4_rht_quantize(bf(2 * 640, 512, seed=31, std=0.05), U.BLOCKS_ALONG_COLS)
+
+    def inputs(seed):
+        return [bf(m, k, seed=seed + i) for i, (m, n, k) in enumerate(shapes)] + \
+            [bf(500, 640, seed=seed + 40), bf(40, 512, seed=seed + 41), bf(3000, 512, seed=seed + 42)]
+
+    def step(xs):
+        out = [F.ufp4_int8_linear(x, w, act=F.ACT_SILU if w.q.shape[0] % 2 == 0 else F.ACT_NONE)
+               for x, w in zip(xs, ws)]
+        out.append(F.ufp4_int8_linear(xs[-3], experts, offsets=offsets))
+        for x in xs[-2:]:
+            out += F.ufp4_gated_gemm(U.ufp4_rht_quantize(x, U.BLOCKS_ALONG_COLS), wq)
+        return out
+
+    held = [inputs(100), inputs(200)]
+    step(held[0])
+    torch.cuda.synchronize()
+    graphs, captured = [], []
+    for xs in held:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            captured.append(step(xs))
+    for i in range(4):
+        for x, new in zip(held[i % 2], inputs(300 + 100 * i)):
+            x.copy_(new)
+        want = step(held[i % 2])
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        for j, (p, q) in enumerate(zip(captured[i % 2], want)):
+            assert torch.equal(p, q), (i, j)
+
+
 def test_two_streams_at_once():
     """The same calls on two streams without waits between them, workspaces of
     their own: what each gives alone."""
