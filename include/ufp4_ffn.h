@@ -145,7 +145,8 @@ typedef struct {
  * dtype; workspace: device, 16-byte aligned, at least
  * ufp4_int8_linear_workspace_size(M, k, grouped) bytes, overwritten, grouped 0
  * where d_group_offsets is NULL (0 bytes for a few rows, which every workgroup
- * quantizes itself: then it may be NULL).  y may not be x.
+ * quantizes itself: then it may be NULL; a workspace of the size for grouped 1 makes
+ * such a call faster where y has more than 16384 columns).  y may not be x.
  * Returns OK, INVALID_ARG, SHAPE (k of a and w differ, rows not a multiple of
  * the groups, n_groups outside 1..1024), UNSUPPORTED (k beyond 131071: a sum
  * could pass 31 bits), HIP. */

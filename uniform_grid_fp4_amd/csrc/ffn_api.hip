@@ -270,10 +270,13 @@ ufp4_status ufp4_int8_linear(const void *x, int64_t ld_x, int32_t dtype, int64_t
   if (rows == 0) return UFP4_OK;
   const size_t need =
       ufp4_int8_linear_workspace_size(rows, cols, d_group_offsets != nullptr ? 1 : 0);
+  if (need > 0 && (!good(workspace, 16) || workspace_bytes < need)) return UFP4_ERR_INVALID_ARG;
+  const int64_t out_n = act == UFP4_ACT_NONE ? g.N : g.N / 2;
+  const bool splits = int8_splits(rows, g.kpad, out_n) && good(workspace, 16) &&
+                      workspace_bytes >= ufp4_int8_linear_workspace_size(rows, cols, 1);
   int8_t *q = nullptr;
   float *scale = nullptr;
-  if (need > 0) {
-    if (!good(workspace, 16) || workspace_bytes < need) return UFP4_ERR_INVALID_ARG;
+  if (need > 0 || splits) {
     q = static_cast<int8_t *>(workspace);
     scale = reinterpret_cast<float *>(q + rows * g.kpad);
   }

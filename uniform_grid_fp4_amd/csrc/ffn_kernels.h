@@ -104,8 +104,19 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a, hipStream_t st);
 inline bool int8_fuses(int64_t rows, int64_t kpad) {
   return rows == 1 ? kpad <= 32768 : rows <= 16 && rows * kpad <= 16384;
 }
-// Quantizes q.x into q.q and q.scale, which are a.a and a.sa, and multiplies; where
-// it fuses and there is one group without offsets, q.q and q.scale are not used.
+// Whether a workspace that the caller brings all the same is used, for two launches:
+// every 16 output columns quantize the rows once more, and beyond so many columns
+// that costs more than the launch, but for the fewest elements (us on the GPU, one
+// launch and two, to 16384, 32768 and 65536 columns of a plain product: 1 x 2048 10.1 and
+// 10.5, 17.1 and 14.8, 30.2 and 25.4; 8 x 2048 15.3 and 11.5, 25.8 and 17.1, 46.6 and 30.2;
+// 16 x 1024 13.5 and 8.9, 23.4 and 13.2, 40.9 and 21.7; 16 x 128 8.4 and 4.9, 13.8 and 6.1,
+// 23.4 and 8.2.  One eager call after the other the host takes 10 and 13.4: 1 x 512 to
+// 32768 10.1 and 13.4, 8 x 512 11.6 and 13.6, 16 x 1024 23.9 and 13.4).
+inline bool int8_splits(int64_t rows, int64_t kpad, int64_t out_n) {
+  return out_n > 16384 && rows * kpad >= 2048;
+}
+// Quantizes q.x into q.q and q.scale, which are a.a and a.sa, and multiplies; with
+// q.q nullptr (rows that fuse, one group without offsets) in one launch.
 hipError_t launch_int8_linear(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st);
 
 constexpr int kMaxFfnGroups = 1024;

@@ -738,7 +738,7 @@ static hipError_t fused(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream
 }
 hipError_t launch_int8_linear(const Int8GemmArgs &a, const Int8QuantArgs &q, hipStream_t st) {
   if (a.M == 0) return hipSuccess;
-  if (a.goff == nullptr && int8_fuses(a.M, a.kpad))
+  if (q.q == nullptr)
     return q.bf16 ? fused<uint16_t>(a, q, st) : fused<float>(a, q, st);
   const hipError_t e = launch_int8_quantize(q, st);
   return e == hipSuccess ? launch_int8_gemm(a, st) : e;

@@ -28,6 +28,8 @@ EXPORTS = ("ufp4_layernorm", "ufp4_layernorm_bwd", "ufp4_layernorm_bwd_workspace
 ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 MAX_GROUPS = 1024
 INT8_MAX_K = 131071
+INT8_FEW_COLUMNS = 16384      # beyond, few rows too are quantized into a workspace,
+INT8_FEW_ELEMENTS = 2048      # from so many on
 
 _lib = None
 
@@ -368,10 +370,11 @@ def ufp4_int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] 
         raise ValueError(f"x has rows of {cols}, w of {w.k}")
     out_dtype = x.dtype if out_dtype is None else out_dtype
     dw, groups, y = _int8_out(rows, w, bias, act, offsets, out_dtype, dev)
-    need = lib().ufp4_int8_linear_workspace_size(rows, cols, offsets is not None)
+    size = lib().ufp4_int8_linear_workspace_size
+    need = size(rows, cols, offsets is not None)
     ws = None
-    if need:
-        ws, need = _workspace(workspace, need, dev)
+    if need or (y.shape[1] > INT8_FEW_COLUMNS and rows * int8_kpad(cols) >= INT8_FEW_ELEMENTS):
+        ws, need = _workspace(workspace, need or size(rows, cols, True), dev)
         ws = ws.data_ptr()
     _call("ufp4_int8_linear", dev, x.data_ptr(), ld, _CODE[x.dtype], rows, cols,
           dw.buffer_info()[0], _p(bias), act, groups, _p(offsets), _CODE[out_dtype], y.data_ptr(),
