@@ -95,10 +95,14 @@ ufp4_status ufp4_dropout(const void *x, int64_t ld_x, const void *residual, int6
  * pass.  Both of type out_dtype, rounded once from FP32 (y from the unrounded
  * g and u).  d_group_offsets NULL: one group of all rows (n_groups 1), else
  * int64 [n_groups + 1] as ufp4_grouped_gemm takes them; rows in no group are
- * left as they are.  Accumulation as in ufp4_gemm_out, whose g and u these are
- * bit for bit.  Returns OK, INVALID_ARG (also act NONE), SHAPE (also an odd
- * number of rows per group, n_groups outside 1..1024, T = 0 or F = 0), MISMATCH, UNSUPPORTED
- * (K beyond 65536), HIP.
+ * left as they are.  g and u are the FP32 sums of ufp4_gemm_out's terms, one per block
+ * of 16.  Where there are many tiles of output they are added in its order, one after
+ * the other, and g and u are its bits; where there are few, in eight such chains and
+ * the chains' sums in order.  T, F and n_groups decide, so a row's last bits may
+ * change with the rows beside it; either way a sum is within (K / 16 + 8) 2^-24 of the
+ * sum of its terms' sizes, and a call repeated gives the same bits.  Returns OK,
+ * INVALID_ARG (also act NONE), SHAPE (also an odd number of rows per group, n_groups
+ * outside 1..1024, T = 0 or F = 0), MISMATCH, UNSUPPORTED (K beyond 65536), HIP.
  *
  * ufp4_gated_bwd: from dy [rows, cols] and gu [rows, 2 cols],
  *   dgu = (dy u act'(g) | dy act(g))   dense [rows, 2 cols],
@@ -139,8 +143,9 @@ typedef struct {
  * FP32, rounded once to out_dtype.  d_group_offsets NULL: one group of all
  * rows (n_groups 1); else int64 [n_groups + 1] over a's rows, w has n_groups
  * times the rows of one expert, and a bias as many entries; rows of a in no
- * group leave their rows of y as they are.  Which kernel runs goes by M /
- * n_groups; results are the same bit for bit.
+ * group leave their rows of y as they are.  Which kernel runs goes by M, N, K and
+ * n_groups; results are the same bit for bit.  The FP32 operations are ((sum *
+ * scale_a) * scale_w) + bias, each rounded.
  * ufp4_int8_linear: the same with a = ufp4_int8_quantize(x), x [M, k] of type
  * dtype; workspace: device, 16-byte aligned, at least
  * ufp4_int8_linear_workspace_size(M, k, grouped) bytes, overwritten, grouped 0

@@ -125,7 +125,7 @@ def test_strides_and_rows_in_no_group(dtype, code):
 
 def test_a_row_in_few_tiles_and_in_many():
     """The same row alone and in a batch of the other kernel: the same block terms,
-    added up in another order."""
+    added up in another order, the same one at every call."""
     (few, k, f), (many, _, _) = SEAM
     xq, wq = quantized(bf(many, k, seed=13)), quantized(bf(2 * f, k, seed=14, std=0.1))
     part = quantized(bf(many, k, seed=13)[:few])
@@ -133,3 +133,7 @@ def test_a_row_in_few_tiles_and_in_many():
     b = F.ufp4_gated_gemm(xq, wq, out_dtype=torch.float32)
     assert near(a.gu, b.gu[:few], part, wq)
     check_whole(a.y, a.gu, F.ACT_SILU)
+    assert torch.equal(b.gu, U.ufp4_gemm_out(U.FPROP, xq, wq, torch.float32))
+    for q, want in ((part, a), (xq, b)):
+        again = F.ufp4_gated_gemm(q, wq, out_dtype=torch.float32)
+        assert torch.equal(again.gu, want.gu) and torch.equal(again.y, want.y)

@@ -54,7 +54,8 @@
 // same 32 columns (the workgroup's 128 rows of B are 64 of either, in runs of
 // 32), so gate and up values meet in the same lane and register and the
 // activation and the product are an epilogue of two operands in registers.  The
-// K loop is the same, and so are g and u bit for bit.  Few tiles go to gated_small.hip.
+// K loop is the same, and so are g and u bit for bit.  Few tiles go to gated_small.hip,
+// which adds the same terms up in another order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

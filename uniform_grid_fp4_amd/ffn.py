@@ -248,7 +248,8 @@ def ufp4_gated_gemm(xq: U.Quantized, wq: U.Quantized, act: int = ACT_SILU, keep:
     """act(x Wg^T) * (x Wu^T) of quantized operands.  wq has Wg's rows, then
     Wu's, for each expert of `offsets` (int64 [experts + 1] over x's rows, the
     last entry their number; None: one group).  `keep` returns g and u too, in
-    out_dtype (bf16 or float32)."""
+    out_dtype (bf16 or float32).  The order of their sums, and so a row's last bits,
+    goes by the sizes of the whole call."""
     if out_dtype not in _CODE:
         raise TypeError(f"out_dtype is float32 or bfloat16, got {out_dtype}")
     dx = _operand(xq, "xq")
