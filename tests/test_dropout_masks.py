@@ -1,0 +1,61 @@
+"""Which masks the dropout layers name, without a GPU: the library's call stands in
+as a note of (seed, offset)."""
+import copy
+import itertools
+
+import pytest
+import torch
+
+from uniform_grid_fp4_amd import feedforward as W
+from uniform_grid_fp4_amd import layers as Y
+
+
+@pytest.fixture
+def seen(monkeypatch):
+    """(seed, offset) of every call, forward or backward."""
+    calls = []
+
+    def call(x, p, seed, offset, residual=None):
+        calls.append((seed, int(offset)))
+        return x * 0.5 if residual is None else x * 0.5 + residual
+
+    monkeypatch.setattr(W.F, "ufp4_dropout", call)
+    return calls
+
+
+def test_layers_have_masks_of_their_own(seen):
+    x = torch.ones(2, 4)
+    drops = [W.Dropout(0.5) for _ in range(3)] + [W.UFP4FeedForward(8, 4, p=0.1).drop
+                                                  for _ in range(3)]
+    drops += [copy.deepcopy(drops[0]), copy.deepcopy(torch.nn.ModuleList([drops[1]]))[0]]
+    for d in drops:
+        d(x)
+    assert len(set(seen)) == len(drops)
+    # a run that seeds torch and builds the same layers draws the same
+    again = []
+    for _ in range(2):
+        W._drawn = itertools.count(1)
+        torch.manual_seed(7)
+        again.append([W.Dropout(0.5).seed, W.UFP4FeedForward(8, 4, p=0.1).drop.seed])
+    assert again[0] == again[1] and again[0][0] != again[0][1]
+    assert all(0 <= s < 1 << 64 for s in again[0])
+
+
+def test_a_given_seed_is_kept():
+    assert W.Dropout(0.5, seed=3).seed == 3 and W.Dropout(0.5, 0).seed == 0
+    layer = W.UFP4FeedForward(8, 4, p=0.1, seed=3)
+    assert layer.drop.seed == copy.deepcopy(layer).drop.seed == 3
+    assert layer.gated.masks == Y.draw_sign_masks(3) and layer.down.masks == Y.draw_sign_masks(4)
+
+
+def test_the_products_of_a_layer_without_a_seed_have_zero():
+    layer = W.UFP4FeedForward(8, 4)
+    assert layer.gated.masks == Y.draw_sign_masks(0) and layer.down.masks == Y.draw_sign_masks(1)
+    assert layer.gated.sr_seed == 0 and layer.down.sr_seed == 0x9E3779B97F4A7C15
+
+
+def test_building_a_layer_draws_nothing_from_torch():
+    torch.manual_seed(1)
+    before = torch.get_rng_state()
+    W.Dropout(0.5)
+    assert torch.equal(before, torch.get_rng_state())

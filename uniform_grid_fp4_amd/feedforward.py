@@ -10,6 +10,8 @@ needs kept, and next to them the bf16 gate and up values.
 """
 from __future__ import annotations
 
+import copy
+import itertools
 from typing import Optional, Union
 
 import torch
@@ -114,19 +116,39 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
     return y.reshape(x.shape)
 
 
+_drawn = itertools.count(1)
+
+
+def _own_seed() -> int:
+    """A seed that no other layer of the process has, from torch's and the number
+    drawn so far."""
+    return (torch.initial_seed() + next(_drawn) * 0x9E3779B97F4A7C15) & ((1 << 64) - 1)
+
+
 class Dropout(torch.nn.Module):
     """forward(x, residual=None) = residual + dropout(x); in eval mode nothing is
     dropped.  Every training call draws another mask: the k-th has offset k, or
     what `offset` holds, an int64 tensor of one element on the GPU that the caller
-    advances (between the replays of a captured step, for instance).  A call that
-    is run again to recompute its activations counts as another: give such calls
-    `dropout` with the same offset both times."""
+    advances (between the replays of a captured step, for instance).  Layers of one
+    seed drop the same elements; without one a layer, and a deep copy of it, has its
+    own, the same in every run that seeds torch and builds its layers in one order.
+    A call that is run again to recompute its activations counts as another: give
+    such calls `dropout` with the same offset both times."""
 
-    def __init__(self, p: float, seed: int = 0, offset: Optional[torch.Tensor] = None):
+    def __init__(self, p: float, seed: Optional[int] = None,
+                 offset: Optional[torch.Tensor] = None):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p = {p}: a probability")
-        self.p, self.seed, self.calls, self.offset = p, seed, 0, offset
+        self.given = seed is not None
+        self.p, self.seed, self.calls, self.offset = p, seed if self.given else _own_seed(), 0, offset
+
+    def __deepcopy__(self, memo):
+        new = memo[id(self)] = self.__class__.__new__(self.__class__)
+        new.__dict__.update(copy.deepcopy(self.__dict__, memo))
+        if not getattr(new, "given", True):          # a pickle of before has none
+            new.seed = _own_seed()
+        return new
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         p = self.p if self.training else 0.0
@@ -240,15 +262,17 @@ class UFP4GatedExpertLinear(torch.nn.Module):
 class UFP4FeedForward(torch.nn.Module):
     """A pre-norm feed-forward sublayer: h = x + residual, then h + dropout(down(
     gated(norm(h)))), the new residual stream.  x and residual are bf16 [...,
-    hidden]; without a residual h is x."""
+    hidden]; without a residual h is x.  `seed` is that of the products (0 without
+    one) and of the dropout (its own without one)."""
 
-    def __init__(self, hidden: int, ffn: int, p: float = 0.0, act: str = "silu", seed: int = 0,
-                 device=None, grid: int = U.GRID_UNIFORM):
+    def __init__(self, hidden: int, ffn: int, p: float = 0.0, act: str = "silu",
+                 seed: Optional[int] = None, device=None, grid: int = U.GRID_UNIFORM):
         super().__init__()
         self.norm = LayerNorm(hidden, device=device)
+        given, seed = seed, 0 if seed is None else seed
         self.gated = UFP4GatedLinear(hidden, ffn, act=act, seed=seed, grid=grid, device=device)
         self.down = UFP4Linear(ffn, hidden, seed=seed + 1, grid=grid, device=device)
-        self.drop = Dropout(p, seed=seed)
+        self.drop = Dropout(p, seed=given)
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         if residual is None:
