@@ -59,3 +59,37 @@ def test_building_a_layer_draws_nothing_from_torch():
     before = torch.get_rng_state()
     W.Dropout(0.5)
     assert torch.equal(before, torch.get_rng_state())
+
+
+def test_a_state_dict_goes_on_with_the_masks(seen):
+    x = torch.ones(2, 4)
+    for make in (lambda: W.Dropout(0.5), lambda: W.Dropout(0.5, seed=2 ** 64 - 3),
+                 lambda: W.Dropout(0.5, seed=-1)):
+        old, new = make(), make()
+        for _ in range(3):
+            old(x)
+        new.load_state_dict(old.state_dict())
+        del seen[:]
+        old(x), new(x)
+        word = (1 << 64) - 1
+        assert seen[0][0] & word == seen[1][0] & word and seen[0][1] == seen[1][1] == 4
+    # as a part of a sublayer, through what only tensors pass
+    old, new = W.UFP4FeedForward(8, 4, p=0.5), W.UFP4FeedForward(8, 4, p=0.5)
+    old.drop(x)
+    state = old.state_dict()
+    assert all(isinstance(v, torch.Tensor) for v in state.values())
+    new.load_state_dict({k: v.clone() for k, v in state.items()})
+    assert (new.drop.seed, new.drop.calls) == (old.drop.seed, 1)
+
+
+def test_a_state_dict_from_before_loads():
+    """Without the masks' place a layer keeps its own."""
+    layer = W.UFP4FeedForward(8, 4, p=0.5)
+    seed = layer.drop.seed
+    layer.drop.calls = 2
+    state = {k: v for k, v in layer.state_dict().items() if "drop" not in k}
+    assert len(state) == 4
+    layer.load_state_dict(state)
+    assert (layer.drop.seed, layer.drop.calls) == (seed, 2)
+    with pytest.raises(RuntimeError, match="Missing"):
+        layer.load_state_dict({k: v for k, v in state.items() if "down" not in k})

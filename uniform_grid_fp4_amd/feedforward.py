@@ -132,6 +132,7 @@ class Dropout(torch.nn.Module):
     advances (between the replays of a captured step, for instance).  Layers of one
     seed drop the same elements; without one a layer, and a deep copy of it, has its
     own, the same in every run that seeds torch and builds its layers in one order.
+    The state dict holds seed and number of calls: who loads it goes on from there.
     A call that is run again to recompute its activations counts as another: give
     such calls `dropout` with the same offset both times."""
 
@@ -149,6 +150,19 @@ class Dropout(torch.nn.Module):
         if not getattr(new, "given", True):          # a pickle of before has none
             new.seed = _own_seed()
         return new
+
+    def get_extra_state(self) -> torch.Tensor:
+        seed = self.seed & ((1 << 64) - 1)
+        return torch.tensor([seed - (seed >> 63 << 64), self.calls], dtype=torch.int64)
+
+    def set_extra_state(self, state: torch.Tensor) -> None:
+        seed, self.calls = state.tolist()
+        self.seed = seed & ((1 << 64) - 1)
+
+    def _load_from_state_dict(self, state_dict, prefix, metadata, strict, *more):
+        # a state dict without the extra state is one from before there was any
+        strict = strict and prefix + "_extra_state" in state_dict
+        super()._load_from_state_dict(state_dict, prefix, metadata, strict, *more)
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         p = self.p if self.training else 0.0
