@@ -5,6 +5,7 @@ import itertools
 
 import pytest
 import torch
+import torch.utils.checkpoint
 
 from uniform_grid_fp4_amd import feedforward as W
 from uniform_grid_fp4_amd import layers as Y
@@ -93,3 +94,11 @@ def test_a_state_dict_from_before_loads():
     assert (layer.drop.seed, layer.drop.calls) == (seed, 2)
     with pytest.raises(RuntimeError, match="Missing"):
         layer.load_state_dict({k: v for k, v in state.items() if "down" not in k})
+
+
+def test_recomputed_with_an_offset_in_a_tensor(seen):
+    """Recomputation hands what was saved out once."""
+    x, step = torch.ones(2, 4, requires_grad=True), torch.tensor([3])
+    torch.utils.checkpoint.checkpoint(lambda t: W.dropout(t, 0.5, 1, step).sin(), x,
+                                      use_reentrant=False).sum().backward()
+    assert set(seen) == {(1, 3)}

@@ -97,8 +97,9 @@ class _DropoutFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        # an offset on the GPU that was changed since raises here
-        offset = ctx.offset if not ctx.saved_tensors else ctx.saved_tensors[0]
+        # an offset on the GPU that was changed since raises here; a recomputed call
+        # gives what it saved once
+        offset, = ctx.saved_tensors or (ctx.offset,)
         dx = None
         if ctx.needs_input_grad[0]:
             dx = first_order(F.ufp4_dropout, _rows(dy), ctx.p, ctx.seed, offset)
