@@ -102,3 +102,49 @@ def test_recomputed_with_an_offset_in_a_tensor(seen):
     torch.utils.checkpoint.checkpoint(lambda t: W.dropout(t, 0.5, 1, step).sin(), x,
                                       use_reentrant=False).sum().backward()
     assert set(seen) == {(1, 3)}
+
+
+def test_a_call_takes_an_offset(seen):
+    """In place of the layer's count, and of the layer's own tensor."""
+    x = torch.ones(2, 4, requires_grad=True)
+    step = torch.tensor([9])
+    for drop in (W.Dropout(0.5, seed=1), W.Dropout(0.5, seed=1, offset=step)):
+        del seen[:]
+        drop(x, offset=5).sum().backward()
+        drop(x, x, torch.tensor([6])).sum().backward()
+        assert seen == [(1, 5), (1, 5), (1, 6), (1, 6)] and drop.calls == 0
+        drop.eval()
+        assert drop(x, offset=5) is x
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_recomputed_calls(seen, reentrant):
+    """A call that runs again in the backward pass names the mask it named before,
+    or is refused: with the next one the gradients would not be the loss's."""
+    x = torch.ones(2, 4, requires_grad=True)
+    run = lambda *a: torch.utils.checkpoint.checkpoint(*a, use_reentrant=reentrant).sum()
+    drop = W.Dropout(0.5, seed=1)
+    run(lambda t: drop(t, None, 5).sin(), x).backward()
+    assert {at for _, at in seen} == {5}
+    layer = W.Dropout(0.5, seed=1, offset=torch.tensor([6]))
+    del seen[:]
+    run(lambda t: layer(t).sin(), x).backward()
+    assert {at for _, at in seen} == {6}
+    loss = run(lambda t: drop(t).sin(), x)
+    with pytest.raises(RuntimeError, match="offset"):
+        loss.backward()
+    assert drop.calls == 1
+    drop(x).sum().backward()                     # the next call is none of that
+    assert drop.calls == 2
+    # nothing is drawn where nothing is dropped
+    none = W.Dropout(0.0)
+    run(lambda t: none(t, t).sin(), x).backward()
+
+
+def test_the_sublayer_hands_an_offset_on(seen, monkeypatch):
+    layer = W.UFP4FeedForward(8, 4, p=0.5, seed=3, offset=torch.tensor([4]))
+    for part in ("norm", "gated", "down"):
+        monkeypatch.setattr(layer, part, torch.nn.Identity())
+    x = torch.ones(2, 8)
+    layer(x), layer(x, offset=8)
+    assert seen == [(3, 4), (3, 8)]

@@ -126,6 +126,10 @@ def _own_seed() -> int:
     return (torch.initial_seed() + next(_drawn) * 0x9E3779B97F4A7C15) & ((1 << 64) - 1)
 
 
+# Whether autograd is running a backward pass on this thread (-1: no).
+_in_backward = getattr(torch._C, "_current_graph_task_id", lambda: -1)
+
+
 class Dropout(torch.nn.Module):
     """forward(x, residual=None) = residual + dropout(x); in eval mode nothing is
     dropped.  Every training call draws another mask: the k-th has offset k, or
@@ -134,8 +138,9 @@ class Dropout(torch.nn.Module):
     seed drop the same elements; without one a layer, and a deep copy of it, has its
     own, the same in every run that seeds torch and builds its layers in one order.
     The state dict holds seed and number of calls: who loads it goes on from there.
-    A call that is run again to recompute its activations counts as another: give
-    such calls `dropout` with the same offset both times."""
+    `forward` takes an `offset` too (as `dropout` does), in place of the layer's.  A
+    call that a backward pass runs again to recompute its activations needs one: by
+    count it would draw another mask than the loss had, and is refused."""
 
     def __init__(self, p: float, seed: Optional[int] = None,
                  offset: Optional[torch.Tensor] = None):
@@ -165,13 +170,18 @@ class Dropout(torch.nn.Module):
         strict = strict and prefix + "_extra_state" in state_dict
         super()._load_from_state_dict(state_dict, prefix, metadata, strict, *more)
 
-    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                offset: Union[int, torch.Tensor, None] = None) -> torch.Tensor:
         p = self.p if self.training else 0.0
         if p == 0.0 and residual is None:
             return x
-        offset = self.offset
         if offset is None:
-            self.calls += p > 0.0
+            offset = self.offset
+        if offset is None:
+            if p > 0.0:
+                if _in_backward() != -1:
+                    raise RuntimeError("a dropout that a backward pass recomputes needs an offset")
+                self.calls += 1
             offset = self.calls
         return dropout(x, p, self.seed, offset, residual)
 
@@ -278,23 +288,26 @@ class UFP4FeedForward(torch.nn.Module):
     """A pre-norm feed-forward sublayer: h = x + residual, then h + dropout(down(
     gated(norm(h)))), the new residual stream.  x and residual are bf16 [...,
     hidden]; without a residual h is x.  `seed` is that of the products (0 without
-    one) and of the dropout (its own without one)."""
+    one) and of the dropout (its own without one); `offset`, of the layer or of a
+    call, is the dropout's (see Dropout: captured and recomputed calls need one)."""
 
     def __init__(self, hidden: int, ffn: int, p: float = 0.0, act: str = "silu",
-                 seed: Optional[int] = None, device=None, grid: int = U.GRID_UNIFORM):
+                 seed: Optional[int] = None, device=None, grid: int = U.GRID_UNIFORM,
+                 offset: Optional[torch.Tensor] = None):
         super().__init__()
         self.norm = LayerNorm(hidden, device=device)
         given, seed = seed, 0 if seed is None else seed
         self.gated = UFP4GatedLinear(hidden, ffn, act=act, seed=seed, grid=grid, device=device)
         self.down = UFP4Linear(ffn, hidden, seed=seed + 1, grid=grid, device=device)
-        self.drop = Dropout(p, seed=given)
+        self.drop = Dropout(p, seed=given, offset=offset)
 
-    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                offset: Union[int, torch.Tensor, None] = None) -> torch.Tensor:
         if residual is None:
             y, h = self.norm(x), x
         else:
             y, h = self.norm(x, residual)
-        return self.drop(self.down(self.gated(y)), h)
+        return self.drop(self.down(self.gated(y)), h, offset)
 
 
 # ---------------------------------------------------------------------------
