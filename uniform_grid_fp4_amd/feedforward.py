@@ -332,6 +332,16 @@ class Int8Linear(torch.nn.Module):
         self.register_buffer("bias", None if bias is None else bias.detach().float().contiguous())
         self.in_features = w.k
 
+    def _apply(self, fn, *more):
+        """Moves go through; a cast of the model's floating-point numbers leaves the
+        scales and the bias, which are FP32 whatever the activations are."""
+        had = {n: t for n, t in self.named_buffers(recurse=False) if t.is_floating_point()}
+        super()._apply(fn, *more)
+        for n, t in had.items():
+            if self._buffers[n].dtype != t.dtype:
+                self._buffers[n] = t.to(self._buffers[n].device)
+        return self
+
     @torch.no_grad()
     def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
         if (offsets is None) != (self.n_experts == 1) or \
