@@ -25,11 +25,11 @@ __device__ __forceinline__ float sigmoid(float g) {
 
 // c = erfc(-g / sqrt 2) / 2.  For z = |g| / sqrt 2 in the form erfc(z) = t exp(P(t)
 // - z^2), t = 1 / (1 + z / 2) (Press et al., Numerical Recipes), P of degree 9 fitted
-// by least squares at Chebyshev nodes, within 6e-8 of log(erfc(z) exp(z^2) / t) over t
-// in [0.155, 1], where erfc is above the smallest number.  In FP32 erfc(z) is within 6
-// (1 + z^2) half steps; the rounding of the exponent is what grows.  The device
-// library's erfcf, with its branches, took the gated int8 product of 1387 x 180 to 2 x
-// 5568 from 20 to 49 us.
+// by least squares at Chebyshev nodes; with its coefficients in FP32, as they stand
+// here, it is within 1.01e-7 of log(erfc(z) exp(z^2) / t) over t in [0.155, 1], where
+// erfc is above the smallest number.  In FP32 erfc(z) is within 6 (1 + z^2) half steps;
+// the rounding of the exponent is what grows.  The device library's erfcf, with its
+// branches, took the gated int8 product of 1387 x 180 to 2 x 5568 from 20 to 49 us.
 __device__ __forceinline__ float normal_share(float g) {
   const float z = fabsf(g) * 0.70710678118654752f;
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.0f));
