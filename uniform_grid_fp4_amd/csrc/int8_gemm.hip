@@ -716,7 +716,12 @@ static hipError_t int8_gemm(const Int8GemmArgs &a, hipStream_t st) {
   // reads them in every workgroup, which pays while there are few (32 rows, 8192 to
   // 2048 columns: 13 us, tiles 22; 48 rows, 1024 to 2 x 2048: 5.0 and 6.0; 32 rows, 2048
   // to 2 x 8192: 10.1 and 10.1; 64 rows, 2048 to 2 x 4096: 8.6 and 8.1; 300 rows over 8
-  // experts, 2048 to 2 x 1024: 14.5 and 12.3).
+  // experts, 2048 to 2 x 1024: 14.5 and 12.3).  Where the rows of each group lie is known
+  // on the GPU only, so both this rule and that of the tiles take the groups to be even.
+  // An expert with more rows than that has its weights read again for every 16 of them, 3
+  // us each at this size (2048 to 2 x 2048; even, half the rows with one expert, all: 512
+  // rows over 32 experts 46, 72 and 100 us; 1024 over 64 113, 154 and 203; with tiles 1024
+  // over 32 45, 53 and 18; 4096 over 8 42, 67 and 41).
   if (rows <= 16) return launch_rows<1, ACT>(a, st);
   if (rows <= 32 && groups16 <= 512) return launch_rows<2, ACT>(a, st);
   if (rows <= 64 && groups16 <= 256) return launch_rows<4, ACT>(a, st);
