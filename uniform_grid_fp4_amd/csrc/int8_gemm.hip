@@ -132,8 +132,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void int8_rows_kernel(const Int8Gem
 // by itself: one launch instead of two, and no workspace.  The waves share out the
 // rows (or parts of one), their largest elements meet in LDS, the codes go to LDS,
 // and the products read them there.  The first loads of w are on their way
-// meanwhile.  1 x 2048 to 2 x 8192 columns, bf16: 10 us (34 MB, 3.4 TB/s; 7.6 us with the
-// weights in the caches): bound by latency, of the row, of two exchanges and of w.
+// meanwhile.  1 x 2048 to 2 x 8192 columns, bf16: 10 us (34 MB, 3.4 TB/s; 9 us with one
+// set of weights that stays in the caches): bound by latency, of the row, of two
+// exchanges and of w.
 // ---------------------------------------------------------------------------
 template <typename T, int ACT>
 __global__ __launch_bounds__(64 * kRowWaves) void int8_fused_kernel(const Int8GemmArgs a,

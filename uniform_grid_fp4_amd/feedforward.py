@@ -357,7 +357,8 @@ def _act_name(code: int) -> str:
 
 
 class Int8FeedForward(torch.nn.Module):
-    """What serves a trained UFP4FeedForward: its norm, and its products in int8."""
+    """What serves a trained UFP4FeedForward: its norm (the same module), and its
+    products in int8 (of the weights as they are now)."""
 
     def __init__(self, trained: UFP4FeedForward):
         super().__init__()
@@ -375,8 +376,8 @@ class Int8FeedForward(torch.nn.Module):
 
 
 class Int8MoEBlock(torch.nn.Module):
-    """What serves a trained gated `moe.UFP4MoEBlock`: its norm and router, and its
-    experts' products in int8."""
+    """What serves a trained gated `moe.UFP4MoEBlock`: its norm and router (the same
+    modules), and its experts' products in int8 (of the weights as they are now)."""
 
     def __init__(self, trained: "M.UFP4MoEBlock"):
         super().__init__()
