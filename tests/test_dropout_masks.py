@@ -148,3 +148,10 @@ def test_the_sublayer_hands_an_offset_on(seen, monkeypatch):
     x = torch.ones(2, 8)
     layer(x), layer(x, offset=8)
     assert seen == [(3, 4), (3, 8)]
+
+
+def test_the_state_lies_on_the_host_whatever_the_default_device():
+    drop = W.Dropout(0.5)
+    with torch.device("meta"):
+        state = drop.state_dict()
+    W.Dropout(0.5).load_state_dict(state)

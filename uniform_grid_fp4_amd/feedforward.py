@@ -159,7 +159,8 @@ class Dropout(torch.nn.Module):
 
     def get_extra_state(self) -> torch.Tensor:
         seed = self.seed & ((1 << 64) - 1)
-        return torch.tensor([seed - (seed >> 63 << 64), self.calls], dtype=torch.int64)
+        return torch.tensor([seed - (seed >> 63 << 64), self.calls], dtype=torch.int64,
+                            device="cpu")
 
     def set_extra_state(self, state: torch.Tensor) -> None:
         seed, self.calls = state.tolist()
