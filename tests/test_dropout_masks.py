@@ -155,3 +155,18 @@ def test_the_state_lies_on_the_host_whatever_the_default_device():
     with torch.device("meta"):
         state = drop.state_dict()
     W.Dropout(0.5).load_state_dict(state)
+
+
+def test_copies_follow_the_callers_offset(seen):
+    """The tensor is the caller's, who advances one; where it is a part of what is
+    copied, the copy has the copied one."""
+    step = torch.tensor([4])
+    layers = [W.UFP4FeedForward(8, 4, p=0.5, offset=step)]
+    layers.append(copy.deepcopy(layers[0]))
+    assert layers[1].drop.offset is step and layers[1].drop.seed != layers[0].drop.seed
+    model = torch.nn.Module()
+    model.register_buffer("step", step)
+    model.drop = layers[0].drop
+    there = copy.deepcopy(model)
+    assert there.step is not step and there.drop.offset is there.step
+    assert copy.deepcopy(W.Dropout(0.5)).offset is None

@@ -152,7 +152,10 @@ class Dropout(torch.nn.Module):
 
     def __deepcopy__(self, memo):
         new = memo[id(self)] = self.__class__.__new__(self.__class__)
-        new.__dict__.update(copy.deepcopy(self.__dict__, memo))
+        own = {k: v for k, v in self.__dict__.items() if k != "offset"}
+        new.__dict__.update(copy.deepcopy(own, memo))
+        # the caller's tensor, which a copy of it would not follow
+        new.offset = memo.get(id(self.offset), self.offset)
         if not getattr(new, "given", True):          # a pickle of before has none
             new.seed = _own_seed()
         return new
