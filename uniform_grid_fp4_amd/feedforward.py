@@ -148,7 +148,8 @@ class Dropout(torch.nn.Module):
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p = {p}: a probability")
         self.given = seed is not None
-        self.p, self.seed, self.calls, self.offset = p, seed if self.given else _own_seed(), 0, offset
+        self.seed = seed if self.given else _own_seed()
+        self.p, self.calls, self.offset = p, 0, offset
 
     def __deepcopy__(self, memo):
         new = memo[id(self)] = self.__class__.__new__(self.__class__)
@@ -156,7 +157,7 @@ class Dropout(torch.nn.Module):
         new.__dict__.update(copy.deepcopy(own, memo))
         # the caller's tensor, which a copy of it would not follow
         new.offset = memo.get(id(self.offset), self.offset)
-        if not getattr(new, "given", True):          # a pickle of before has none
+        if not getattr(new, "given", True):          # absent in older pickles
             new.seed = _own_seed()
         return new
 
